@@ -44,6 +44,9 @@ extern "C" {
 #define MLA_DV 512      /* value width: the first 512 codes of a row              */
 #define MLA_MAX_HEADS 16
 #define MLA_MAX_NQ 4    /* verify positions per sequence                          */
+#define MLA_ROPE 64     /* RoPE dims per row: the last 64 of its 576 codes        */
+#define MLA_MAX_TREE 64 /* drafted nodes per sequence (tree verify, acceptance)   */
+#define MLA_MAX_VOCAB (1 << 19) /* probabilities per row of mla_accept_drafts     */
 
 typedef enum {
   MLA_OK = 0,
@@ -55,7 +58,12 @@ typedef enum {
   MLA_ERR_BOUNDS = 6       /* device: page index outside the pool or length > table    */
 } mla_status_t;
 
-typedef enum { MLA_OP_DECODE = 0, MLA_OP_VERIFY = 1, MLA_OP_PREFILL = 2 } mla_op_t;
+typedef enum {
+  MLA_OP_DECODE = 0,
+  MLA_OP_VERIFY = 1,
+  MLA_OP_PREFILL = 2,
+  MLA_OP_VERIFY_TREE = 3
+} mla_op_t;
 
 /*
  * The paged latent cache.
@@ -88,7 +96,8 @@ typedef struct mla_kv {
  * depends on H, n_q and the SM count, not on B); it must be 256-byte aligned and stay untouched until the call's
  * work has finished on its stream. Its contents need no initialisation: every call
  * rewrites all it later reads (zero-fill it once if mla_read_status may run before the
- * first call). For MLA_OP_PREFILL pass B = 1 and n_q = T. Returns 0 for unsupported
+ * first call). For MLA_OP_PREFILL pass B = 1 and n_q = T, for MLA_OP_VERIFY_TREE n_q = the
+ * nodes per sequence. Returns 0 for unsupported
  * arguments.
  */
 size_t mla_workspace_size(mla_op_t op, int B, int H, int n_q, int device);
@@ -242,6 +251,144 @@ mla_status_t mla_merge_lse(const float* part_out, const float* part_lse, int S, 
 mla_status_t mla_cache_append(uint8_t* pool, int64_t num_pages, int32_t page_size,
                               const void* x, const int64_t* slots, int64_t n, float kv_scale,
                               unsigned* status, void* stream);
+
+/*
+ * Rotary positions of the 64 RoPE dims. Pair i (of 32) at position m turns by the angle
+ * m * f_i and is scaled by `amplitude`:
+ *     (a, b) -> amplitude * (a cos - b sin, a sin + b cos).
+ * interleaved != 0: pair i is dims (2i, 2i + 1); otherwise (half layout) dims (i, i + 32).
+ * turns[i] is f_i / (2 pi), the turns a position adds, in units of 2^-64: the phase of any
+ * position is the integer product m * turns[i] modulo 2^64, so it loses nothing at far
+ * positions (a float32 product is off by 0.06 rad at position 10^6). Filled by
+ * mla_rope_init; read on the host when a call is made (a captured graph keeps the values).
+ */
+typedef struct mla_rope {
+  uint64_t turns[MLA_ROPE / 2];
+  float amplitude;
+  int32_t interleaved;
+} mla_rope_t;
+
+/*
+ * Fill a mla_rope_t (host only). f_i = base^(-2i/64), for a context stretched `factor` times:
+ * factor = 1 leaves them; original_positions = 0 divides every f_i by factor (linear position
+ * interpolation); original_positions > 0 is YaRN: pairs that turn more than beta_fast times over
+ * the original positions keep f_i, those that turn less than beta_slow times get f_i / factor,
+ * with a linear ramp between the two pair indices (rounded outwards to whole ones). amplitude is
+ * the model's attention factor for that stretch (1 where it is folded into sm_scale).
+ * MLA_ERR_INVALID_ARG: base <= 1, factor <= 0, original_positions < 0, not
+ * beta_fast > beta_slow > 0 (YaRN), or anything not finite.
+ */
+mla_status_t mla_rope_init(mla_rope_t* rope, double base, double factor, int original_positions,
+                           double beta_fast, double beta_slow, float amplitude, int interleaved);
+
+/*
+ * Rotate the RoPE part of n tokens' heads, for queries that mla_decode, mla_verify,
+ * mla_verify_tree, mla_prefill (dims 512..575 of 576) or mla_prefill_mha (dims 128..191 of
+ * 192) read next. Each bfloat16 output is the float32 result rounded once.
+ *   x, out     device, the first RoPE element of token 0, head 0 (16-byte aligned); token t,
+ *              head h starts t * *_token_stride + h * *_head_stride elements further (strides
+ *              are multiples of 8). out may be x with the same strides (in place); otherwise
+ *              the two must not overlap.
+ *   positions  device, [n] int64 (any sign)
+ */
+mla_status_t mla_rope(const mla_rope_t* rope, const void* x, int64_t x_token_stride,
+                      int64_t x_head_stride, const int64_t* positions, int64_t n, int H, void* out,
+                      int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/*
+ * mla_cache_append for rows as the latent projection leaves them: row i is (c, r), c the 512
+ * latent entries before their norm and r the 64 RoPE entries before their rotation. Cache row
+ * slots[i] becomes the e4m3 codes of y * (1 / kv_scale), where
+ *     y = c * rsqrt(mean(c^2) + eps) * norm_weight      (c itself if norm_weight is NULL)
+ * and, for the RoPE part, r rotated to positions[i] (r itself if rope is NULL). All of it
+ * stays in float32; the codes are the only rounding (nearest even, saturating, NaN kept).
+ *   pool, slots, n, kv_scale, status  as mla_cache_append
+ *   x            device, rows of 576 bfloat16 x_stride elements apart (>= 576, a multiple of
+ *                8), 16-byte aligned: a slice of a wider projection's rows will do
+ *   norm_weight  device, [512] bfloat16, 16-byte aligned, or NULL
+ *   eps          added to the mean square (>= 0, finite)
+ *   rope, positions  both given, or both NULL; positions: device, [n] int64
+ * Two rows with the same slot leave a mixture of both in that cache row.
+ */
+mla_status_t mla_cache_append_rope(uint8_t* pool, int64_t num_pages, int32_t page_size,
+                                   const void* x, int64_t x_stride, const int64_t* slots, int64_t n,
+                                   float kv_scale, const void* norm_weight, float eps,
+                                   const mla_rope_t* rope, const int64_t* positions,
+                                   unsigned* status, void* stream);
+
+/*
+ * Read cached rows back: positions starts[b], starts[b] + 1, ... of sequence b, dequantised
+ * as e4m3(code) * kv_scale (one float32 product, then rounded to the output's type), one
+ * after the other in out. Sequence b fills rows cu_rows[b] .. cu_rows[b + 1] - 1, so it reads
+ * cu_rows[b + 1] - cu_rows[b] positions.
+ *   kv       the cache; seq_lens bounds the positions
+ *   starts   device, [B] int32 first position of each sequence, or NULL for 0
+ *   cu_rows  device, [B + 1] int64, non-decreasing (its last entry: the rows filled)
+ *   n        rows of out; rows outside cu_rows[0] .. cu_rows[B] - 1 stay as they were
+ *   out      device, [n][576] bfloat16 (out_is_f32 = 0) or float32, 16-byte aligned
+ *   status   device word or NULL: set to MLA_ERR_BOUNDS (if it held 0) when a position lies
+ *            outside its sequence or its page outside the pool; that output row is zeros
+ */
+mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
+                              const int64_t* cu_rows, int64_t n, void* out, int out_is_f32,
+                              unsigned* status, void* stream);
+
+/*
+ * mla_verify for a tree of drafted tokens: n nodes per sequence (1..64), their rows the last n
+ * of the sequence's seq_lens[b] cached positions, node j's key at position
+ * seq_lens[b] - n + j. Every node sees the whole prefix (the positions before the nodes) and
+ * the nodes i whose bit i is set in tree_mask[b][j]: for a draft tree its ancestors and
+ * itself. Any mask is allowed (a prefix mask, separate documents, nothing at all); bits at or
+ * above n are ignored. A node that sees no key gives out = 0, lse = -inf. With fewer than n
+ * cached positions the missing ones are the first nodes' keys.
+ *   q          device, [B][n][H][576] bfloat16, 16-byte aligned
+ *   tree_mask  device, [B][n] uint64, 8-byte aligned
+ *   out        device, [B][n][H][512] bfloat16
+ *   lse        device, [B][n][H] float32, or NULL
+ *   workspace  mla_workspace_size(MLA_OP_VERIFY_TREE, B, H, n, device) bytes
+ * Numerics, errors and the split of long sequences as mla_verify. More than 48 rows (n * H)
+ * run as groups of whole nodes, each of which reads the sequence's keys.
+ */
+mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, int H, float sm_scale,
+                             const uint64_t* tree_mask, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Accept drafted tokens against the target's probabilities with given random numbers, and
+ * draw the token after them: the emitted tokens are distributed as the target's own.
+ * A sequence's n nodes are the positions of its verify call: node 0 is the last token already
+ * emitted, node j >= 1 a draft tokens[b][j] that follows node parents[b][j] < j (parents =
+ * NULL: node j - 1, a chain). target[b][j] holds the probabilities of the token after node j.
+ * From node 0 on, at node a with u = uniforms[b][a]:
+ *   draft = NULL  the children lie side by side on [0, 1) in the order of their indices, each
+ *         as wide as target[b][a] gives its token (a repeated token: nothing); the child whose
+ *         share holds u is accepted. At the last node accepted, the next token is drawn from
+ *         target[b][a] without its children's tokens.
+ *   draft given (chains only)  draft[b][j - 1] holds the probabilities that tokens[b][j] was
+ *         drawn from; node j = a + 1 is accepted if u * draft[token] < target[token] (float32).
+ *         At the first refusal the next token is drawn from max(target - draft, 0).
+ * The draw inverts the cumulative sum with uniforms[b][n]: the first token whose cumulative
+ * weight exceeds u * total. A row left without weight is drawn from the whole target row; if
+ * that holds none either, the token is -1. Weights are rounded to multiples of 2^-43 (a
+ * float32 probability above 2^-19 is one already) and shares and sums are whole numbers, so
+ * results do not depend on the order of summation. Weights outside [0, 1] count as the nearer
+ * end, NaN as 0; so do the uniforms (1 counts as the number just below it).
+ * A token outside [0, V) or a parent outside [0, j) makes node j no draft (padding): it and
+ * what hangs below it are never accepted, and it takes nothing from the draw.
+ *   target        device, [B][n][V] float32
+ *   tokens        device, [B][n] int32 (node 0's is not read)
+ *   parents       device, [B][n] int32 or NULL (node 0's is not read)
+ *   draft         device, [B][n - 1][V] float32 or NULL; with parents: MLA_ERR_UNSUPPORTED
+ *   uniforms      device, [B][n + 1] float32 in [0, 1)
+ *   out_tokens    device, [B][n] int32: the accepted tokens, the drawn one, then -1
+ *   path          device, [B][n] int32: the nodes kept (0 first), then -1: the cache rows to keep
+ *   num_accepted  device, [B] int32: drafts accepted (0 .. n - 1)
+ * n in 1..64, V in 1..MLA_MAX_VOCAB; the emitted tokens are num_accepted + 1.
+ */
+mla_status_t mla_accept_drafts(const float* target, const int32_t* tokens, const int32_t* parents,
+                               const float* draft, const float* uniforms, int B, int n, int V,
+                               int32_t* out_tokens, int32_t* path, int32_t* num_accepted,
+                               void* stream);
 
 /*
  * Top-k renormalisation of probability rows, the sampling step of speculative-verify

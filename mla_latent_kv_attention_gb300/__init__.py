@@ -21,7 +21,10 @@ LIB_PATH = os.path.join(_PKG, "libmla.so")
 
 MLA_D = 576
 MLA_DV = 512
-MLA_OP_DECODE, MLA_OP_VERIFY, MLA_OP_PREFILL = 0, 1, 2
+MLA_ROPE = 64
+MLA_MAX_TREE = 64
+MLA_MAX_VOCAB = 1 << 19
+MLA_OP_DECODE, MLA_OP_VERIFY, MLA_OP_PREFILL, MLA_OP_VERIFY_TREE = 0, 1, 2, 3
 (MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_WORKSPACE, MLA_ERR_CUDA,
  MLA_ERR_TIMEOUT, MLA_ERR_BOUNDS) = range(7)
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_WORKSPACE",
@@ -34,7 +37,8 @@ EXPORTS = ("mla_workspace_size", "mla_decode", "mla_verify", "mla_prefill", "mla
            "mla_top_k_renorm_prob", "mla_verify_f32", "mla_prefill_mha",
            "mla_prefill_mha_workspace_size", "mla_test_stall_next_call",
            "mla_read_status_static", "mla_set_trace_buffer", "mla_verify_f32_shard",
-           "mla_prefill_mha_bf16")
+           "mla_prefill_mha_bf16", "mla_rope_init", "mla_rope", "mla_cache_append_rope",
+           "mla_cache_gather", "mla_verify_tree", "mla_accept_drafts")
 
 
 class MlaError(RuntimeError):
@@ -49,6 +53,12 @@ class mla_kv_t(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("page_table", ctypes.c_void_p),
                 ("page_table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
                 ("kv_scale", ctypes.c_float)]
+
+
+class mla_rope_t(ctypes.Structure):
+    """Rotary frequencies as mla_rope_init fills them (see include/mla.h)."""
+    _fields_ = [("turns", ctypes.c_uint64 * (MLA_ROPE // 2)), ("amplitude", ctypes.c_float),
+                ("interleaved", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -93,6 +103,17 @@ def _load() -> ctypes.CDLL:
     lib.mla_cache_append.restype = i32
     lib.mla_top_k_renorm_prob.argtypes = [P, P, i32, i32, P, i32, P]
     lib.mla_top_k_renorm_prob.restype = i32
+    ROPE = ctypes.POINTER(mla_rope_t)
+    f64 = ctypes.c_double
+    lib.mla_rope_init.argtypes = [ROPE, f64, f64, i32, f64, f64, f32, i32]
+    lib.mla_rope.argtypes = [ROPE, P, i64, i64, P, i64, i32, P, i64, i64, P]
+    lib.mla_cache_append_rope.argtypes = [P, i64, i32, P, i64, P, i64, f32, P, f32, ROPE, P, P, P]
+    lib.mla_cache_gather.argtypes = [KV, i32, P, P, i64, P, i32, P, P]
+    lib.mla_verify_tree.argtypes = [KV, P, i32, i32, i32, f32, P, P, P, P, sz, P]
+    lib.mla_accept_drafts.argtypes = [P, P, P, P, P, i32, i32, i32, P, P, P, P]
+    for name in ("mla_rope_init", "mla_rope", "mla_cache_append_rope", "mla_cache_gather",
+                 "mla_verify_tree", "mla_accept_drafts"):
+        getattr(lib, name).restype = i32
     for name in ("mla_decode", "mla_verify", "mla_prefill", "mla_merge_lse", "mla_read_status",
                  "mla_last_launch_count"):
         getattr(lib, name).restype = i32
@@ -320,6 +341,164 @@ def mla_top_k_renorm_prob(probs: torch.Tensor, top_k, out: Optional[torch.Tensor
     _check("mla_top_k_renorm_prob", library().mla_top_k_renorm_prob(
         probs.data_ptr(), out.data_ptr(), B, V, kp, k, _stream(stream)))
     return out
+
+
+def _on(dev: torch.device, stream) -> int:
+    """The raw stream for a call on tensors of device `dev` (which has to be the current one:
+    the library launches on the current device)."""
+    if stream is not None:
+        return _stream(stream)
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but cuda:{torch.cuda.current_device()} is the current "
+                         "device (use torch.cuda.device)")
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> int:
+    """Pointer of a contiguous tensor of the given type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _status_ptr(status: Optional[torch.Tensor], dev: torch.device) -> Optional[int]:
+    return None if status is None else _dense(status, "status", torch.int32, (1,), dev)
+
+
+def mla_rope_init(base: float = 10000.0, factor: float = 1.0, original_positions: int = 0,
+                  beta_fast: float = 32.0, beta_slow: float = 1.0, amplitude: float = 1.0,
+                  interleaved: bool = True) -> mla_rope_t:
+    """Rotary frequencies f_i = base^(-2i/64) of the 64 RoPE dims, for a context stretched
+    `factor` times: linearly (original_positions = 0) or by YaRN. Kept by the caller and
+    handed to mla_rope and mla_cache_append_rope."""
+    rope = mla_rope_t()
+    _check("mla_rope_init", library().mla_rope_init(ctypes.byref(rope), base, factor, original_positions,
+                                               beta_fast, beta_slow, amplitude, int(interleaved)))
+    return rope
+
+
+def _rope_part(t: torch.Tensor, name: str, shape) -> None:
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape != shape or not t.is_cuda or \
+            t.stride(2) != 1:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor [n, H, 64] (any token and head "
+                         "strides, the 64 RoPE dims contiguous)")
+
+
+def mla_rope(rope: mla_rope_t, x: torch.Tensor, positions: torch.Tensor, out=None,
+             stream=None) -> torch.Tensor:
+    """Rotate x [n, H, 64] bf16 (a view of the RoPE dims, e.g. q[..., 512:] or q_mha[..., 128:])
+    to positions int64 [n]. `out` may be another such view, or x itself (in place)."""
+    _rope_part(x, "x", (*x.shape[:2], MLA_ROPE))
+    n, H = x.shape[0], x.shape[1]
+    dev = x.device
+    if out is None:
+        out = torch.empty(n, H, MLA_ROPE, dtype=torch.bfloat16, device=dev)
+    else:
+        _rope_part(out, "out", x.shape)
+        if out.device != dev or (n > 1 and out.stride(0) == 0) or (H > 1 and out.stride(1) == 0):
+            raise ValueError("out must be on x's device, every element a place of its own")
+    _check("mla_rope", library().mla_rope(
+        ctypes.byref(rope), x.data_ptr(), x.stride(0), x.stride(1),
+        _dense(positions, "positions", torch.int64, (n,), dev), n, H, out.data_ptr(), out.stride(0),
+        out.stride(1), _on(dev, stream)))
+    return out
+
+
+def mla_cache_append_rope(pool: torch.Tensor, x: torch.Tensor, slots: torch.Tensor, kv_scale: float,
+                          rope: Optional[mla_rope_t] = None, positions: Optional[torch.Tensor] = None,
+                          norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """mla_cache_append for rows x [n, 576] bf16 as the latent projection leaves them: the
+    latent is normalised by its root mean square and weighted with norm_weight [512] bf16
+    (None: as it is), the 64 RoPE dims are turned to positions int64 [n] (rope None: as they
+    are), and both are quantised in one pass. x may be a slice of a wider projection's rows."""
+    if pool.dtype is not torch.uint8 or pool.dim() != 3 or pool.shape[2] != MLA_D or \
+            not pool.is_contiguous() or not pool.is_cuda:
+        raise ValueError("pool must be a contiguous uint8 CUDA tensor [num_pages, page_size, 576]")
+    dev = pool.device
+    if x.dtype is not torch.bfloat16 or x.dim() != 2 or x.shape[1] != MLA_D or x.stride(1) != 1 or \
+            x.device != dev:
+        raise ValueError("x must be a bfloat16 tensor [n, 576] on the pool's device, its rows contiguous")
+    if (rope is None) != (positions is None):
+        raise ValueError("give rope and positions together, or neither")
+    n = x.shape[0]
+    _check("mla_cache_append_rope", library().mla_cache_append_rope(
+        pool.data_ptr(), pool.shape[0], pool.shape[1], x.data_ptr(), x.stride(0) if n > 1 else MLA_D,
+        _dense(slots, "slots", torch.int64, (n,), dev), n, kv_scale,
+        None if norm_weight is None else _dense(norm_weight, "norm_weight", torch.bfloat16, (MLA_DV,), dev),
+        eps, None if rope is None else ctypes.byref(rope),
+        None if positions is None else _dense(positions, "positions", torch.int64, (n,), dev),
+        _status_ptr(status, dev), _on(dev, stream)))
+
+
+def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optional[torch.Tensor] = None,
+                     out=None, dtype: torch.dtype = torch.bfloat16,
+                     status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Cached rows read back and dequantised: rows cu_rows[b] .. cu_rows[b + 1] - 1 of out
+    [n, 576] (bf16 or float32) are positions starts[b], starts[b] + 1, ... of sequence b.
+    cu_rows int64 [B + 1], starts int32 [B] (None: 0); rows outside them stay as they were."""
+    c = kv.c_struct()
+    dev = kv.pool.device
+    B = cu_rows.shape[0] - 1
+    if B < 0 or B > kv.seq_lens.shape[0] or B > kv.page_table.shape[0]:
+        raise ValueError("cu_rows must have an entry more than there are sequences")
+    if out is None:
+        out = torch.empty(n, MLA_D, dtype=dtype, device=dev)
+    if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+        raise ValueError("out must be bfloat16 or float32")
+    _check("mla_cache_gather", library().mla_cache_gather(
+        ctypes.byref(c), B, None if starts is None else _dense(starts, "starts", torch.int32, (B,), dev),
+        _dense(cu_rows, "cu_rows", torch.int64, (B + 1,), dev), n,
+        _dense(out, "out", out.dtype, (n, MLA_D), dev), out.dtype is torch.float32,
+        _status_ptr(status, dev), _on(dev, stream)))
+    return out
+
+
+def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_scale: float, out=None,
+                    lse=None, ws=None, stream=None):
+    """q [B, n, H, 576] bf16 of a tree's n <= 64 nodes -> (out [B, n, H, 512] bf16, lse [B, n, H]
+    fp32). Every node sees the prefix and the nodes whose bit its tree_mask (int64 [B, n]) sets."""
+    _q_check(q, 4)
+    B, n, H = q.shape[0], q.shape[1], q.shape[2]
+    dev = q.device
+    out = torch.empty(B, n, H, MLA_DV, dtype=torch.bfloat16, device=dev) if out is None else out
+    lse = torch.empty(B, n, H, dtype=torch.float32, device=dev) if lse is None else lse
+    ws = workspace(MLA_OP_VERIFY_TREE, B, H, n, dev) if ws is None else ws
+    if kv.seq_lens.shape[0] < B or kv.page_table.shape[0] < B or kv.pool.device != dev:
+        raise ValueError("kv must describe q's sequences, on q's device")
+    c = kv.c_struct()
+    _check("mla_verify_tree", library().mla_verify_tree(
+        ctypes.byref(c), q.data_ptr(), B, n, H, sm_scale,
+        _dense(tree_mask, "tree_mask", torch.int64, (B, n), dev),
+        _dense(out, "out", torch.bfloat16, (B, n, H, MLA_DV), dev),
+        _dense(lse, "lse", torch.float32, (B, n, H), dev), ws.data_ptr(), ws.numel(), _on(dev, stream)))
+    return out, lse
+
+
+def mla_accept_drafts(target_probs: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Tensor,
+                      parents: Optional[torch.Tensor] = None,
+                      draft_probs: Optional[torch.Tensor] = None, stream=None):
+    """Accept drafted tokens against target_probs [B, n, V] float32 (row j: the token after node
+    j) and draw the token after them. tokens int32 [B, n] (node 0 is the last token emitted),
+    uniforms float32 [B, n + 1] in [0, 1), parents int32 [B, n] (None: a chain), draft_probs
+    float32 [B, n - 1, V] (chains: what tokens[:, 1:] were drawn from). Returns int32 tensors
+    (out_tokens [B, n], path [B, n], num_accepted [B]); unused places hold -1."""
+    if target_probs.dim() != 3 or not target_probs.is_cuda:
+        raise ValueError("target_probs must be a CUDA tensor [B, n, V]")
+    B, n, V = target_probs.shape
+    dev = target_probs.device
+    out_tokens = torch.empty(B, n, dtype=torch.int32, device=dev)
+    path = torch.empty(B, n, dtype=torch.int32, device=dev)
+    num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+    _check("mla_accept_drafts", library().mla_accept_drafts(
+        _dense(target_probs, "target_probs", torch.float32, (B, n, V), dev),
+        _dense(tokens, "tokens", torch.int32, (B, n), dev),
+        None if parents is None else _dense(parents, "parents", torch.int32, (B, n), dev),
+        None if draft_probs is None else _dense(draft_probs, "draft_probs", torch.float32, (B, n - 1, V), dev),
+        _dense(uniforms, "uniforms", torch.float32, (B, n + 1), dev), B, n, V, out_tokens.data_ptr(),
+        path.data_ptr(), num_accepted.data_ptr(), _on(dev, stream)))
+    return out_tokens, path, num_accepted
 
 
 def mla_read_status(ws: torch.Tensor, stream=None) -> int:

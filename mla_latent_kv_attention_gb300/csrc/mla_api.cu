@@ -135,6 +135,11 @@ size_t mla_workspace_size(mla_op_t op, int B, int H, int n_q, int device) {
     const int sms = sm_count(device);
     return sms > 0 ? mla::ws_prefill_bytes(sms) : 0;
   }
+  if (op == MLA_OP_VERIFY_TREE) {
+    if (n_q < 1 || n_q > MLA_MAX_TREE) return 0;
+    const int sms = sm_count(device);
+    return sms > 0 ? mla::ws_layout(B, mla::tree_groups(n_q, H).nodes * H, sms).total : 0;
+  }
   if (op == MLA_OP_DECODE) n_q = 1;
   if (n_q < 1 || n_q > MLA_MAX_NQ) return 0;
   const int sms = sm_count(device);
@@ -167,6 +172,58 @@ mla_status_t mla_verify_f32_shard(const mla_kv_t* kv, const void* q, int B, int 
   const int shift = (n_q >= 1 && visible_shift > n_q - 1) ? n_q - 1 : visible_shift;
   return run_split(kv, q, B, n_q, H, sm_scale, out, lse, workspace, workspace_bytes, stream, true,
                    shift);
+}
+
+mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, int H, float sm_scale,
+                             const uint64_t* tree_mask, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  g_last_launches = 0;
+  mla_status_t st = check_kv(kv);
+  if (st != MLA_OK) return st;
+  if (B < 0) return MLA_ERR_INVALID_ARG;
+  if (H < 1 || H > MLA_MAX_HEADS || n < 1 || n > MLA_MAX_TREE) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)B * n * H > 0x7fffffff) return MLA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
+  if (B > 0 && (!q || !out || !tree_mask)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(tree_mask, 8))
+    return MLA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
+  int dev;
+  if ((st = current_device(&dev)) != MLA_OK) return st;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return MLA_ERR_CUDA;
+  const mla::TreeGroups g = mla::tree_groups(n, H);
+  const mla::WsLayout w = mla::ws_layout(B, g.nodes * H, sms);
+  if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE;
+  if (B == 0) return MLA_OK;
+  mla::AttnParams p = base_params(kv, q, B, n, H, sm_scale, out, lse);
+  p.B = B * g.groups;
+  p.R = p.part_rows = g.nodes * H;
+  p.groups = g.groups;
+  p.group_nodes = g.nodes;
+  p.tree_mask = tree_mask;
+  p.trace = nullptr;  // the profiling hook traces decode, verify and prefill
+  char* base = static_cast<char*>(workspace);
+  p.hdr = reinterpret_cast<mla::WsHeader*>(base + w.hdr);
+  p.status = reinterpret_cast<unsigned*>(base + w.status);
+  p.part_lse = reinterpret_cast<float*>(base + w.part_lse);
+  p.part_out = reinterpret_cast<float*>(base + w.part_out);
+  p.qimg = reinterpret_cast<uint8_t*>(base + w.qimg);
+  p.qimg_stride = (int64_t)w.qimg_stride;
+  p.num_ctas = sms;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prof_mark(g_prof_start, s);
+  const cudaError_t e = mla::launch_tree_tc(p, s, &g_last_launches);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  prof_mark(g_prof_stop, s);
+  if (mla::launch_merge_tree(p, B, s) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  ++g_last_launches;
+  return MLA_OK;
 }
 
 size_t mla_prefill_mha_workspace_size(int L, int H, int device) {
@@ -332,6 +389,133 @@ mla_status_t mla_cache_append(uint8_t* pool, int64_t num_pages, int32_t page_siz
   if (mla::launch_cache_append(pool, num_pages * (int64_t)page_size, static_cast<const uint16_t*>(x),
                                slots, n, inv, status, sms, static_cast<cudaStream_t>(stream)) !=
       cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  ++g_last_launches;
+  return MLA_OK;
+}
+
+mla_status_t mla_rope(const mla_rope_t* rope, const void* x, int64_t x_token_stride,
+                      int64_t x_head_stride, const int64_t* positions, int64_t n, int H, void* out,
+                      int64_t out_token_stride, int64_t out_head_stride, void* stream) {
+  g_last_launches = 0;
+  if (!rope || n < 0 || H < 0) return MLA_ERR_INVALID_ARG;
+  if (n == 0 || H == 0) return MLA_OK;
+  if (!x || !out || !positions) return MLA_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(positions, 8)) return MLA_ERR_INVALID_ARG;
+  if (((x_token_stride | x_head_stride | out_token_stride | out_head_stride) & 7) != 0)
+    return MLA_ERR_INVALID_ARG;
+  if (n > (int64_t)1 << 40 || n * H > (int64_t)1 << 34) return MLA_ERR_UNSUPPORTED;  // one grid
+  int dev;
+  mla_status_t st = current_device(&dev);
+  if (st != MLA_OK) return st;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return MLA_ERR_CUDA;
+  if (mla::launch_rope(*rope, static_cast<const uint16_t*>(x), x_token_stride, x_head_stride,
+                       positions, n, H, static_cast<uint16_t*>(out), out_token_stride,
+                       out_head_stride, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  ++g_last_launches;
+  return MLA_OK;
+}
+
+mla_status_t mla_cache_append_rope(uint8_t* pool, int64_t num_pages, int32_t page_size,
+                                   const void* x, int64_t x_stride, const int64_t* slots, int64_t n,
+                                   float kv_scale, const void* norm_weight, float eps,
+                                   const mla_rope_t* rope, const int64_t* positions,
+                                   unsigned* status, void* stream) {
+  g_last_launches = 0;
+  if (n < 0 || num_pages < 0 || page_size <= 0) return MLA_ERR_INVALID_ARG;
+  if (!(kv_scale > 0.f) || !(kv_scale < INFINITY)) return MLA_ERR_INVALID_ARG;
+  if (norm_weight && (!(eps >= 0.f) || !(eps < INFINITY))) return MLA_ERR_INVALID_ARG;
+  if ((rope == nullptr) != (positions == nullptr) && n > 0) return MLA_ERR_INVALID_ARG;
+  if (x_stride < MLA_D || x_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (n == 0) return MLA_OK;
+  if (!pool || !x || !slots) return MLA_ERR_INVALID_ARG;
+  if (!aligned(pool, 16) || !aligned(x, 16) || !aligned(slots, 8) || !aligned(norm_weight, 16) ||
+      !aligned(positions, 8) || !aligned(status, 4))
+    return MLA_ERR_INVALID_ARG;
+  int dev;
+  mla_status_t st = current_device(&dev);
+  if (st != MLA_OK) return st;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return MLA_ERR_CUDA;
+  mla::AppendRopeArgs a;
+  a.pool = pool;
+  a.pool_rows = num_pages * (int64_t)page_size;
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_stride = x_stride;
+  a.slots = slots;
+  a.n = n;
+  a.inv = 1.0f / kv_scale;  // binary32, as the definition states
+  a.weight = static_cast<const uint16_t*>(norm_weight);
+  a.eps = eps;
+  a.positions = positions;
+  a.status = status;
+  mla_rope_t none = {};
+  none.interleaved = 1;
+  if (mla::launch_cache_append_rope(a, rope ? *rope : none, sms, static_cast<cudaStream_t>(stream)) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  ++g_last_launches;
+  return MLA_OK;
+}
+
+mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
+                              const int64_t* cu_rows, int64_t n, void* out, int out_is_f32,
+                              unsigned* status, void* stream) {
+  g_last_launches = 0;
+  const mla_status_t st = check_kv(kv);
+  if (st != MLA_OK) return st;
+  if (B < 0 || n < 0) return MLA_ERR_INVALID_ARG;
+  if (n == 0 || B == 0) return MLA_OK;
+  if (!cu_rows || !out) return MLA_ERR_INVALID_ARG;
+  if (!aligned(starts, 4) || !aligned(cu_rows, 8) || !aligned(out, 16) || !aligned(status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (n > (int64_t)1 << 36) return MLA_ERR_UNSUPPORTED;  // one grid
+  if (mla::launch_cache_gather(*kv, B, starts, cu_rows, n, out, out_is_f32 != 0, status,
+                               static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  ++g_last_launches;
+  return MLA_OK;
+}
+
+mla_status_t mla_accept_drafts(const float* target, const int32_t* tokens, const int32_t* parents,
+                               const float* draft, const float* uniforms, int B, int n, int V,
+                               int32_t* out_tokens, int32_t* path, int32_t* num_accepted,
+                               void* stream) {
+  g_last_launches = 0;
+  if (B < 0) return MLA_ERR_INVALID_ARG;
+  if (n < 1 || n > MLA_MAX_TREE || V < 1 || V > MLA_MAX_VOCAB) return MLA_ERR_UNSUPPORTED;
+  if (parents && draft) return MLA_ERR_UNSUPPORTED;
+  if (B == 0) return MLA_OK;
+  if (B > 65535) return MLA_ERR_UNSUPPORTED;  // one grid row a sequence
+  if (!target || !tokens || !uniforms || !out_tokens || !path || !num_accepted)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(target, 4) || !aligned(tokens, 4) || !aligned(parents, 4) || !aligned(draft, 4) ||
+      !aligned(uniforms, 4) || !aligned(out_tokens, 4) || !aligned(path, 4) ||
+      !aligned(num_accepted, 4))
+    return MLA_ERR_INVALID_ARG;
+  mla::AcceptArgs a;
+  a.target = target;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.draft = n > 1 ? draft : nullptr;  // no drafts, no rows of theirs
+  a.uniforms = uniforms;
+  a.B = B;
+  a.n = n;
+  a.V = V;
+  a.out_tokens = out_tokens;
+  a.path = path;
+  a.num_accepted = num_accepted;
+  if (mla::launch_accept(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;
   }

@@ -229,8 +229,33 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int64_t idx, floa
 
 // PF: 0 decode/verify (the split plan's units); 1 prefill (units are blocks of new
 // positions, one a round per CTA); 2 prefill, the two halves along the keys of each unit of
-// an incomplete last round (one half a CTA, a partial for the merge). A compile-time
-// parameter: each kernel carries only its own paths.
+// an incomplete last round (one half a CTA, a partial for the merge); 3 tree verify (the split
+// plan over groups of a sequence's nodes). A compile-time parameter: each kernel carries only
+// its own paths.
+__host__ __device__ constexpr bool is_prefill(int pf) { return pf == 1 || pf == 2; }
+
+// Tree verify: what the plan calls a sequence is a group of p.group_nodes nodes of one, group
+// b % groups of sequence b / groups. The sequence an index of the plan's stands for, its first
+// row of q, out and lse, and its rows (the last group may hold fewer nodes).
+template <int PF>
+__device__ __forceinline__ int seq_of(const AttnParams& p, int b) {
+  return PF == 3 ? b / p.groups : b;
+}
+template <int PF>
+__device__ __forceinline__ int row0_of(const AttnParams& p, int b) {
+  if constexpr (PF == 3)
+    return (b / p.groups * p.n_q + b % p.groups * p.group_nodes) * p.H;
+  else
+    return b * p.R;
+}
+template <int PF>
+__device__ __forceinline__ int rows_of(const DecodeArgs& a, int b) {
+  if constexpr (PF == 3)
+    return min(a.p.group_nodes, a.p.n_q - b % a.p.groups * a.p.group_nodes) * a.p.H;
+  else
+    return a.rows;
+}
+
 template <int PF>
 __device__ __forceinline__ Cursor first_unit(const DecodeArgs& a, const Misc* ms) {
   Cursor c;
@@ -243,21 +268,21 @@ __device__ __forceinline__ Cursor first_unit(const DecodeArgs& a, const Misc* ms
 
 template <int PF>
 __device__ __forceinline__ bool has_unit(const DecodeArgs& a, const Misc* ms, const Cursor& c) {
-  return PF ? c.u < a.unit_end : (c.b < a.p.B && c.pre < ms->plan_x1);
+  return is_prefill(PF) ? c.u < a.unit_end : (c.b < a.p.B && c.pre < ms->plan_x1);
 }
 
 // The next unit: the next sequence with at least one key (decode/verify), or the next
 // unit index this CTA owns (prefill).
 template <int PF>
 __device__ __forceinline__ Cursor next_unit(const DecodeArgs& a, Cursor c) {
-  if (PF) {
+  if (is_prefill(PF)) {
     c.u += gridDim.x;
     return c;
   }
   c.pre += blocks_of(c.L);
   do {
     ++c.b;
-    c.L = (c.b < a.p.B) ? seq_len_of(a.p, c.b) : 0;
+    c.L = (c.b < a.p.B) ? seq_len_of(a.p, seq_of<PF>(a.p, c.b)) : 0;
   } while (c.b < a.p.B && c.L == 0);
   c.pre += kUnitCost;  // the next sequence's fixed cost precedes its blocks
   return c;
@@ -267,16 +292,16 @@ template <int PF>
 __device__ __forceinline__ UnitInfo unit_info(const DecodeArgs& a, const Misc* ms, const Cursor& c) {
   const AttnParams& p = a.p;
   UnitInfo x;
-  if (!PF) {
+  if (!is_prefill(PF)) {
     const long long nb = blocks_of(c.L);
     const long long blo = max(ms->plan_x0, c.pre), bhi = min(ms->plan_x1, c.pre + nb);
-    x.b = c.b;
+    x.b = seq_of<PF>(p, c.b);
     x.L = c.L;
     x.key_lo = (int)(blo - c.pre) * kKeyBlock;
     x.key_hi = (bhi > blo) ? min(c.L, (int)(bhi - c.pre) * kKeyBlock) : x.key_lo;
-    x.qrow0 = c.b * p.R;
-    x.j0 = 0;
-    x.rows = a.rows;
+    x.qrow0 = row0_of<PF>(p, c.b);
+    x.j0 = PF == 3 ? c.b % p.groups * p.group_nodes : 0;
+    x.rows = rows_of<PF>(a, c.b);
     x.final_out = (blo == c.pre && bhi == c.pre + nb);
     // the CTA's first unit (nothing of an earlier sequence in its range) takes slot 2c
     x.slot = 2 * (int)blockIdx.x + (c.pre - kUnitCost <= ms->plan_x0 ? 0 : 1);
@@ -542,7 +567,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;");
   if (trace && threadIdx.x == 0) trace[kTrWaited] = globaltimer_ns();
 
-  if (!PF) {
+  if (!is_prefill(PF)) {
     // ---- split plan (decode/verify), computed by every CTA for itself. All sequences,
     // laid end to end on a cost axis (each as kUnitCost fixed units, then its 128-key
     // blocks), are cut into gridDim.x nearly equal contiguous ranges; this CTA owns
@@ -557,10 +582,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
     long long mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
-      const int L = p.seq_lens[b];
+      const int L = p.seq_lens[seq_of<PF>(p, b)];
       const int64_t cap = p.pt_stride * (int64_t)p.page_size;
       if (L < 0 || (int64_t)L > cap) report(ms, MLA_ERR_BOUNDS);
-      const int nb = blocks_of(seq_len_of(p, b));
+      const int nb = blocks_of(seq_len_of(p, seq_of<PF>(p, b)));
       mine += nb > 0 ? nb + kUnitCost : 0;
     }
     // exclusive prefix of the per-thread block counts over the CTA
@@ -583,14 +608,14 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const long long x0 = total > 0 ? range_lo(c, total, n) : 0;
     const long long x1 = total > 0 ? range_lo(c + 1, total, n) : 0;
     for (int b = b_lo; b < b_hi; ++b) {
-      const int nb = blocks_of(seq_len_of(p, b));
+      const int nb = blocks_of(seq_len_of(p, seq_of<PF>(p, b)));
       const long long first = pre + kUnitCost;  // the sequence's first block
       // the range's first unit: the sequence whose span holds x0, if the range reaches
       // one of its blocks
       if (nb > 0 && pre <= x0 && x0 < first + nb && first < x1 && x0 < x1) {
         ms->plan_b0 = b;
         ms->plan_pre0 = first;
-        ms->plan_L0 = seq_len_of(p, b);
+        ms->plan_L0 = seq_len_of(p, seq_of<PF>(p, b));
       }
       if (nb > 0) pre = first + nb;
     }
@@ -606,21 +631,21 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     if (warp >= 2 && ms->plan_b0 < B) {
       const int b0 = ms->plan_b0;
       const int t = threadIdx.x - 64;
-      const int qlines = args.rows * 9;  // 1,152 bytes per row
-      if (t < qlines)
+      // 1,152 bytes per row
+      if (t < rows_of<PF>(args, b0) * 9)
         prefetch_l2(reinterpret_cast<const uint8_t*>(
-                        p.q + ((int64_t)b0 * p.R + ms->row_off[t / 9]) * kD) + (t % 9) * 128);
+                        p.q + ((int64_t)row0_of<PF>(p, b0) + ms->row_off[t / 9]) * kD) + (t % 9) * 128);
       // and the second unit's rows (its sequence follows b0) for the prologue's second pass
       const Cursor c1 = next_unit<PF>(args, first_unit<PF>(args, ms));
-      if (t < qlines && has_unit<PF>(args, ms, c1))
+      if (has_unit<PF>(args, ms, c1) && t < rows_of<PF>(args, c1.b) * 9)
         prefetch_l2(reinterpret_cast<const uint8_t*>(
-                        p.q + ((int64_t)c1.b * p.R + ms->row_off[t / 9]) * kD) + (t % 9) * 128);
+                        p.q + ((int64_t)row0_of<PF>(p, c1.b) + ms->row_off[t / 9]) * kD) + (t % 9) * 128);
       // four lines of 32 page-table entries, by the CTA's last four threads (past the
       // query lines: at most 48 rows x 9)
       const int64_t pg0 = max(0ll, ms->plan_x0 - ms->plan_pre0) * kKeyBlock / p.page_size;
       const int tp = (int)threadIdx.x - (C::kThreads - 4);
       const int64_t pg = pg0 + (int64_t)tp * 32;
-      if (tp >= 0 && pg < p.pt_stride) prefetch_l2(p.page_table + (int64_t)b0 * p.pt_stride + pg);
+      if (tp >= 0 && pg < p.pt_stride) prefetch_l2(p.page_table + (int64_t)seq_of<PF>(p, b0) * p.pt_stride + pg);
     }
     __syncthreads();
     if (trace && threadIdx.x == 0) trace[kTrPlanPrefetch] = globaltimer_ns();
@@ -670,8 +695,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   };
   // Decode reads each cached row once per call: its lines should not push out of L2 what is
   // reused (code, query rows, page tables, the partials the merge reads next). Prefill
-  // re-reads the same rows for every unit and keeps the default policy.
-  const uint64_t read_once = PF ? l2_policy_evict_normal() : l2_policy_evict_first();
+  // re-reads the same rows for every unit and keeps the default policy, as a tree's verify does
+  // for the groups of one sequence.
+  const uint64_t read_once = (is_prefill(PF) || (PF == 3 && p.groups > 1)) ? l2_policy_evict_normal()
+                                                                          : l2_policy_evict_first();
   // The first unit's first tiles go out from here, straight after the plan: on the way to
   // the producer's loop a cold kernel spends microseconds fetching instructions.
   uint32_t early = 0;
@@ -971,7 +998,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       // last visible key of new position j is L - n_q + j + mask_shift (and the unit ends at
       // key_hi); mask_shift is 0 except for a shard that holds none of the new positions
       const int lim_cap = un.key_hi - 1;
-      const int lim0 = min(lim_cap, L - p.n_q + un.j0 + p.mask_shift);
+      // (tree: the last key of the prefix, which every node sees; the nodes' own keys follow)
+      const int lim0 = min(lim_cap, L - p.n_q + (PF == 3 ? -1 : un.j0 + p.mask_shift));
       // this unit's row scales (staged with its query terms)
       ok &= warp_wait(&ms->q_full[k % C::kQB], (k / C::kQB) & 1);
       // mo: the row's running max less kPScale (p = 2^(x - mo)); kNoMax before its first key
@@ -1011,10 +1039,28 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         }
         // masking only on tiles that reach past the first new position's last visible key
         if (k0 + kTileKeys - 1 > lim0) {
+          if constexpr (PF == 3) {
+            // this thread's key is node `node`'s: the half of each row's mask that holds its bit
+            const int node = kabs - (L - p.n_q);
+            if (kabs >= un.key_hi) {
 #pragma unroll
-          for (int r = 0; r < RH; ++r) {
-            const int lim = min(lim_cap, lim0 + ms->row_j[rb + r]);
-            if (kabs > lim) x[r] = -INFINITY;
+              for (int r = 0; r < RH; ++r) x[r] = -INFINITY;
+            } else if (node >= 0) {
+              const uint32_t* half = reinterpret_cast<const uint32_t*>(p.tree_mask) +
+                                     2 * ((int64_t)un.b * p.n_q + un.j0) + (node >> 5);
+              const int nodes = p.n_q - un.j0;
+#pragma unroll
+              for (int r = 0; r < RH; ++r) {
+                const int j = min(max(ms->row_j[rb + r], 0), nodes - 1);  // (a padding row: any node)
+                if (!(__ldg(half + 2 * j) >> (node & 31) & 1u)) x[r] = -INFINITY;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < RH; ++r) {
+              const int lim = min(lim_cap, lim0 + ms->row_j[rb + r]);
+              if (kabs > lim) x[r] = -INFINITY;
+            }
           }
         }
         // The running max of a row moves only when some score exceeds it by more than the
@@ -1116,8 +1162,21 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             tmem_wait_st();
           }
         }
-        // keys past this unit's range: zero their V bytes so 0 * garbage cannot be NaN
-        if (wg == 0 && kabs >= un.key_hi) {
+        // keys past this unit's range: zero their V bytes so 0 * garbage cannot be NaN; in a
+        // tree also the keys that none of the unit's nodes sees (nodes that pad a batch, whose
+        // cache rows nobody wrote)
+        bool unseen = kabs >= un.key_hi;
+        if constexpr (PF == 3) {
+          const int node = kabs - (L - p.n_q);
+          if (wg == 0 && !unseen && node >= 0) {
+            const uint32_t* half = reinterpret_cast<const uint32_t*>(p.tree_mask) +
+                                   2 * ((int64_t)un.b * p.n_q + un.j0) + (node >> 5);
+            uint32_t any = 0;
+            for (int j = 0; j * p.H < un.rows; ++j) any |= __ldg(half + 2 * j);
+            unseen = !(any >> (node & 31) & 1u);
+          }
+        }
+        if (wg == 0 && unseen) {
           uint8_t* st = smem + C::kOffStages + s * C::kStageStride + (i >> 6) * 8192 + (i & 63) * 128;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -1332,7 +1391,7 @@ cudaError_t launch_rp_tr(const DecodeArgs& a, const CUtensorMap& mm, const CUten
 template <int RP, int PF>
 cudaError_t launch_rp(const DecodeArgs& a, const CUtensorMap& mm, const CUtensorMap& mt,
                       int grid, cudaStream_t s) {
-  if constexpr (PF == 2) {  // (never traced)
+  if constexpr (PF >= 2) {  // (never traced)
     return launch_rp_tr<RP, PF, false>(a, mm, mt, grid, s);
   } else {
     return a.p.trace ? launch_rp_tr<RP, PF, true>(a, mm, mt, grid, s)
@@ -1374,6 +1433,27 @@ cudaError_t launch_decode_tc(const AttnParams& p, int num_sms, cudaStream_t s, i
     ++*launches;
   }
   return cudaSuccess;
+}
+
+// Tree verify: the split plan over the groups of every sequence's nodes (p.B groups in all, at
+// most 48 rows each; mla_internal.cuh, tree_groups).
+cudaError_t launch_tree_tc(const AttnParams& p, cudaStream_t s, int* launches) {
+  CUtensorMap mm, mt;
+  if (!encode_pool_maps(p, &mm, &mt)) return cudaErrorInvalidValue;
+  DecodeArgs a = {};
+  a.p = p;
+  a.Hs = p.H;
+  a.rows = p.R;
+  a.status_overwrite = 1;
+  cudaError_t e;
+  if (a.rows <= 16)
+    e = launch_rp<16, 3>(a, mm, mt, p.num_ctas, s);
+  else if (a.rows <= 32)
+    e = launch_rp<32, 3>(a, mm, mt, p.num_ctas, s);
+  else
+    e = launch_rp<48, 3>(a, mm, mt, p.num_ctas, s);
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 // Causal prefill of one sequence: units are blocks of P = 48 / H new positions (all their

@@ -1,4 +1,4 @@
-// mla_cache.cu -- appending new latent rows to the paged FP8 cache.
+// mla_cache.cu -- writing new latent rows to the paged FP8 cache, and reading rows back.
 //
 // The step in front of decode, verify and prefill: the new positions' latent rows (576
 // wide: 512 latent + 64 RoPE) are written into their cache slots as e4m3 codes under the
@@ -10,9 +10,12 @@
 // code = e4m3(x * inv_scale), both the reciprocal and the product rounded to binary32,
 // the conversion rounding to nearest even and saturating at +-448. HBM-bound: 1,152 bytes
 // read and 576 written per row, one warp per row, every access 16 bytes wide.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "mla_internal.cuh"
+#include "mla_rope.cuh"
 
 namespace mla {
 namespace {
@@ -58,7 +61,175 @@ __global__ void __launch_bounds__(256) cache_append_kernel(uint8_t* __restrict__
   }
 }
 
+// Rows as the latent projection leaves them, one warp a row: lane l holds latent entries 16 l ..
+// 16 l + 15 and RoPE pair l. y = c * rsqrt(mean(c^2) + eps) * w for the latent (the sum of
+// squares of 512 float32 values over the lanes), the pair turned to its position, and
+// e4m3(y * inv) for all 576, the only rounding: the values never pass through bf16, which a
+// norm and a rotation run on their own would add. HBM-bound when there are many rows (1,152
+// bytes read and 576 written a row), by the launch and one round of loads when there are few.
+__global__ void __launch_bounds__(256)
+    cache_append_rope_kernel(const __grid_constant__ AppendRopeArgs a,
+                             const __grid_constant__ mla_rope_t rope) {
+  const int lane = threadIdx.x & 31;
+  const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < a.n; i += nwarps) {
+    const int64_t slot = a.slots[i];
+    if (slot < 0) continue;  // padding: nothing to write
+    if (slot >= a.pool_rows) {
+      if (lane == 0 && a.status) atomicCAS(a.status, 0u, (unsigned)MLA_ERR_BOUNDS);
+      continue;
+    }
+    const uint16_t* row = a.x + i * a.x_stride;
+    const uint4* src = reinterpret_cast<const uint4*>(row) + 2 * lane;
+    const uint4 v0 = src[0], v1 = src[1];
+    uint32_t pair;  // this lane's RoPE pair, the first entry in the low half
+    if (rope.interleaved)
+      pair = *reinterpret_cast<const uint32_t*>(row + kDV + 2 * lane);
+    else
+      pair = row[kDV + lane] | (uint32_t)row[kDV + MLA_ROPE / 2 + lane] << 16;
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    float c[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c[2 * e] = __uint_as_float(w[e] << 16);
+      c[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+    if (a.weight) {
+      const uint4* wp = reinterpret_cast<const uint4*>(a.weight) + 2 * lane;
+      const uint4 g0 = __ldg(wp), g1 = __ldg(wp + 1);
+      const uint32_t g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ss = fmaf(c[e], c[e], ss);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = rsqrtf(ss * (1.0f / kDV) + a.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        c[2 * e] = c[2 * e] * r * __uint_as_float(g[e] << 16);
+        c[2 * e + 1] = c[2 * e + 1] * r * __uint_as_float(g[e] & 0xFFFF0000u);
+      }
+    }
+    float2 pe = make_float2(__uint_as_float(pair << 16), __uint_as_float(pair & 0xFFFF0000u));
+    if (a.positions)
+      pe = rope_turn(pe.x, pe.y, rope_cos_sin(rope.turns[lane], a.positions[i], rope.amplitude));
+    uint32_t code[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      code[e] = e4m3x2(c[4 * e] * a.inv, c[4 * e + 1] * a.inv) |
+                e4m3x2(c[4 * e + 2] * a.inv, c[4 * e + 3] * a.inv) << 16;
+    uint8_t* dst = a.pool + slot * kD;
+    reinterpret_cast<uint4*>(dst)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
+    uint32_t pc = e4m3x2(pe.x * a.inv, pe.y * a.inv);
+    if (!rope.interleaved) {
+      // dims 2 l, 2 l + 1 of the row: first entries of two pairs (lanes below 16) or second ones
+      const uint32_t p0 = __shfl_sync(0xffffffffu, pc, (2 * lane) & 31);
+      const uint32_t p1 = __shfl_sync(0xffffffffu, pc, (2 * lane + 1) & 31);
+      pc = lane < 16 ? (p0 & 0xFFu) | (p1 & 0xFFu) << 8 : (p0 >> 8) | (p1 & 0xFF00u);
+    }
+    *reinterpret_cast<uint16_t*>(dst + kDV + 2 * lane) = (uint16_t)pc;
+  }
+}
+
+// Cached rows back into a dense array. A CTA takes 32 consecutive output rows: first a thread a
+// row finds its sequence (binary search in cu_rows), its page and the pool row, then the threads
+// move the rows 8 codes at a time (72 pieces a row, 4 rows a round), every load of a thread in
+// flight before its first store. HBM-bound: 576 bytes read and 1,152 (bf16) or 2,304 (float32)
+// written a row.
+constexpr int kGatherRows = 32;
+constexpr int kGatherPieces = kD / 8;                // 8-code pieces of a row
+constexpr int kGatherThreads = 4 * kGatherPieces;    // four rows a round
+constexpr int kGatherRounds = kGatherRows / 4;
+constexpr int64_t kRowSkip = -1, kRowBad = -2;
+
+template <typename Out>
+__global__ void __launch_bounds__(kGatherThreads)
+    cache_gather_kernel(const __grid_constant__ mla_kv_t kv, int B, const int32_t* __restrict__ starts,
+                        const int64_t* __restrict__ cu_rows, int64_t n, Out* __restrict__ out,
+                        unsigned* status) {
+  __shared__ int64_t s_row[kGatherRows];  // pool row, or kRowSkip / kRowBad
+  const int64_t row0 = (int64_t)blockIdx.x * kGatherRows;
+  if (threadIdx.x < kGatherRows) {
+    const int64_t row = row0 + threadIdx.x;
+    int64_t from = kRowSkip;
+    if (row < n && row >= cu_rows[0] && row < cu_rows[B]) {
+      int lo = 0, hi = B;  // cu_rows[lo] <= row < cu_rows[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu_rows[mid] <= row)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const int64_t pos = row - cu_rows[lo] + (starts ? starts[lo] : 0);
+      from = kRowBad;
+      if (pos >= 0 && pos < kv.seq_lens[lo] && pos / kv.page_size < kv.page_table_stride) {
+        const int64_t page = kv.page_table[lo * kv.page_table_stride + pos / kv.page_size];
+        if (page >= 0 && page < kv.num_pages) from = page * kv.page_size + pos % kv.page_size;
+      }
+      if (from == kRowBad && status) atomicCAS(status, 0u, (unsigned)MLA_ERR_BOUNDS);
+    }
+    s_row[threadIdx.x] = from;
+  }
+  __syncthreads();
+  const int r = threadIdx.x / kGatherPieces, piece = threadIdx.x % kGatherPieces;
+  uint2 code[kGatherRounds];
+#pragma unroll
+  for (int k = 0; k < kGatherRounds; ++k) {
+    const int64_t from = s_row[4 * k + r];
+    code[k] = make_uint2(0u, 0u);
+    if (from >= 0) code[k] = __ldcs(reinterpret_cast<const uint2*>(kv.pool + from * kD) + piece);
+  }
+#pragma unroll
+  for (int k = 0; k < kGatherRounds; ++k) {
+    if (s_row[4 * k + r] == kRowSkip) continue;
+    const uint32_t w[4] = {code[k].x & 0xFFFFu, code[k].x >> 16, code[k].y & 0xFFFFu, code[k].y >> 16};
+    float2 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[e], __NV_E4M3);
+      v[e] = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      v[e].x *= kv.kv_scale;
+      v[e].y *= kv.kv_scale;
+    }
+    Out* dst = out + (row0 + 4 * k + r) * kD + 8 * piece;
+    if constexpr (sizeof(Out) == 4) {
+      __stcs(reinterpret_cast<float4*>(dst), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+      __stcs(reinterpret_cast<float4*>(dst) + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
+    } else {
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[e].x, v[e].y);
+        o[e] = *reinterpret_cast<const uint32_t*>(&t);
+      }
+      __stcs(reinterpret_cast<uint4*>(dst), make_uint4(o[0], o[1], o[2], o[3]));
+    }
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_cache_append_rope(const AppendRopeArgs& a, const mla_rope_t& rope, int num_sms,
+                                     cudaStream_t s) {
+  const int64_t blocks = (a.n * 32 + 255) / 256;  // one warp per row, at most 8 CTAs per SM
+  const int grid = (int)(blocks < (int64_t)num_sms * 8 ? blocks : (int64_t)num_sms * 8);
+  cache_append_rope_kernel<<<grid, 256, 0, s>>>(a, rope);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_gather(const mla_kv_t& kv, int B, const int32_t* starts,
+                                const int64_t* cu_rows, int64_t n, void* out, int out_f32,
+                                unsigned* status, cudaStream_t s) {
+  const unsigned grid = (unsigned)((n + kGatherRows - 1) / kGatherRows);
+  if (out_f32)
+    cache_gather_kernel<float><<<grid, kGatherThreads, 0, s>>>(kv, B, starts, cu_rows, n,
+                                                               static_cast<float*>(out), status);
+  else
+    cache_gather_kernel<uint16_t><<<grid, kGatherThreads, 0, s>>>(kv, B, starts, cu_rows, n,
+                                                                  static_cast<uint16_t*>(out), status);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_cache_append(uint8_t* pool, int64_t pool_rows, const uint16_t* x,
                                 const int64_t* slots, int64_t n, float inv, unsigned* status,

@@ -67,6 +67,18 @@ inline WsLayout ws_layout(int B, int rows_per_seq, int num_sms) {
   return w;
 }
 
+// Tree verify: a sequence's n nodes run as groups of whole nodes, H rows each, of at most 48
+// rows (what one unit of the attention kernel holds), as equal as they come.
+struct TreeGroups {
+  int groups, nodes;  // groups a sequence, nodes of a group (the last may hold fewer)
+};
+inline TreeGroups tree_groups(int n, int H) {
+  const int most = 48 / H;
+  const int groups = (n + most - 1) / most;
+  const int nodes = (n + groups - 1) / groups;
+  return {(n + nodes - 1) / nodes, nodes};
+}
+
 // Prefill: the header, the per-CTA status words, the per-CTA query images (48 rows), and
 // the partials of the units of the last round that are split in two along the keys: one
 // slot per CTA, 48 rows each (float32 LSE, then float32 outputs).
@@ -110,6 +122,10 @@ struct AttnParams {
   int test_stall;     // test hook: the producer issues no loads, so every consumer's bounded
                       // wait runs out and the call reports MLA_ERR_TIMEOUT
   int mask_shift;     // key n visible to new position j iff n <= L - n_q + j + mask_shift
+  // tree verify (null otherwise): which nodes each node sees. B then counts groups of
+  // group_nodes nodes, groups of them a sequence, R the rows of a full group, n_q all nodes.
+  const uint64_t* tree_mask;  // [sequences][n_q]
+  int groups, group_nodes;
   unsigned long long* trace;  // profiling hook: kTraceWords globaltimer stamps per CTA, or null
   int trace_ctas;             // CTAs the trace buffer has room for
 };
@@ -197,6 +213,8 @@ struct MhaArgs {
 // Launchers (each returns the CUDA error of its launch).
 cudaError_t launch_merge(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_decode_tc(const AttnParams& p, int num_sms, cudaStream_t s, int* launches);
+cudaError_t launch_tree_tc(const AttnParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_merge_tree(const AttnParams& p, int sequences, cudaStream_t s);
 cudaError_t launch_prefill_tc(const AttnParams& p, int num_sms, cudaStream_t s, int* launches);
 cudaError_t launch_merge_prefill(const AttnParams& p, int P, int split_units, cudaStream_t s);
 cudaError_t launch_merge_standalone(const float* part_out, const float* part_lse, int S, int64_t R,
@@ -204,6 +222,39 @@ cudaError_t launch_merge_standalone(const float* part_out, const float* part_lse
 cudaError_t launch_cache_append(uint8_t* pool, int64_t pool_rows, const uint16_t* x,
                                 const int64_t* slots, int64_t n, float inv, unsigned* status,
                                 int num_sms, cudaStream_t s);
+cudaError_t launch_rope(const mla_rope_t& rope, const uint16_t* x, int64_t x_token, int64_t x_head,
+                        const int64_t* positions, int64_t n, int H, uint16_t* out, int64_t out_token,
+                        int64_t out_head, int num_sms, cudaStream_t s);
+struct AppendRopeArgs {
+  uint8_t* pool;
+  int64_t pool_rows;
+  const uint16_t* x;       // [n] rows of 576 bf16, x_stride elements apart
+  int64_t x_stride;
+  const int64_t* slots;    // [n]
+  int64_t n;
+  float inv;               // 1 / kv_scale
+  const uint16_t* weight;  // [512] bf16, or null: the latent is not normalised
+  float eps;
+  const int64_t* positions;  // [n], or null: no rotation
+  unsigned* status;        // or null
+};
+cudaError_t launch_cache_append_rope(const AppendRopeArgs& a, const mla_rope_t& rope, int num_sms,
+                                     cudaStream_t s);
+cudaError_t launch_cache_gather(const mla_kv_t& kv, int B, const int32_t* starts,
+                                const int64_t* cu_rows, int64_t n, void* out, int out_f32,
+                                unsigned* status, cudaStream_t s);
+struct AcceptArgs {
+  const float* target;     // [B][n][V]
+  const int32_t* tokens;   // [B][n]
+  const int32_t* parents;  // [B][n], or null: a chain
+  const float* draft;      // [B][n - 1][V], or null: drafts without probabilities
+  const float* uniforms;   // [B][n + 1]
+  int B, n, V;
+  int32_t* out_tokens;     // [B][n]
+  int32_t* path;           // [B][n]
+  int32_t* num_accepted;   // [B]
+};
+cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s);
 cudaError_t launch_mha_prefill(const MhaArgs& a, int num_sms, cudaStream_t s, int* launches);
 cudaError_t launch_mha_projection(const void* latent, const void* w, void* kvup, int L, int H,
                                   float kv_scale, int precise, unsigned* status, cudaStream_t s);

@@ -179,13 +179,35 @@ __device__ __forceinline__ int plan_blocks(const AttnParams& p, int b) {
 template <int VEC, int WPR>
 constexpr int kMergeMinBlocks = (VEC == 16 && WPR == 4) ? 2 : ((VEC == 1) ? 0 : 3);
 
-template <int VEC, int WPR, typename OutT>
+// TREE: what the plan calls a sequence is a group of a sequence's nodes (mla_internal.cuh,
+// tree_groups); rows are still numbered through all sequences' nodes.
+template <bool TREE>
+struct PlanRow {
+  int b;      // the plan's sequence
+  int64_t r;  // row within it
+};
+template <bool TREE>
+__device__ __forceinline__ PlanRow<TREE> plan_row(const AttnParams& p, int64_t row) {
+  if constexpr (TREE) {
+    const int64_t per = (int64_t)p.n_q * p.H;
+    const int64_t in = row % per;
+    return {(int)(row / per * p.groups + in / p.R), in % p.R};
+  } else {
+    return {(int)(row / p.R), row % p.R};
+  }
+}
+template <bool TREE>
+__device__ __forceinline__ int plan_seq(const AttnParams& p, int b) {
+  return TREE ? b / p.groups : b;
+}
+
+template <int VEC, int WPR, typename OutT, bool TREE = false>
 __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
     merge_split_kernel(AttnParams p) {
   constexpr int kRowsPerCta = kMergeWarps / WPR;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = warp / WPR, gt = threadIdx.x - g * 32 * WPR;
-  const int64_t rows = (int64_t)p.B * p.R;
+  const int64_t rows = TREE ? (int64_t)(p.B / p.groups) * p.n_q * p.H : (int64_t)p.B * p.R;
   const int64_t row0 = (int64_t)blockIdx.x * kRowsPerCta;
   // the cost axis: every sequence as kUnitCost units, then its blocks (none if empty);
   // its length, and the units before each row group's sequence
@@ -193,11 +215,11 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
   long long tot = 0, before[kRowsPerCta];
 #pragma unroll
   for (int k = 0; k < kRowsPerCta; ++k) {
-    bg[k] = (int)(min(row0 + k, rows - 1) / p.R);
+    bg[k] = plan_row<TREE>(p, min(row0 + k, rows - 1)).b;
     before[k] = 0;
   }
   for (int x = threadIdx.x; x < p.B; x += kMergeThreads) {
-    const int nb = plan_blocks(p, x);
+    const int nb = plan_blocks(p, plan_seq<TREE>(p, x));
     const long long cost = nb > 0 ? nb + kUnitCost : 0;
     tot += cost;
 #pragma unroll
@@ -228,8 +250,8 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
   const int chunk = blockIdx.y;
   static_assert(kRowsPerCta <= 2, "row groups a CTA");
   const int b = (g == 0) ? bg[0] : bg[kRowsPerCta - 1];  // (no indexing of a local array)
-  const int64_t r = row % p.R;
-  const int num_blocks = plan_blocks(p, b);
+  const int64_t r = plan_row<TREE>(p, row).r;
+  const int num_blocks = plan_blocks(p, plan_seq<TREE>(p, b));
   OutT* out_row;
   if constexpr (sizeof(OutT) == 4)
     out_row = p.out_f32 + row * kDV;
@@ -336,6 +358,26 @@ cudaError_t launch_merge(const AttnParams& p, cudaStream_t s) {
   if (vec == 16) return cudaLaunchKernelEx(&cfg, merge_split_kernel<16, kMergeWarps, uint16_t>, p);
   if (vec == 4) return cudaLaunchKernelEx(&cfg, merge_split_kernel<4, kMergeWarps, uint16_t>, p);
   return cudaLaunchKernelEx(&cfg, merge_split_kernel<1, kMergeWarps, uint16_t>, p);
+}
+
+cudaError_t launch_merge_tree(const AttnParams& p, int sequences, cudaStream_t s) {
+  const int64_t rows = (int64_t)sequences * p.n_q * p.H;
+  const int vec = merge_vec(rows, p.num_ctas);
+  const bool two_rows = vec == 16 && p.num_ctas <= 8 * p.B;  // as launch_merge
+  const int64_t per = two_rows ? 2 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + per - 1) / per), kDV / (32 * vec));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (two_rows) return cudaLaunchKernelEx(&cfg, merge_split_kernel<16, 4, uint16_t, true>, p);
+  if (vec == 16) return cudaLaunchKernelEx(&cfg, merge_split_kernel<16, kMergeWarps, uint16_t, true>, p);
+  if (vec == 4) return cudaLaunchKernelEx(&cfg, merge_split_kernel<4, kMergeWarps, uint16_t, true>, p);
+  return cudaLaunchKernelEx(&cfg, merge_split_kernel<1, kMergeWarps, uint16_t, true>, p);
 }
 
 cudaError_t launch_merge_prefill(const AttnParams& p, int P, int split_units, cudaStream_t s) {
