@@ -138,7 +138,7 @@ size_t mla_workspace_size(mla_op_t op, int B, int H, int n_q, int device) {
   if (op == MLA_OP_VERIFY_TREE) {
     if (n_q < 1 || n_q > MLA_MAX_TREE) return 0;
     const int sms = sm_count(device);
-    return sms > 0 ? mla::ws_layout(B, mla::tree_groups(n_q, H).nodes * H, sms).total : 0;
+    return sms > 0 ? mla::ws_layout(B, mla::tree_plan(n_q, H, sms).nodes * H, sms).total : 0;
   }
   if (op == MLA_OP_DECODE) n_q = 1;
   if (n_q < 1 || n_q > MLA_MAX_NQ) return 0;
@@ -191,15 +191,16 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
   if ((st = current_device(&dev)) != MLA_OK) return st;
   const int sms = sm_count(dev);
   if (sms <= 0) return MLA_ERR_CUDA;
-  const mla::TreeGroups g = mla::tree_groups(n, H);
+  const mla::TreePlan g = mla::tree_plan(n, H, sms);
   const mla::WsLayout w = mla::ws_layout(B, g.nodes * H, sms);
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE;
   if (B == 0) return MLA_OK;
   mla::AttnParams p = base_params(kv, q, B, n, H, sm_scale, out, lse);
-  p.B = B * g.groups;
+  p.B = B * g.passes;
   p.R = p.part_rows = g.nodes * H;
-  p.groups = g.groups;
   p.group_nodes = g.nodes;
+  p.team = g.team;
+  p.passes = g.passes;
   p.tree_mask = tree_mask;
   p.trace = nullptr;  // the profiling hook traces decode, verify and prefill
   char* base = static_cast<char*>(workspace);
@@ -209,7 +210,7 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
   p.part_out = reinterpret_cast<float*>(base + w.part_out);
   p.qimg = reinterpret_cast<uint8_t*>(base + w.qimg);
   p.qimg_stride = (int64_t)w.qimg_stride;
-  p.num_ctas = sms;
+  p.num_ctas = sms / g.team * g.team;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_mark(g_prof_start, s);
   const cudaError_t e = mla::launch_tree_tc(p, s, &g_last_launches);

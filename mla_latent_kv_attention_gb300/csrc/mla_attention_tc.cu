@@ -74,6 +74,10 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;        // 1 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPScale = 11.0f;     // P carried as 2^(x - m + 11): at most 2^15 while x <= m + 4
 constexpr float kRescaleGap = 4.0f;  // the running max (log2 units) moves only past m + 4
+// Tree verify uses what e5m2 still holds above that (2^15.75 < 57,344 < 2^16): moving the max
+// rescales O in tensor memory, and half as many tiles of N(0, 1) data do (a rescale costs its
+// warpgroup about 1.5 us).
+constexpr float kTreeGap = 4.75f;
 constexpr float kQTerm2 = 16.0f;     // the second query term carries the residual times 16
 constexpr float kNoMax = -1e30f;     // running max (less kPScale) of a row that has seen no key
 constexpr int kPrefetchTiles = 1;    // tiles the producer pulls into L2 ahead of its TMA loads
@@ -100,6 +104,8 @@ struct Cfg {
   static constexpr __host__ __device__ int ocol(int c) {
     return kOCol + (c < kStackedChunks ? c * 3 * RP : kStackedChunks * 3 * RP + (c - kStackedChunks) * RP);
   }
+  // all O^T columns are one run of kOParts pieces of RP columns (chunk by chunk, term by term)
+  static constexpr int kOParts = kStackedChunks * 3 + (4 - kStackedChunks);
   static constexpr int kTmemUsed = ocol(3) + oterms(3) * RP;
   static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
   static constexpr int kQBytes = NQK * kD;
@@ -234,24 +240,31 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int64_t idx, floa
 // its own paths.
 __host__ __device__ constexpr bool is_prefill(int pf) { return pf == 1 || pf == 2; }
 
-// Tree verify: what the plan calls a sequence is a group of p.group_nodes nodes of one, group
-// b % groups of sequence b / groups. The sequence an index of the plan's stands for, its first
-// row of q, out and lse, and its rows (the last group may hold fewer nodes).
+// Tree verify: neighbouring CTAs form teams of p.team, and the plan cuts its cost axis into one
+// range a team. What the plan calls a sequence is a pass over one, in which member m of the team
+// takes group (pass * team + m) of its nodes: the members walk the same keys at the same time,
+// so a tile comes from HBM once and from L2 for the others. The sequence an index of the plan's
+// stands for, the first node of this CTA's group of it, the group's first row of q, out and lse,
+// and its rows (the last group may hold fewer nodes).
 template <int PF>
 __device__ __forceinline__ int seq_of(const AttnParams& p, int b) {
-  return PF == 3 ? b / p.groups : b;
+  return PF == 3 ? b / p.passes : b;
+}
+template <int PF>
+__device__ __forceinline__ int node0_of(const AttnParams& p, int b) {
+  return PF == 3 ? (b % p.passes * p.team + (int)blockIdx.x % p.team) * p.group_nodes : 0;
 }
 template <int PF>
 __device__ __forceinline__ int row0_of(const AttnParams& p, int b) {
   if constexpr (PF == 3)
-    return (b / p.groups * p.n_q + b % p.groups * p.group_nodes) * p.H;
+    return (seq_of<PF>(p, b) * p.n_q + node0_of<PF>(p, b)) * p.H;
   else
     return b * p.R;
 }
 template <int PF>
 __device__ __forceinline__ int rows_of(const DecodeArgs& a, int b) {
   if constexpr (PF == 3)
-    return min(a.p.group_nodes, a.p.n_q - b % a.p.groups * a.p.group_nodes) * a.p.H;
+    return min(a.p.group_nodes, a.p.n_q - node0_of<PF>(a.p, b)) * a.p.H;
   else
     return a.rows;
 }
@@ -300,7 +313,7 @@ __device__ __forceinline__ UnitInfo unit_info(const DecodeArgs& a, const Misc* m
     x.key_lo = (int)(blo - c.pre) * kKeyBlock;
     x.key_hi = (bhi > blo) ? min(c.L, (int)(bhi - c.pre) * kKeyBlock) : x.key_lo;
     x.qrow0 = row0_of<PF>(p, c.b);
-    x.j0 = PF == 3 ? c.b % p.groups * p.group_nodes : 0;
+    x.j0 = node0_of<PF>(p, c.b);
     x.rows = rows_of<PF>(a, c.b);
     x.final_out = (blo == c.pre && bhi == c.pre + nb);
     // the CTA's first unit (nothing of an earlier sequence in its range) takes slot 2c
@@ -604,7 +617,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       total += ms->scan[w];
     }
     long long pre = before + incl - mine;
-    const long long n = gridDim.x, c = blockIdx.x;
+    // (a tree's ranges belong to teams of CTAs)
+    const long long n = PF == 3 ? gridDim.x / p.team : gridDim.x;
+    const long long c = PF == 3 ? blockIdx.x / p.team : blockIdx.x;
     const long long x0 = total > 0 ? range_lo(c, total, n) : 0;
     const long long x1 = total > 0 ? range_lo(c + 1, total, n) : 0;
     for (int b = b_lo; b < b_hi; ++b) {
@@ -697,7 +712,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   // reused (code, query rows, page tables, the partials the merge reads next). Prefill
   // re-reads the same rows for every unit and keeps the default policy, as a tree's verify does
   // for the groups of one sequence.
-  const uint64_t read_once = (is_prefill(PF) || (PF == 3 && p.groups > 1)) ? l2_policy_evict_normal()
+  const uint64_t read_once = (is_prefill(PF) || (PF == 3 && p.team * p.passes > 1)) ? l2_policy_evict_normal()
                                                                           : l2_policy_evict_first();
   // The first unit's first tiles go out from here, straight after the plan: on the way to
   // the producer's loop a cold kernel spends microseconds fetching instructions.
@@ -937,6 +952,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // Two or three warpgroups, each owning an equal share of the query rows; thread i of a
     // warpgroup owns key i of the tile (its TMEM lane).
     constexpr int RH = C::kRH;
+    constexpr float kHeadroom = kPScale + (PF == 3 ? kTreeGap : kRescaleGap);
     const int wg = (warp - kSoftmaxWarp0) >> 2;
     const int rb = wg * RH;  // rows [rb, rb + RH)
     const int wq = warp & 3;  // TMEM lane quadrant
@@ -1069,7 +1085,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         // common case skips the exchange of per-row maxima.
         bool over = false;
 #pragma unroll
-        for (int r = 0; r < RH; ++r) over |= (x[r] > mo[r] + (kPScale + kRescaleGap));
+        for (int r = 0; r < RH; ++r) over |= (x[r] > mo[r] + kHeadroom);
         over = __any_sync(0xffffffffu, over);
         if (__any_sync(0xffffffffu, !ok)) {  // the warp's once-a-tile vote on its waits
           ok = false;
@@ -1093,7 +1109,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             const float4 t4 = *reinterpret_cast<const float4*>(&red[(rb + r) * 4]);
             const float tm = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
             float al = 1.f;
-            if (tm > mo[r] + (kPScale + kRescaleGap)) {  // lazy: the headroom absorbs small increases
+            if (tm > mo[r] + kHeadroom) {  // lazy: the headroom absorbs small increases
               al = ex2(mo[r] + kPScale - tm);  // 0 before the first key (nothing accumulated yet)
               need_rescale |= (mo[r] != kNoMax);
               l[r] *= al;
@@ -1138,7 +1154,25 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           tc_fence_after();
         }
         if (t > 0) {
-          if (need_rescale) {
+          if (PF == 3 && need_rescale) {
+            // (tree: one small loop over the pieces of O; its code is fetched cold when a short
+            // call first needs it)
+            __syncwarp();
+            const float* al = &ms->alpha[rb];
+#pragma unroll 1
+            for (int part = 0; part < C::kOParts; ++part) {
+              const uint32_t a = tmem + lane_addr + C::kOCol + part * RP + rb;
+              float v[RH];
+#pragma unroll
+              for (int cc = 0; cc < RH; cc += 8) tmem_ld8(a + cc, *reinterpret_cast<float(*)[8]>(&v[cc]));
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < RH; ++e) v[e] *= al[e];
+#pragma unroll
+              for (int cc = 0; cc < RH; cc += 8) tmem_st8(a + cc, *reinterpret_cast<float(*)[8]>(&v[cc]));
+            }
+            tmem_wait_st();
+          } else if (need_rescale) {
             __syncwarp();
             const float* al = &ms->alpha[rb];
             // (rare: rolled up at 16 rows, so that the code of the tile loop stays small; at
@@ -1245,6 +1279,47 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       }
       tc_fence_after();
       if (trace && threadIdx.x == 32 * kSoftmaxWarp0) trace[kTrLastPV] = globaltimer_ns();
+      if constexpr (PF == 3) {
+        // One small loop (the rows' reciprocals in shared memory, not in registers that only
+        // unrolled code can index): a short call fetches the epilogue's code cold. Row r of the
+        // unit is row r of its group in q, out and lse.
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < RH; ++r)
+          if (lane == 0) ms->alpha[rb + r] = inv[r];  // (every warp of the warpgroup the same)
+        __syncwarp();
+#pragma unroll 1
+        for (int u = 0; u < 4 * (RH / 8); ++u) {
+          const int c = u / (RH / 8), row = rb + u % (RH / 8) * 8;
+          if (row >= R) continue;
+          const uint32_t a = tmem + lane_addr + C::ocol(c) + row;
+          float o[8];
+          tmem_ld8(a, o);
+          if (C::oterms(c) == 3) {
+            float o1[8], o2[8];
+            tmem_ld8(a + RP, o1);
+            tmem_ld8(a + 2 * RP, o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += o1[e] + o2[e];
+          } else {
+            tmem_wait_ld();
+          }
+          const int dv = c * 128 + i;
+          const float* scale = &ms->alpha[row];
+          if (final_out) {
+            uint16_t* dst = p.out + ((int64_t)un.qrow0 + row) * kDV + dv;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (row + e < R) dst[e * kDV] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e] * scale[e]));
+          } else {
+            float* dst = p.part_out + ((int64_t)un.slot * p.part_rows + row) * kDV + dv;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (row + e < R) dst[e * kDV] = o[e] * scale[e];
+          }
+        }
+      } else {
       // (once a unit: rolled up over the dv chunks at 16 rows, fewer instructions to fetch)
 #pragma unroll(C::kUnrollChunks)
       for (int c = 0; c < 4; ++c) {
@@ -1279,6 +1354,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             }
           }
         }
+      }
       }
       tc_fence_before();
       if (i < RH && rb + i < R) {
@@ -1435,8 +1511,8 @@ cudaError_t launch_decode_tc(const AttnParams& p, int num_sms, cudaStream_t s, i
   return cudaSuccess;
 }
 
-// Tree verify: the split plan over the groups of every sequence's nodes (p.B groups in all, at
-// most 48 rows each; mla_internal.cuh, tree_groups).
+// Tree verify: the split plan over the passes of every sequence's groups of nodes (p.B passes in
+// all, groups of at most 48 rows; mla_internal.cuh, tree_plan).
 cudaError_t launch_tree_tc(const AttnParams& p, cudaStream_t s, int* launches) {
   CUtensorMap mm, mt;
   if (!encode_pool_maps(p, &mm, &mt)) return cudaErrorInvalidValue;

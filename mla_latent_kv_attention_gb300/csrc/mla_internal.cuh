@@ -68,15 +68,25 @@ inline WsLayout ws_layout(int B, int rows_per_seq, int num_sms) {
 }
 
 // Tree verify: a sequence's n nodes run as groups of whole nodes, H rows each, of at most 48
-// rows (what one unit of the attention kernel holds), as equal as they come.
-struct TreeGroups {
-  int groups, nodes;  // groups a sequence, nodes of a group (the last may hold fewer)
+// rows (what one unit of the attention kernel holds), as equal as they come. Every group reads
+// all the sequence's keys, so teams of neighbouring CTAs take a group each of the same keys (a
+// sequence's groups in `passes` passes of a team). The team divides the groups; of the divisors
+// from four up (where the tensor cores, not HBM, set the pace of a team) or the whole the one
+// that leaves the fewest SMs without a team.
+struct TreePlan {
+  int nodes;   // nodes of a group (the last may hold fewer)
+  int team;    // CTAs of a team
+  int passes;  // groups a sequence = team * passes
 };
-inline TreeGroups tree_groups(int n, int H) {
+inline TreePlan tree_plan(int n, int H, int num_sms) {
   const int most = 48 / H;
-  const int groups = (n + most - 1) / most;
+  int groups = (n + most - 1) / most;
   const int nodes = (n + groups - 1) / groups;
-  return {(n + nodes - 1) / nodes, nodes};
+  groups = (n + nodes - 1) / nodes;
+  int team = groups <= num_sms ? groups : 1;
+  for (int t = 4; t < groups; ++t)
+    if (groups % t == 0 && num_sms / t * t > num_sms / team * team) team = t;
+  return {nodes, team, groups / team};
 }
 
 // Prefill: the header, the per-CTA status words, the per-CTA query images (48 rows), and
@@ -122,10 +132,10 @@ struct AttnParams {
   int test_stall;     // test hook: the producer issues no loads, so every consumer's bounded
                       // wait runs out and the call reports MLA_ERR_TIMEOUT
   int mask_shift;     // key n visible to new position j iff n <= L - n_q + j + mask_shift
-  // tree verify (null otherwise): which nodes each node sees. B then counts groups of
-  // group_nodes nodes, groups of them a sequence, R the rows of a full group, n_q all nodes.
+  // tree verify (null otherwise): which nodes each node sees. B then counts passes over
+  // sequences (`passes` each), R the rows of a full group of group_nodes nodes, n_q all nodes.
   const uint64_t* tree_mask;  // [sequences][n_q]
-  int groups, group_nodes;
+  int group_nodes, team, passes;
   unsigned long long* trace;  // profiling hook: kTraceWords globaltimer stamps per CTA, or null
   int trace_ctas;             // CTAs the trace buffer has room for
 };

@@ -179,26 +179,27 @@ __device__ __forceinline__ int plan_blocks(const AttnParams& p, int b) {
 template <int VEC, int WPR>
 constexpr int kMergeMinBlocks = (VEC == 16 && WPR == 4) ? 2 : ((VEC == 1) ? 0 : 3);
 
-// TREE: what the plan calls a sequence is a group of a sequence's nodes (mla_internal.cuh,
-// tree_groups); rows are still numbered through all sequences' nodes.
-template <bool TREE>
+// TREE: the plan's sequences are passes over one, its ranges belong to teams of CTAs, and
+// member m's slots are those of CTA range * team + m (mla_internal.cuh, tree_plan); rows are
+// still numbered through all sequences' nodes.
 struct PlanRow {
   int b;      // the plan's sequence
-  int64_t r;  // row within it
+  int64_t r;  // row within its unit
+  int member;
 };
 template <bool TREE>
-__device__ __forceinline__ PlanRow<TREE> plan_row(const AttnParams& p, int64_t row) {
+__device__ __forceinline__ PlanRow plan_row(const AttnParams& p, int64_t row) {
   if constexpr (TREE) {
-    const int64_t per = (int64_t)p.n_q * p.H;
-    const int64_t in = row % per;
-    return {(int)(row / per * p.groups + in / p.R), in % p.R};
+    const int per = p.n_q * p.H;
+    const int in = (int)(row % per), group = in / p.R;
+    return {(int)(row / per) * p.passes + group / p.team, in % p.R, group % p.team};
   } else {
-    return {(int)(row / p.R), row % p.R};
+    return {(int)(row / p.R), row % p.R, 0};
   }
 }
 template <bool TREE>
 __device__ __forceinline__ int plan_seq(const AttnParams& p, int b) {
-  return TREE ? b / p.groups : b;
+  return TREE ? b / p.passes : b;
 }
 
 template <int VEC, int WPR, typename OutT, bool TREE = false>
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
   constexpr int kRowsPerCta = kMergeWarps / WPR;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = warp / WPR, gt = threadIdx.x - g * 32 * WPR;
-  const int64_t rows = TREE ? (int64_t)(p.B / p.groups) * p.n_q * p.H : (int64_t)p.B * p.R;
+  const int64_t rows = TREE ? (int64_t)(p.B / p.passes) * p.n_q * p.H : (int64_t)p.B * p.R;
   const int64_t row0 = (int64_t)blockIdx.x * kRowsPerCta;
   // the cost axis: every sequence as kUnitCost units, then its blocks (none if empty);
   // its length, and the units before each row group's sequence
@@ -250,7 +251,8 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
   const int chunk = blockIdx.y;
   static_assert(kRowsPerCta <= 2, "row groups a CTA");
   const int b = (g == 0) ? bg[0] : bg[kRowsPerCta - 1];  // (no indexing of a local array)
-  const int64_t r = plan_row<TREE>(p, row).r;
+  const PlanRow at = plan_row<TREE>(p, row);
+  const int64_t r = at.r;
   const int num_blocks = plan_blocks(p, plan_seq<TREE>(p, b));
   OutT* out_row;
   if constexpr (sizeof(OutT) == 4)
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
     if (gt == 0 && chunk == 0 && lse_out) *lse_out = -INFINITY;
     return;
   }
-  const int64_t n = p.num_ctas;
+  const int64_t n = TREE ? p.num_ctas / p.team : p.num_ctas;
   const int64_t first = pre + kUnitCost;  // the sequence's first block
   // pieces: one per CTA range the sequence's blocks overlap (with fewer blocks than CTAs
   // every range holds at most one block)
@@ -274,14 +276,135 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
   // piece 0 takes the second slot of its CTA when that CTA's range began before this
   // sequence's span (in an earlier sequence); every later piece begins its CTA's range
   const int64_t first_odd = (range_lo(c0, total, n) < first - kUnitCost) ? 1 : 0;
+  auto cta_of = [&](int64_t c) -> int64_t { return TREE ? c * p.team + at.member : c; };
   auto slot_of = [&](int i) -> int64_t {
-    if (i == 0) return 2 * c0 + first_odd;
-    return 2 * ((total >= n) ? c0 + i : range_of(first + i, total, n));
+    if (i == 0) return 2 * cta_of(c0) + first_odd;
+    return 2 * cta_of((total >= n) ? c0 + i : range_of(first + i, total, n));
   };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   merge_row_chunk<VEC, WPR, OutT>(p.part_out, p.part_lse, count, slot_of, r, p.R, chunk, out_row,
                                   lse_out);
+}
+
+// Tree verify, when there are rows enough to fill the GPU: a CTA takes eight rows of one group of
+// a sequence's nodes, a warp a row. The rows of a group share their pieces, so the plan is looked
+// up once for the eight, and a warp moves whole 2 KB rows of partials (a lane 16 values).
+// merge_split_kernel, two rows a CTA, looked it up four times as often: 73 us where this takes
+// 12 us (12,288 rows, most of them in two or three pieces). Bound: one round of dependent L2
+// loads a CTA, then the partials' bytes through L2.
+constexpr int kTreeMergePieces = 2;  // pieces a warp loads at once
+__global__ void __launch_bounds__(kMergeThreads) merge_tree_kernel(AttnParams p, int chunks) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunk = blockIdx.x % chunks;            // eight rows of the group
+  const int group = blockIdx.x / chunks % (p.team * p.passes);
+  const int seq = blockIdx.x / chunks / (p.team * p.passes);
+  const int b = seq * p.passes + group / p.team, member = group % p.team;
+  const int r = chunk * kMergeWarps + warp;         // row of the group
+  long long tot = 0, before = 0;
+  for (int x = threadIdx.x; x < p.B; x += kMergeThreads) {
+    const int nb = plan_blocks(p, x / p.passes);
+    const long long cost = nb > 0 ? nb + kUnitCost : 0;
+    tot += cost;
+    if (x < b) before += cost;
+  }
+  __shared__ long long s_red[kMergeWarps][2];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (lane == 0) {
+    s_red[warp][0] = tot;
+    s_red[warp][1] = before;
+  }
+  __syncthreads();
+  long long total = 0, pre = 0;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    total += s_red[w][0];
+    pre += s_red[w][1];
+  }
+  const int node0 = group * p.group_nodes;
+  if (r >= min(p.group_nodes, p.n_q - node0) * p.H) return;
+  const int64_t row = ((int64_t)seq * p.n_q + node0) * p.H + r;
+  uint4* out = reinterpret_cast<uint4*>(p.out + row * kDV + lane * 16);
+  const int num_blocks = plan_blocks(p, seq);
+  if (num_blocks == 0) {  // no unit of the attention kernel touches these rows
+    out[0] = out[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0 && p.lse) p.lse[row] = -INFINITY;
+    return;
+  }
+  // the pieces and their slots, as in merge_split_kernel
+  const int64_t n = p.num_ctas / p.team;
+  const int64_t first = pre + kUnitCost;
+  const int64_t c0 = range_of(first, total, n);
+  const int count = (total >= n) ? (int)(range_of(first + num_blocks - 1, total, n) - c0 + 1)
+                                 : num_blocks;
+  if (count == 1) return;  // the attention kernel writes this row itself
+  const int64_t first_odd = (range_lo(c0, total, n) < first - kUnitCost) ? 1 : 0;
+  auto at_of = [&](int i) -> int64_t {
+    const int64_t c = (i == 0 || total >= n) ? c0 + i : range_of(first + i, total, n);
+    return (2 * (c * p.team + member) + (i == 0 ? first_odd : 0)) * p.part_rows + r;
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  float lse_of = lane < count ? __ldg(p.part_lse + at_of(lane)) : -INFINITY;
+  float4 v[kTreeMergePieces][4];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kTreeMergePieces; ++k)
+      if (i0 + k < count) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_out + at_of(i0 + k) * kDV + lane * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = __ldg(src + e);
+      }
+  };
+  load(0);
+  float m = lse_of;
+  for (int i = lane + 32; i < count; i += 32) m = fmaxf(m, __ldg(p.part_lse + at_of(i)));
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (m == -INFINITY) {  // no piece saw a key
+    out[0] = out[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0 && p.lse) p.lse[row] = -INFINITY;
+    return;
+  }
+  float sum = expf(lse_of - m);
+  for (int i = lane + 32; i < count; i += 32) sum += expf(__ldg(p.part_lse + at_of(i)) - m);
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float lse = m + logf(sum);
+  float acc[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  for (int i0 = 0;;) {
+#pragma unroll
+    for (int k = 0; k < kTreeMergePieces; ++k) {
+      const int i = i0 + k;
+      if (i >= count) break;
+      const float l = i < 32 ? __shfl_sync(0xffffffffu, lse_of, i) : __ldg(p.part_lse + at_of(i));
+      if (l == -INFINITY) continue;  // an empty piece's data was never written
+      const float w = expf(l - lse);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[4 * e] += w * v[k][e].x;
+        acc[4 * e + 1] += w * v[k][e].y;
+        acc[4 * e + 2] += w * v[k][e].z;
+        acc[4 * e + 3] += w * v[k][e].w;
+      }
+    }
+    i0 += kTreeMergePieces;
+    if (i0 >= count) break;
+    load(i0);
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&t);
+  }
+  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (lane == 0 && p.lse) p.lse[row] = lse;
 }
 
 // Prefill units of an incomplete last round, each run as two halves along the keys: split
@@ -363,10 +486,7 @@ cudaError_t launch_merge(const AttnParams& p, cudaStream_t s) {
 cudaError_t launch_merge_tree(const AttnParams& p, int sequences, cudaStream_t s) {
   const int64_t rows = (int64_t)sequences * p.n_q * p.H;
   const int vec = merge_vec(rows, p.num_ctas);
-  const bool two_rows = vec == 16 && p.num_ctas <= 8 * p.B;  // as launch_merge
-  const int64_t per = two_rows ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((rows + per - 1) / per), kDV / (32 * vec));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr;
@@ -374,7 +494,14 @@ cudaError_t launch_merge_tree(const AttnParams& p, int sequences, cudaStream_t s
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (two_rows) return cudaLaunchKernelEx(&cfg, merge_split_kernel<16, 4, uint16_t, true>, p);
+  // (a warp a row takes its pieces two at a time: with more than eight or so of them, eight warps
+  // a row; 192 rows of 38 pieces: 22 us against 8 us)
+  if (vec == 16 && p.num_ctas / p.team <= 8 * p.B) {
+    const int chunks = (p.R + kMergeWarps - 1) / kMergeWarps;
+    cfg.gridDim = dim3((unsigned)sequences * p.team * p.passes * chunks);
+    return cudaLaunchKernelEx(&cfg, merge_tree_kernel, p, chunks);
+  }
+  cfg.gridDim = dim3((unsigned)rows, kDV / (32 * vec));
   if (vec == 16) return cudaLaunchKernelEx(&cfg, merge_split_kernel<16, kMergeWarps, uint16_t, true>, p);
   if (vec == 4) return cudaLaunchKernelEx(&cfg, merge_split_kernel<4, kMergeWarps, uint16_t, true>, p);
   return cudaLaunchKernelEx(&cfg, merge_split_kernel<1, kMergeWarps, uint16_t, true>, p);

@@ -96,13 +96,17 @@ def test_long_and_batched(B, H, n, lens):
 
 @pytest.mark.parametrize("n", [1, 2, 3, 4])
 def test_chain_is_verify(n):
-    """A chain's masks give bit for bit what mla_verify gives (12 heads: up to 48 rows)."""
+    """A chain's masks give what mla_verify gives: the same kernel and split (12 heads: up to 48
+    rows), apart from when a row's running max moves. Both are within 2^-8 of the same row's
+    exact value by bfloat16's rounding alone, so they may differ by one step of it."""
     inp = W.make_inputs("chain", [900, 4100, 64, 20000], H=12, n_q=n, seed=n)
     rows = [[(2 << j) - 1 for j in range(n)]] * 4
     out, lse = run(inp, rows)
     kv = mla.KVCache.from_inputs(inp, DEV)
     want, want_lse = mla.mla_verify(kv, inp.q.to(DEV), inp.sm_scale)
-    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    a, b = out.double(), want.double()
+    assert torch.all((a - b).abs() <= 2.0 ** -7 * torch.maximum(a.abs(), b.abs()) + 1e-4)
+    assert torch.all((lse - want_lse).abs() <= 2e-6 * (1 + want_lse.abs()))
 
 
 def test_masks_of_any_kind():
