@@ -41,6 +41,10 @@ EXPORTS = ("mla_workspace_size", "mla_decode", "mla_verify", "mla_prefill", "mla
            "mla_cache_gather", "mla_verify_tree", "mla_accept_drafts")
 
 
+_U8, _I32, _I64, _F32, _BF16 = (torch.uint8, torch.int32, torch.int64, torch.float32,
+                                torch.bfloat16)
+
+
 class MlaError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -142,16 +146,15 @@ class KVCache:
     kv_scale: float
 
     def c_struct(self) -> mla_kv_t:
-        for name in ("pool", "page_table", "seq_lens"):
-            t = getattr(self, name)
+        pool, table, lens = self.pool, self.page_table, self.seq_lens
+        for name, t in (("pool", pool), ("page_table", table), ("seq_lens", lens)):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"KVCache.{name} must be a contiguous CUDA tensor")
-        if self.pool.dtype != torch.uint8 or self.page_table.dtype != torch.int32 or \
-                self.seq_lens.dtype != torch.int32:
+        if pool.dtype is not _U8 or table.dtype is not _I32 or lens.dtype is not _I32:
             raise TypeError("KVCache dtypes: pool uint8, page_table int32, seq_lens int32")
-        return mla_kv_t(self.pool.data_ptr(), self.pool.shape[0], self.pool.shape[1],
-                        self.page_table.data_ptr(), self.page_table.shape[1],
-                        self.seq_lens.data_ptr(), float(self.kv_scale))
+        pages, size, _ = pool.shape
+        return mla_kv_t(pool.data_ptr(), pages, size, table.data_ptr(), table.shape[1],
+                        lens.data_ptr(), self.kv_scale)
 
     @staticmethod
     def from_inputs(inp, device="cuda") -> "KVCache":
@@ -348,22 +351,23 @@ def _on(dev: torch.device, stream) -> int:
     the library launches on the current device)."""
     if stream is not None:
         return _stream(stream)
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but cuda:{torch.cuda.current_device()} is the current "
-                         "device (use torch.cuda.device)")
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    index = torch._C._cuda_getDevice()
+    if dev.index != index:
+        raise ValueError(f"tensors on {dev}, but cuda:{index} is the current device "
+                         "(use torch.cuda.device)")
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> int:
     """Pointer of a contiguous tensor of the given type, shape and device."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _status_ptr(status: Optional[torch.Tensor], dev: torch.device) -> Optional[int]:
-    return None if status is None else _dense(status, "status", torch.int32, (1,), dev)
+    return None if status is None else _dense(status, "status", _I32, (1,), dev)
 
 
 def mla_rope_init(base: float = 10000.0, factor: float = 1.0, original_positions: int = 0,
@@ -373,35 +377,36 @@ def mla_rope_init(base: float = 10000.0, factor: float = 1.0, original_positions
     `factor` times: linearly (original_positions = 0) or by YaRN. Kept by the caller and
     handed to mla_rope and mla_cache_append_rope."""
     rope = mla_rope_t()
-    _check("mla_rope_init", library().mla_rope_init(ctypes.byref(rope), base, factor, original_positions,
-                                               beta_fast, beta_slow, amplitude, int(interleaved)))
+    _check("mla_rope_init", library().mla_rope_init(rope, base, factor, original_positions, beta_fast,
+                                               beta_slow, amplitude, int(interleaved)))
     return rope
 
 
-def _rope_part(t: torch.Tensor, name: str, shape) -> None:
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape != shape or not t.is_cuda or \
-            t.stride(2) != 1:
-        raise ValueError(f"{name} must be a bfloat16 CUDA tensor [n, H, 64] (any token and head "
-                         "strides, the 64 RoPE dims contiguous)")
+def _rope_part(t: torch.Tensor, name: str):
+    """Shape and strides of a view of the RoPE dims."""
+    if t.dtype is _BF16 and t.dim() == 3 and t.is_cuda:
+        n, H, width = t.shape
+        st, sh, sd = t.stride()
+        if width == MLA_ROPE and sd == 1:
+            return n, H, st, sh
+    raise ValueError(f"{name} must be a bfloat16 CUDA tensor [n, H, 64] (any token and head "
+                     "strides, the 64 RoPE dims contiguous)")
 
 
 def mla_rope(rope: mla_rope_t, x: torch.Tensor, positions: torch.Tensor, out=None,
              stream=None) -> torch.Tensor:
     """Rotate x [n, H, 64] bf16 (a view of the RoPE dims, e.g. q[..., 512:] or q_mha[..., 128:])
     to positions int64 [n]. `out` may be another such view, or x itself (in place)."""
-    _rope_part(x, "x", (*x.shape[:2], MLA_ROPE))
-    n, H = x.shape[0], x.shape[1]
+    n, H, xt, xh = _rope_part(x, "x")
     dev = x.device
     if out is None:
-        out = torch.empty(n, H, MLA_ROPE, dtype=torch.bfloat16, device=dev)
-    else:
-        _rope_part(out, "out", x.shape)
-        if out.device != dev or (n > 1 and out.stride(0) == 0) or (H > 1 and out.stride(1) == 0):
-            raise ValueError("out must be on x's device, every element a place of its own")
+        out = torch.empty((n, H, MLA_ROPE), dtype=_BF16, device=dev)
+    m, G, ot, oh = _rope_part(out, "out")
+    if m != n or G != H or out.device != dev or (n > 1 and ot == 0) or (H > 1 and oh == 0):
+        raise ValueError("out must have x's shape and device, and a place of its own for every element")
     _check("mla_rope", library().mla_rope(
-        ctypes.byref(rope), x.data_ptr(), x.stride(0), x.stride(1),
-        _dense(positions, "positions", torch.int64, (n,), dev), n, H, out.data_ptr(), out.stride(0),
-        out.stride(1), _on(dev, stream)))
+        rope, x.data_ptr(), xt, xh, _dense(positions, "positions", _I64, (n,), dev), n, H,
+        out.data_ptr(), ot, oh, _on(dev, stream)))
     return out
 
 
@@ -413,22 +418,22 @@ def mla_cache_append_rope(pool: torch.Tensor, x: torch.Tensor, slots: torch.Tens
     latent is normalised by its root mean square and weighted with norm_weight [512] bf16
     (None: as it is), the 64 RoPE dims are turned to positions int64 [n] (rope None: as they
     are), and both are quantised in one pass. x may be a slice of a wider projection's rows."""
-    if pool.dtype is not torch.uint8 or pool.dim() != 3 or pool.shape[2] != MLA_D or \
-            not pool.is_contiguous() or not pool.is_cuda:
+    if pool.dtype is not _U8 or pool.dim() != 3 or not pool.is_contiguous() or not pool.is_cuda or \
+            pool.shape[2] != MLA_D:
         raise ValueError("pool must be a contiguous uint8 CUDA tensor [num_pages, page_size, 576]")
+    pages, size, _ = pool.shape
     dev = pool.device
-    if x.dtype is not torch.bfloat16 or x.dim() != 2 or x.shape[1] != MLA_D or x.stride(1) != 1 or \
+    if x.dtype is not _BF16 or x.dim() != 2 or x.shape[1] != MLA_D or x.stride(1) != 1 or \
             x.device != dev:
         raise ValueError("x must be a bfloat16 tensor [n, 576] on the pool's device, its rows contiguous")
     if (rope is None) != (positions is None):
         raise ValueError("give rope and positions together, or neither")
     n = x.shape[0]
     _check("mla_cache_append_rope", library().mla_cache_append_rope(
-        pool.data_ptr(), pool.shape[0], pool.shape[1], x.data_ptr(), x.stride(0) if n > 1 else MLA_D,
-        _dense(slots, "slots", torch.int64, (n,), dev), n, kv_scale,
-        None if norm_weight is None else _dense(norm_weight, "norm_weight", torch.bfloat16, (MLA_DV,), dev),
-        eps, None if rope is None else ctypes.byref(rope),
-        None if positions is None else _dense(positions, "positions", torch.int64, (n,), dev),
+        pool.data_ptr(), pages, size, x.data_ptr(), x.stride(0) if n > 1 else MLA_D,
+        _dense(slots, "slots", _I64, (n,), dev), n, kv_scale,
+        None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, (MLA_DV,), dev),
+        eps, rope, None if positions is None else _dense(positions, "positions", _I64, (n,), dev),
         _status_ptr(status, dev), _on(dev, stream)))
 
 
@@ -444,13 +449,12 @@ def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optiona
     if B < 0 or B > kv.seq_lens.shape[0] or B > kv.page_table.shape[0]:
         raise ValueError("cu_rows must have an entry more than there are sequences")
     if out is None:
-        out = torch.empty(n, MLA_D, dtype=dtype, device=dev)
-    if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
-        raise ValueError("out must be bfloat16 or float32")
+        out = torch.empty((n, MLA_D), dtype=dtype, device=dev)
+    f32 = out.dtype is _F32
     _check("mla_cache_gather", library().mla_cache_gather(
-        ctypes.byref(c), B, None if starts is None else _dense(starts, "starts", torch.int32, (B,), dev),
-        _dense(cu_rows, "cu_rows", torch.int64, (B + 1,), dev), n,
-        _dense(out, "out", out.dtype, (n, MLA_D), dev), out.dtype is torch.float32,
+        c, B, None if starts is None else _dense(starts, "starts", _I32, (B,), dev),
+        _dense(cu_rows, "cu_rows", _I64, (B + 1,), dev), n,
+        _dense(out, "out", _F32 if f32 else _BF16, (n, MLA_D), dev), f32,
         _status_ptr(status, dev), _on(dev, stream)))
     return out
 
@@ -460,19 +464,19 @@ def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_sc
     """q [B, n, H, 576] bf16 of a tree's n <= 64 nodes -> (out [B, n, H, 512] bf16, lse [B, n, H]
     fp32). Every node sees the prefix and the nodes whose bit its tree_mask (int64 [B, n]) sets."""
     _q_check(q, 4)
-    B, n, H = q.shape[0], q.shape[1], q.shape[2]
+    B, n, H, _ = q.shape
     dev = q.device
-    out = torch.empty(B, n, H, MLA_DV, dtype=torch.bfloat16, device=dev) if out is None else out
-    lse = torch.empty(B, n, H, dtype=torch.float32, device=dev) if lse is None else lse
+    out = torch.empty((B, n, H, MLA_DV), dtype=_BF16, device=dev) if out is None else out
+    lse = torch.empty((B, n, H), dtype=_F32, device=dev) if lse is None else lse
     ws = workspace(MLA_OP_VERIFY_TREE, B, H, n, dev) if ws is None else ws
     if kv.seq_lens.shape[0] < B or kv.page_table.shape[0] < B or kv.pool.device != dev:
         raise ValueError("kv must describe q's sequences, on q's device")
-    c = kv.c_struct()
+    if not ws.is_contiguous() or ws.dtype is not _U8 or ws.device != dev:
+        raise ValueError("ws must be a contiguous uint8 tensor on q's device")
     _check("mla_verify_tree", library().mla_verify_tree(
-        ctypes.byref(c), q.data_ptr(), B, n, H, sm_scale,
-        _dense(tree_mask, "tree_mask", torch.int64, (B, n), dev),
-        _dense(out, "out", torch.bfloat16, (B, n, H, MLA_DV), dev),
-        _dense(lse, "lse", torch.float32, (B, n, H), dev), ws.data_ptr(), ws.numel(), _on(dev, stream)))
+        kv.c_struct(), q.data_ptr(), B, n, H, sm_scale,
+        _dense(tree_mask, "tree_mask", _I64, (B, n), dev), _dense(out, "out", _BF16, (B, n, H, MLA_DV), dev),
+        _dense(lse, "lse", _F32, (B, n, H), dev), ws.data_ptr(), ws.numel(), _on(dev, stream)))
     return out, lse
 
 
@@ -488,15 +492,15 @@ def mla_accept_drafts(target_probs: torch.Tensor, tokens: torch.Tensor, uniforms
         raise ValueError("target_probs must be a CUDA tensor [B, n, V]")
     B, n, V = target_probs.shape
     dev = target_probs.device
-    out_tokens = torch.empty(B, n, dtype=torch.int32, device=dev)
-    path = torch.empty(B, n, dtype=torch.int32, device=dev)
-    num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+    _dense(tokens, "tokens", _I32, (B, n), dev)
+    out_tokens = torch.empty_like(tokens)
+    path = torch.empty_like(tokens)
+    num_accepted = torch.empty((B,), dtype=_I32, device=dev)
     _check("mla_accept_drafts", library().mla_accept_drafts(
-        _dense(target_probs, "target_probs", torch.float32, (B, n, V), dev),
-        _dense(tokens, "tokens", torch.int32, (B, n), dev),
-        None if parents is None else _dense(parents, "parents", torch.int32, (B, n), dev),
-        None if draft_probs is None else _dense(draft_probs, "draft_probs", torch.float32, (B, n - 1, V), dev),
-        _dense(uniforms, "uniforms", torch.float32, (B, n + 1), dev), B, n, V, out_tokens.data_ptr(),
+        _dense(target_probs, "target_probs", _F32, (B, n, V), dev), tokens.data_ptr(),
+        None if parents is None else _dense(parents, "parents", _I32, (B, n), dev),
+        None if draft_probs is None else _dense(draft_probs, "draft_probs", _F32, (B, n - 1, V), dev),
+        _dense(uniforms, "uniforms", _F32, (B, n + 1), dev), B, n, V, out_tokens.data_ptr(),
         path.data_ptr(), num_accepted.data_ptr(), _on(dev, stream)))
     return out_tokens, path, num_accepted
 

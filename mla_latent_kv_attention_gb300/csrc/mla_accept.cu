@@ -16,14 +16,21 @@
 // together is less than 2^-25 of a row: a float32 uniform cannot tell. The threshold
 // floor(u * total), u in steps of 2^-31, is a 64-bit high product.
 //
-// Layout. A cluster of CTAs takes one sequence. Each CTA first walks the nodes by itself (all
-// nodes' entries are fetched at once, one thread a node: two dependent loads in all), which
-// names the row to draw from. Then warp w of CTA r sums the weights of its own contiguous span
-// of the row, 128 a step; the CTAs exchange their totals through distributed shared memory (one
-// cluster barrier), the CTA that holds the threshold finds the warp from its warps' totals, and
-// that warp the step, the lane and the token. One pass over one row (two with draft
-// probabilities) is all that is read of the vocabulary. Bound: latency (two loads to walk, one
-// round over the row, one barrier), then HBM.
+// Arithmetic. A float32 weight w becomes its whole number in two float32 additions: w + 12
+// rounds w to a multiple of 2^-20 (the unit of [8, 16)), whose count is the difference of the bit
+// patterns, and what is left, at most 2^-21, added to 1.5 * 2^-20 is rounded to 2^-43 the same
+// way. The pair of counts is the weight rounded to nearest even, because the first is a whole
+// multiple of the second's unit. A conversion instruction to 64 bits runs at a small fraction of
+// the rate (it took 14 us of the 32 us of 64 sequences of 129,280 tokens).
+//
+// Layout. A cluster of CTAs takes one sequence. Warp 0 of each CTA walks the nodes by itself (a
+// lane two nodes, all nodes' entries fetched at once: two dependent loads in all), which names
+// the row to draw from. Then warp w of CTA r sums the weights of its own contiguous span of the
+// row, 128 a step; the CTAs exchange their totals through distributed shared memory (one cluster
+// barrier), the CTA that holds the threshold finds the warp from its warps' totals, and that
+// warp the step, the lane and the token. One pass over one row (two with draft probabilities) is
+// all that is read of the vocabulary. Bound: latency (two loads to walk, one round over the row,
+// one barrier), then HBM.
 #include <cuda_runtime.h>
 
 #include "mla_internal.cuh"
@@ -36,23 +43,33 @@ constexpr int kAcThreads = 512;
 constexpr int kAcWarps = kAcThreads / 32;
 constexpr int kAcCluster = 8;
 constexpr int kAcStep = 128;  // entries a warp takes a step
-constexpr int kAcUnroll = 8;  // steps in flight
 constexpr int kNone = -1;
 
 struct AcSmem {
   int tok[MLA_MAX_TREE], par[MLA_MAX_TREE];  // par = kNone: node is no draft
   long long share[MLA_MAX_TREE];             // its width on [0, 1) (drafts without probabilities)
-  unsigned taken[2];                         // one bit a node: accepted if its parent is
-  int path[MLA_MAX_TREE];
+  int kid[MLA_MAX_TREE];                     // tokens of the last node's children, each once
+  int kids;
   int last, count;                           // last node accepted, drafts accepted
+  int more;                                  // 1: a draft after `last` was refused
   unsigned long long cta_sum[kAcCluster];    // every CTA's total (each CTA writes all copies)
   unsigned long long warp_sum[kAcWarps];
 };
 
-// A weight as a whole multiple of 2^-43; NaN and negative weights are 0, larger ones than 1 are 1.
-__device__ __forceinline__ long long weight_of(float w) {
-  return __float2ll_rn(fminf(fmaxf(w, 0.f), 1.f) * 0x1p43f);
+// A weight as whole multiples of 2^-20 (hi) and 2^-43 (lo, signed) that add up to it; NaN and
+// negative weights are 0, larger ones than 1 are 1.
+struct Weight {
+  int hi, lo;
+};
+__device__ __forceinline__ Weight split_weight(float w) {
+  w = fminf(fmaxf(w, 0.f), 1.f);
+  const float coarse = __fadd_rn(w, 12.f);
+  const float rest = __fsub_rn(w, __fsub_rn(coarse, 12.f));  // both exact
+  const float fine = __fadd_rn(rest, 0x1.8p-20f);
+  return {__float_as_int(coarse) - __float_as_int(12.f), __float_as_int(fine) - __float_as_int(0x1.8p-20f)};
 }
+__device__ __forceinline__ long long whole_weight(Weight w) { return ((long long)w.hi << 23) + w.lo; }
+
 // A uniform number in steps of 2^-BITS, in [0, 2^BITS).
 template <int BITS>
 __device__ __forceinline__ long long uniform_of(float u) {
@@ -67,102 +84,145 @@ __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v)
   return v;
 }
 
-// VEC: a lane's four entries of a step are one 16-byte vector (rows 16-byte aligned, V a
-// multiple of four); otherwise they lie 32 apart, so that single loads stay coalesced.
-template <bool VEC>
+// The walk (one warp; lane l holds nodes l and l + 32): which drafts are accepted, what the draw
+// starts from.
+template <bool DRAFT>
+__device__ void walk(const AcceptArgs& a, AcSmem& s, int b, bool write) {
+  const int lane = threadIdx.x & 31, n = a.n;
+  const float* target = a.target + (int64_t)b * n * a.V;
+  const float* u = a.uniforms + (int64_t)b * (n + 1);
+  int tok[2], par[2];
+  float pt[2], qt[2], up[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int t = lane + 32 * h;
+    tok[h] = par[h] = kNone;
+    if (t >= 1 && t < n) {
+      tok[h] = a.tokens[(int64_t)b * n + t];
+      par[h] = a.parents ? a.parents[(int64_t)b * n + t] : t - 1;
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int t = lane + 32 * h;
+    if (tok[h] < 0 || tok[h] >= a.V || par[h] < 0 || par[h] >= t) par[h] = kNone;
+    pt[h] = qt[h] = up[h] = 0.f;
+    if (par[h] != kNone) {
+      pt[h] = target[(int64_t)par[h] * a.V + tok[h]];
+      if (DRAFT) qt[h] = a.draft[((int64_t)b * (n - 1) + t - 1) * a.V + tok[h]];
+      up[h] = u[par[h]];
+    }
+    s.tok[t] = tok[h];
+    s.par[t] = par[h];
+  }
+  __syncwarp();
+  bool first[2] = {par[0] != kNone, par[1] != kNone};  // no sibling before it has its token
+  if (!DRAFT && a.parents) {
+    for (int i = 1; i < n; ++i) {
+      const int pi = s.par[i], ti = s.tok[i];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (i < lane + 32 * h && pi == par[h] && ti == tok[h]) first[h] = false;
+    }
+  }
+  bool taken[2];
+  if (DRAFT) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) taken[h] = par[h] != kNone && __fmul_rn(up[h], qt[h]) < pt[h];
+  } else {
+    long long below[2] = {0, 0}, share[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      share[h] = first[h] ? whole_weight(split_weight(pt[h])) : 0;
+      s.share[lane + 32 * h] = share[h];
+    }
+    __syncwarp();
+    if (a.parents) {
+      for (int i = 1; i < n; ++i) {
+        const int pi = s.par[i];
+        const long long si = s.share[i];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (i < lane + 32 * h && pi == par[h]) below[h] += si;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const long long mark = uniform_of<43>(up[h]);
+      taken[h] = first[h] && mark >= below[h] && mark < below[h] + share[h];
+    }
+  }
+  // a child's index is above its parent's, and of a node's children at most one is taken: one
+  // pass upwards over the taken nodes follows the chain (every lane the same pass)
+  unsigned long long bits = __ballot_sync(0xffffffffu, taken[0]) |
+                            (unsigned long long)__ballot_sync(0xffffffffu, taken[1]) << 32;
+  unsigned long long kept = 1;  // nodes of the chain
+  int last = 0;
+  while (bits) {
+    const int j = __ffsll((long long)bits) - 1;
+    bits &= bits - 1;
+    if (s.par[j] == last) {
+      last = j;
+      kept |= 1ull << j;
+    }
+  }
+  const int count = __popcll(kept) - 1;
+  // the refused children's tokens, each once
+  int at = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const bool kid = first[h] && par[h] == last;
+    const unsigned m = __ballot_sync(0xffffffffu, kid);
+    if (kid) s.kid[at + __popc(m & ((1u << lane) - 1))] = tok[h];
+    at += __popc(m);
+  }
+  if (lane == 0) {
+    s.kids = at;
+    s.last = last;
+    s.count = count;
+    s.more = DRAFT && at > 0;
+  }
+  if (write) {
+    // (the drawn token's own place is written by the CTA that draws it)
+    int32_t* path = a.path + (int64_t)b * n;
+    int32_t* out = a.out_tokens + (int64_t)b * n;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = lane + 32 * h;
+      if (t < n && (kept >> t & 1)) {  // its place on the chain
+        const int k = __popcll(kept & ((1ull << t) - 1));
+        path[k] = t;
+        if (k > 0) out[k - 1] = tok[h];
+      }
+      if (t < n && t > count) path[t] = out[t] = -1;
+    }
+    if (lane == 0) a.num_accepted[b] = count;
+  }
+}
+
+// DRAFT: drafts come with their probabilities (a chain). VEC: a lane's four entries of a step are
+// one 16-byte vector (rows 16-byte aligned, V a multiple of four); otherwise they lie 32 apart, so
+// that single loads stay coalesced.
+template <bool DRAFT, bool VEC>
 __global__ void __launch_bounds__(kAcThreads, 2) accept_kernel(const __grid_constant__ AcceptArgs a) {
+  // steps in flight: 16-byte loads of one row or of two, eight a lane
+  constexpr int kSteps = DRAFT ? 4 : 8;
   __shared__ AcSmem s;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const unsigned rank = sm100::cluster_ctarank();
   const int ctas = gridDim.x;  // CTAs of the cluster
   const int b = blockIdx.y, n = a.n, V = a.V;
-  const float* target = a.target + (int64_t)b * n * V;
-  const float* draft = a.draft ? a.draft + (int64_t)b * (n - 1) * V : nullptr;
-  const float* u = a.uniforms + (int64_t)b * (n + 1);
   // the other CTAs' shared memory may be written once they all run: arrive here, wait below
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-
-  // ---- the walk
-  bool drafted = false, taken = false;
-  int par = kNone, tok = 0;
-  float pt = 0.f, qt = 0.f, up = 0.f;
-  if (t < MLA_MAX_TREE) {
-    if (t >= 1 && t < n) {
-      tok = a.tokens[(int64_t)b * n + t];
-      par = a.parents ? a.parents[(int64_t)b * n + t] : t - 1;
-      drafted = tok >= 0 && tok < V && par >= 0 && par < t;
-    }
-    if (drafted) {
-      pt = target[(int64_t)par * V + tok];
-      if (draft) qt = draft[(int64_t)(t - 1) * V + tok];
-      up = u[par];
-    } else {
-      par = kNone;
-    }
-    s.tok[t] = tok;
-    s.par[t] = par;
-    s.share[t] = weight_of(pt);
-  }
+  if (warp == 0) walk<DRAFT>(a, s, b, rank == 0);
   __syncthreads();
-  if (t < MLA_MAX_TREE) {
-    if (!draft) {
-      // a sibling before this one with the same token leaves it nothing
-      for (int i = 1; i < t && drafted; ++i)
-        if (s.par[i] == par && s.tok[i] == tok) drafted = false;
-    }
-  }
-  __syncthreads();
-  if (t < MLA_MAX_TREE && !draft && !drafted) s.share[t] = 0;
-  __syncthreads();
-  if (t < MLA_MAX_TREE) {
-    if (drafted) {
-      if (draft) {
-        taken = __fmul_rn(up, qt) < pt;
-      } else {
-        long long below = 0;
-        for (int i = 1; i < t; ++i)
-          if (s.par[i] == par) below += s.share[i];
-        const long long mark = uniform_of<43>(up);
-        taken = mark >= below && mark < below + s.share[t];
-      }
-    }
-    const unsigned bits = __ballot_sync(0xffffffffu, taken);
-    if (lane == 0) s.taken[warp] = bits;
-  }
-  __syncthreads();
-  if (t == 0) {
-    // a child's index is above its parent's, and of a node's children at most one is taken:
-    // one pass upwards over the taken nodes follows the chain
-    unsigned long long bits = ((unsigned long long)s.taken[1] << 32) | s.taken[0];
-    int at = 0, k = 0;
-    s.path[0] = 0;
-    while (bits) {
-      const int j = __ffsll((long long)bits) - 1;
-      bits &= bits - 1;
-      if (s.par[j] == at) {
-        at = j;
-        s.path[++k] = j;
-      }
-    }
-    s.last = at;
-    s.count = k;
-  }
-  __syncthreads();
-  const int last = s.last, count = s.count;
-  if (rank == 0 && t < n) {
-    // the drawn token's own place is written by the CTA that draws it
-    const int64_t o = (int64_t)b * n + t;
-    a.path[o] = t <= count ? s.path[t] : -1;
-    if (t != count) a.out_tokens[o] = t < count ? s.tok[s.path[t + 1]] : -1;
-    if (t == 0) a.num_accepted[b] = count;
-  }
-
-  // ---- the draw
-  const float* prow = target + (int64_t)last * V;
+  const float* prow = a.target + ((int64_t)b * n + s.last) * V;
   const float* qrow = nullptr;  // the refused draft's probabilities
-  if (draft && last + 1 < n && s.par[last + 1] == last) qrow = draft + (int64_t)last * V;
+  if (DRAFT && s.more) qrow = a.draft + ((int64_t)b * (n - 1) + s.last) * V;
+  int32_t* drawn = a.out_tokens + (int64_t)b * n + s.count;
+
   const int span = (V + ctas * kAcWarps * kAcStep - 1) / (ctas * kAcWarps * kAcStep) * kAcStep;
-  const int w0 = ((int)rank * kAcWarps + warp) * span;  // (at most 2^19 + a span)
+  const int w0 = ((int)rank * kAcWarps + warp) * span;  // (below 2^19 + 2^18)
   const int w1 = min(V, w0 + span);
   auto load4 = [&](const float* row, int at, float (&v)[4]) {
     if constexpr (VEC) {
@@ -176,117 +236,154 @@ __global__ void __launch_bounds__(kAcThreads, 2) accept_kernel(const __grid_cons
   };
   // index of entry e of this lane in the step at `at`
   auto index_of = [&](int at, int e) { return VEC ? at + 4 * lane + e : at + 32 * e + lane; };
-  bool whole = false;  // second round: nothing was left, draw from the target row itself
-  unsigned long long total = 0, mine = 0, before = 0;
-  // weights of the step at `at`, with the refused children's tokens left out
-  auto weigh = [&](int at, const float (&p)[4], const float (&q)[4], long long (&w)[4]) {
+  // the weights of the steps that w [steps][4] has room for
+  auto load = [&](int at, auto& w) {
+    constexpr int K = sizeof(w) / sizeof(w[0]);
+    float q[K][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = weight_of(whole ? p[e] : p[e] - q[e]);
-    if (!draft && !whole)
-      for (int j = last + 1; j < n; ++j)
-        if (s.par[j] == last) {
+    for (int k = 0; k < K; ++k) load4(prow, at + k * kAcStep, w[k]);
+    if (DRAFT && qrow) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (index_of(at, e) == s.tok[j]) w[e] = 0;
-        }
+      for (int k = 0; k < K; ++k) load4(qrow, at + k * kAcStep, q[k]);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[k][e] -= q[k][e];
+    }
   };
+  // children's tokens in this warp's span: left out of the draw (a bit a child)
+  unsigned long long out_of_span = 0;
+  if (!DRAFT)
+    for (int k = 0; k < s.kids; ++k)
+      if (s.kid[k] >= w0 && s.kid[k] < w1) out_of_span |= 1ull << k;
+  unsigned long long total = 0, mine = 0, before = 0;
   __syncwarp();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  for (;;) {
-    unsigned long long sum = 0;
-    for (int at = w0; at < w1; at += kAcUnroll * kAcStep) {
-      float p[kAcUnroll][4], q[kAcUnroll][4];
+  for (int round = 0;; ++round) {
+    int hi = 0, lo = 0;
+    long long sum = 0;
+    for (int at = w0; at < w1; at += kSteps * kAcStep) {
+      float w[kSteps][4];
+      load(at, w);
 #pragma unroll
-      for (int k = 0; k < kAcUnroll; ++k) {
-        load4(prow, at + k * kAcStep, p[k]);
-        if (qrow)
-          load4(qrow, at + k * kAcStep, q[k]);
-        else
-          q[k][0] = q[k][1] = q[k][2] = q[k][3] = 0.f;
-      }
+      for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-      for (int k = 0; k < kAcUnroll; ++k) {
-        long long w[4];
-        weigh(at + k * kAcStep, p[k], q[k], w);
-        sum += (unsigned long long)(w[0] + w[1] + w[2] + w[3]);
-      }
+        for (int e = 0; e < 4; ++e) {  // (at most 2^7 a lane: 2^27 and 2^29)
+          const Weight x = split_weight(w[k][e]);
+          hi += x.hi;
+          lo += x.lo;
+        }
     }
-    mine = warp_sum_u64(sum);
+    sum = whole_weight({hi, lo});
+    if (lane == 0)
+      for (unsigned long long m = out_of_span; m; m &= m - 1)
+        sum -= whole_weight(split_weight(prow[s.kid[__ffsll((long long)m) - 1]]));
+    mine = warp_sum_u64((unsigned long long)sum);
     if (lane == 0) s.warp_sum[warp] = mine;
     __syncthreads();
-    unsigned long long cta = 0;
-    before = 0;
-    for (int w = 0; w < kAcWarps; ++w) {
-      if (w < warp) before += s.warp_sum[w];
-      cta += s.warp_sum[w];
-    }
+    unsigned long long cta = lane < kAcWarps ? s.warp_sum[lane] : 0;
+    before = warp_sum_u64(lane < warp ? cta : 0);
+    cta = warp_sum_u64(cta);
     if (t < ctas) {
       unsigned* dst = reinterpret_cast<unsigned*>(&s.cta_sum[rank]);
       sm100::st_dsmem_u32(dst, (uint32_t)t, (unsigned)cta);
       sm100::st_dsmem_u32(dst + 1, (uint32_t)t, (unsigned)(cta >> 32));
     }
+    __syncwarp();
     sm100::cluster_sync();  // every CTA holds every total
     total = 0;
     for (int r = 0; r < ctas; ++r) {
       if (r < (int)rank) before += s.cta_sum[r];
       total += s.cta_sum[r];
     }
-    if (total != 0 || whole) break;
-    whole = true;
+    if (total != 0 || round == 1) break;
+    // nothing was left: a second round over the target row itself
     qrow = nullptr;
+    out_of_span = 0;
     sm100::cluster_sync();  // the totals have been read before the second round writes them
   }
   if (total == 0) {
-    if (rank == 0 && t == 0) a.out_tokens[(int64_t)b * n + count] = -1;
+    if (rank == 0 && t == 0) *drawn = -1;
     return;
   }
-  const unsigned long long mark = __umul64hi(total, (unsigned long long)uniform_of<31>(u[n]) << 33);
+  const float un = a.uniforms[(int64_t)b * (n + 1) + n];
+  const unsigned long long mark = __umul64hi(total, (unsigned long long)uniform_of<31>(un) << 33);
   if (mark < before || mark >= before + mine) return;
-  // this warp's span holds the token: find the step, then the entry
+
+  // ---- this warp's span holds the token: find the steps, then the step, then the entry
+  constexpr int kFind = 4;
   unsigned long long left = mark - before;  // weight of the span before the token's end
-  for (int at = w0; at < w1; at += kAcStep) {
-    float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
-    long long w[4];
-    load4(prow, at, p);
-    if (qrow) load4(qrow, at, q);
-    weigh(at, p, q, w);
-    const unsigned long long step = warp_sum_u64((unsigned long long)(w[0] + w[1] + w[2] + w[3]));
-    if (left >= step) {
-      left -= step;
-      continue;
+  for (int at = w0; at < w1; at += kFind * kAcStep) {
+    float w[kFind][4];
+    load(at, w);
+    unsigned long long own[kFind], step[kFind];
+#pragma unroll
+    for (int k = 0; k < kFind; ++k) {
+      for (unsigned long long m = out_of_span; m; m &= m - 1) {
+        const int token = s.kid[__ffsll((long long)m) - 1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (index_of(at + k * kAcStep, e) == token) w[k][e] = 0.f;
+      }
+      long long x = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x += whole_weight(split_weight(w[k][e]));
+      own[k] = step[k] = (unsigned long long)x;
     }
-    // entries in index order: lane by lane (VEC), or the lanes of entry 0, then of entry 1, ...
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < kFind; ++k) step[k] += __shfl_xor_sync(0xffffffffu, step[k], o);
+    // the step that holds the token, and its entries
+    int found = -1;
+    unsigned long long mine_before = left, lane_sum = 0;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kFind; ++k) {
+      if (found < 0) {
+        if (left < step[k]) {
+          found = k;
+          mine_before = left;
+          lane_sum = own[k];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = w[k][e];
+        } else {
+          left -= step[k];
+        }
+      }
+    }
+    if (found < 0) continue;
+    const int base = at + found * kAcStep;
+    int token = 0x7fffffff;
     unsigned long long acc = 0;
-    int found = 0x7fffffff;
-    if constexpr (VEC) {
-      const unsigned long long own = (unsigned long long)(w[0] + w[1] + w[2] + w[3]);
-      unsigned long long incl = own;
+    if constexpr (VEC) {  // entries in index order: lane by lane
+      unsigned long long incl = lane_sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
-      acc = incl - own;
+      acc = incl - lane_sum;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        acc += (unsigned long long)w[e];
-        if (acc > left) found = min(found, index_of(at, e));
+        acc += (unsigned long long)whole_weight(split_weight(x[e]));
+        if (acc > mine_before) token = min(token, index_of(base, e));
       }
-    } else {
+    } else {  // the lanes of entry 0, then of entry 1, ...
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        unsigned long long incl = (unsigned long long)w[e];
+        unsigned long long incl = (unsigned long long)whole_weight(split_weight(x[e]));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += y;
         }
-        if (acc + incl > left) found = min(found, index_of(at, e));
+        if (acc + incl > mine_before) token = min(token, index_of(base, e));
         acc += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    found = __reduce_min_sync(0xffffffffu, found);
-    if (lane == 0) a.out_tokens[(int64_t)b * n + count] = found;
+    token = __reduce_min_sync(0xffffffffu, token);
+    if (lane == 0) *drawn = token;
     return;
   }
 }
@@ -310,8 +407,11 @@ cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return vec ? cudaLaunchKernelEx(&cfg, accept_kernel<true>, a)
-             : cudaLaunchKernelEx(&cfg, accept_kernel<false>, a);
+  if (a.draft)
+    return vec ? cudaLaunchKernelEx(&cfg, accept_kernel<true, true>, a)
+               : cudaLaunchKernelEx(&cfg, accept_kernel<true, false>, a);
+  return vec ? cudaLaunchKernelEx(&cfg, accept_kernel<false, true>, a)
+             : cudaLaunchKernelEx(&cfg, accept_kernel<false, false>, a);
 }
 
 }  // namespace mla
