@@ -73,12 +73,9 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
   for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < a.n; i += nwarps) {
+    // every load of the row at once, its slot among them
     const int64_t slot = a.slots[i];
-    if (slot < 0) continue;  // padding: nothing to write
-    if (slot >= a.pool_rows) {
-      if (lane == 0 && a.status) atomicCAS(a.status, 0u, (unsigned)MLA_ERR_BOUNDS);
-      continue;
-    }
+    const int64_t position = a.positions ? a.positions[i] : 0;
     const uint16_t* row = a.x + i * a.x_stride;
     const uint4* src = reinterpret_cast<const uint4*>(row) + 2 * lane;
     const uint4 v0 = src[0], v1 = src[1];
@@ -87,6 +84,11 @@ __global__ void __launch_bounds__(256)
       pair = *reinterpret_cast<const uint32_t*>(row + kDV + 2 * lane);
     else
       pair = row[kDV + lane] | (uint32_t)row[kDV + MLA_ROPE / 2 + lane] << 16;
+    if (slot < 0) continue;  // padding: nothing to write
+    if (slot >= a.pool_rows) {
+      if (lane == 0 && a.status) atomicCAS(a.status, 0u, (unsigned)MLA_ERR_BOUNDS);
+      continue;
+    }
     const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     float c[16];
 #pragma unroll
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(256)
     }
     float2 pe = make_float2(__uint_as_float(pair << 16), __uint_as_float(pair & 0xFFFF0000u));
     if (a.positions)
-      pe = rope_turn(pe.x, pe.y, rope_cos_sin(rope.turns[lane], a.positions[i], rope.amplitude));
+      pe = rope_turn(pe.x, pe.y, rope_cos_sin(rope.turns[lane], position, rope.amplitude));
     uint32_t code[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)

@@ -246,6 +246,8 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
     total += s_red[w][0];
     pre += s_red[w][1 + g];
   }
+  if (TREE && blockIdx.x + blockIdx.y == 0)  // (as merge_tree_kernel)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row = row0 + g;  // b * R + r
   if (row >= rows) return;
   const int chunk = blockIdx.y;
@@ -325,6 +327,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_tree_kernel(AttnParams p,
     total += s_red[w][0];
     pre += s_red[w][1];
   }
+  // The first CTA waits for the attention grid whatever it has to merge: this grid must not
+  // complete before that one, for the sake of a programmatic dependent that waits for this one.
+  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   const int node0 = group * p.group_nodes;
   if (r >= min(p.group_nodes, p.n_q - node0) * p.H) return;
   const int64_t row = ((int64_t)seq * p.n_q + node0) * p.H + r;
