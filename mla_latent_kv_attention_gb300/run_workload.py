@@ -4,6 +4,7 @@
     python -m mla_latent_kv_attention_gb300.run_workload causal_prefill --T 2048 --iters 3
     python -m mla_latent_kv_attention_gb300.run_workload cache_append --iters 5
     python -m mla_latent_kv_attention_gb300.run_workload top_k_renorm --iters 5
+    python -m mla_latent_kv_attention_gb300.run_workload speculative_step --iters 5
 
 Prints the device status word after the last call. Intended as the command line that
 ncu wraps: every launch it makes is a library launch on the named inputs.
@@ -22,7 +23,7 @@ from mla_latent_kv_attention_gb300 import workloads as W
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("workload", choices=sorted(W.WORKLOADS) + ["cache_append", "top_k_renorm",
-                                                                 "mha_prefill"])
+                                                                 "mha_prefill", "speculative_step"])
     ap.add_argument("--iters", type=int, default=5)
     ap.add_argument("--heads", type=int, default=12, help="long_history_decode only")
     ap.add_argument("--T", type=int, default=8192, help="causal_prefill and mha_prefill only")
@@ -32,6 +33,8 @@ def main(argv=None) -> int:
         return _cache_append(args.iters)
     if args.workload == "mha_prefill":
         return _mha_prefill(args.T, args.iters, args.bf16)
+    if args.workload == "speculative_step":
+        return _speculative_step(args.iters)
     if args.workload == "top_k_renorm":
         return _top_k_renorm(args.iters)
     if args.workload == "long_history_decode":
@@ -91,6 +94,50 @@ def _mha_prefill(T: int, iters: int, bf16: bool = False) -> int:
     torch.cuda.synchronize()
     status = mla.mla_read_status(ws)
     print(f"mha_prefill: {iters} calls, status {mla.STATUS.get(status, status)}")
+    return 0 if status == 0 else 1
+
+
+def _speculative_step(iters: int) -> int:
+    """Eight sequences on a 32,768-position prefix, 16 drafted nodes each (a binary tree): draft
+    rows written (norm, rotation, quantisation), queries rotated, the tree verified, drafts
+    accepted against synthetic target probabilities (129,280 entries a row), the last 512
+    positions of every sequence read back."""
+    B, n, H, V = 8, 16, 12, 129280
+    inp = W.make_inputs("speculative_step", [32768 + n] * B, H=H, n_q=n, seed=0)
+    kv = mla.KVCache.from_inputs(inp, "cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    parents = [-1] + [(j - 1) // 2 for j in range(1, n)]
+    masks, depth = [], []
+    for j, a in enumerate(parents):
+        masks.append((masks[a] if a >= 0 else 0) | 1 << j)
+        depth.append(depth[a] + 1 if a >= 0 else 0)
+    tree_mask = torch.tensor([masks] * B, device="cuda")
+    place = 32768 + torch.arange(n, device="cuda").expand(B, n)
+    positions = (32768 + torch.tensor(depth, device="cuda").expand(B, n)).flatten()
+    slots = (kv.page_table.gather(1, place // 64).long() * 64 + place % 64).flatten()
+    latent = torch.randn(B * n, mla.MLA_D, generator=g, device="cuda").bfloat16()
+    weight = torch.ones(mla.MLA_DV, dtype=torch.bfloat16, device="cuda")
+    q = inp.q.cuda()
+    q_rope = torch.randn(B * n, H, mla.MLA_ROPE, generator=g, device="cuda").bfloat16()
+    probs = torch.softmax(5 * torch.randn(B, n, V, generator=g, device="cuda"), -1)
+    tokens = torch.randint(0, V, (B, n), generator=g, device="cuda", dtype=torch.int32)
+    uniforms = torch.rand(B, n + 1, generator=g, device="cuda")
+    parents = torch.tensor([parents] * B, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, device="cuda") * 512
+    starts = torch.full((B,), 32768 + n - 512, dtype=torch.int32, device="cuda")
+    rope = mla.mla_rope_init(factor=40.0, original_positions=4096)
+    ws = mla.workspace(mla.MLA_OP_VERIFY_TREE, B, H, n)
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(iters):
+        mla.mla_cache_append_rope(kv.pool, latent, slots, kv.kv_scale, rope, positions,
+                                  norm_weight=weight, status=word)
+        mla.mla_rope(rope, q_rope, positions, out=q.view(B * n, H, mla.MLA_D)[..., mla.MLA_DV:])
+        mla.mla_verify_tree(kv, q, tree_mask, inp.sm_scale, ws=ws)
+        mla.mla_accept_drafts(probs, tokens, uniforms, parents=parents)
+        mla.mla_cache_gather(kv, cu, B * 512, starts=starts, status=word)
+    torch.cuda.synchronize()
+    status = mla.mla_read_status(ws) or int(word.item())
+    print(f"speculative_step: {iters} calls, status {mla.STATUS.get(status, status)}")
     return 0 if status == 0 else 1
 
 
