@@ -490,7 +490,9 @@ cudaError_t launch_merge(const AttnParams& p, cudaStream_t s) {
 
 cudaError_t launch_merge_tree(const AttnParams& p, int sequences, cudaStream_t s) {
   const int64_t rows = (int64_t)sequences * p.n_q * p.H;
-  const int vec = merge_vec(rows, p.num_ctas);
+  // 512 or 128 values a CTA, as launch_merge; never 32 (24 rows in up to 64 pieces: 33 to 38 us a
+  // call with 384 CTAs of 32 values, in two waves, 19 to 34 us with 96 of 128)
+  const int vec = rows >= p.num_ctas ? 16 : 4;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
@@ -508,8 +510,7 @@ cudaError_t launch_merge_tree(const AttnParams& p, int sequences, cudaStream_t s
   }
   cfg.gridDim = dim3((unsigned)rows, kDV / (32 * vec));
   if (vec == 16) return cudaLaunchKernelEx(&cfg, merge_split_kernel<16, kMergeWarps, uint16_t, true>, p);
-  if (vec == 4) return cudaLaunchKernelEx(&cfg, merge_split_kernel<4, kMergeWarps, uint16_t, true>, p);
-  return cudaLaunchKernelEx(&cfg, merge_split_kernel<1, kMergeWarps, uint16_t, true>, p);
+  return cudaLaunchKernelEx(&cfg, merge_split_kernel<4, kMergeWarps, uint16_t, true>, p);
 }
 
 cudaError_t launch_merge_prefill(const AttnParams& p, int P, int split_units, cudaStream_t s) {
