@@ -448,14 +448,17 @@ def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optiona
     B = cu_rows.shape[0] - 1
     if B < 0 or B > kv.seq_lens.shape[0] or B > kv.page_table.shape[0]:
         raise ValueError("cu_rows must have an entry more than there are sequences")
+    f32 = (dtype if out is None else out.dtype) is _F32
+    if not f32 and out is None and dtype is not _BF16:
+        raise ValueError("dtype must be bfloat16 or float32")
+    cu_ptr = _dense(cu_rows, "cu_rows", _I64, (B + 1,), dev)
     if out is None:
         out = torch.empty((n, MLA_D), dtype=dtype, device=dev)
-    f32 = out.dtype is _F32
+    else:
+        _dense(out, "out", _F32 if f32 else _BF16, (n, MLA_D), dev)
     _check("mla_cache_gather", library().mla_cache_gather(
-        c, B, None if starts is None else _dense(starts, "starts", _I32, (B,), dev),
-        _dense(cu_rows, "cu_rows", _I64, (B + 1,), dev), n,
-        _dense(out, "out", _F32 if f32 else _BF16, (n, MLA_D), dev), f32,
-        _status_ptr(status, dev), _on(dev, stream)))
+        c, B, None if starts is None else _dense(starts, "starts", _I32, (B,), dev), cu_ptr, n,
+        out.data_ptr(), f32, _status_ptr(status, dev), _on(dev, stream)))
     return out
 
 
@@ -466,8 +469,14 @@ def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_sc
     _q_check(q, 4)
     B, n, H, _ = q.shape
     dev = q.device
-    out = torch.empty((B, n, H, MLA_DV), dtype=_BF16, device=dev) if out is None else out
-    lse = torch.empty((B, n, H), dtype=_F32, device=dev) if lse is None else lse
+    if out is None:
+        out = torch.empty((B, n, H, MLA_DV), dtype=_BF16, device=dev)
+    else:
+        _dense(out, "out", _BF16, (B, n, H, MLA_DV), dev)
+    if lse is None:
+        lse = torch.empty((B, n, H), dtype=_F32, device=dev)
+    else:
+        _dense(lse, "lse", _F32, (B, n, H), dev)
     ws = workspace(MLA_OP_VERIFY_TREE, B, H, n, dev) if ws is None else ws
     if kv.seq_lens.shape[0] < B or kv.page_table.shape[0] < B or kv.pool.device != dev:
         raise ValueError("kv must describe q's sequences, on q's device")
@@ -475,8 +484,8 @@ def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_sc
         raise ValueError("ws must be a contiguous uint8 tensor on q's device")
     _check("mla_verify_tree", library().mla_verify_tree(
         kv.c_struct(), q.data_ptr(), B, n, H, sm_scale,
-        _dense(tree_mask, "tree_mask", _I64, (B, n), dev), _dense(out, "out", _BF16, (B, n, H, MLA_DV), dev),
-        _dense(lse, "lse", _F32, (B, n, H), dev), ws.data_ptr(), ws.numel(), _on(dev, stream)))
+        _dense(tree_mask, "tree_mask", _I64, (B, n), dev), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+        ws.numel(), _on(dev, stream)))
     return out, lse
 
 

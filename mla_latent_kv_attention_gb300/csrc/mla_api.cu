@@ -203,6 +203,8 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
   p.team = g.team;
   p.passes = g.passes;
   p.tree_mask = tree_mask;
+  p.test_stall = g_test_stall;
+  g_test_stall = 0;
   p.trace = nullptr;  // the profiling hook traces decode, verify and prefill
   char* base = static_cast<char*>(workspace);
   p.hdr = reinterpret_cast<mla::WsHeader*>(base + w.hdr);

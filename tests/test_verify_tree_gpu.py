@@ -167,6 +167,24 @@ def test_bounds_status():
     assert mla.mla_read_status(ws) == 0
 
 
+@pytest.mark.parametrize("B,n", [(2, 8), (40, 1), (30, 7)])
+def test_bounded_wait_reports_timeout(B, n):
+    """Waits that nothing satisfies (the test hook switches one call's key loads off) give up after
+    their limit, in every warp of a warpgroup and in CTAs with several units: the kernel
+    returns, the status says so, and the next call on the workspace is correct."""
+    inp = W.make_inputs("stall", [900] * B, H=12, n_q=n, seed=41)
+    kv = mla.KVCache.from_inputs(inp, DEV)
+    q, rows = inp.q.to(DEV), tree_masks(B, n, 1)
+    mask = as_tensor(rows).to(DEV)
+    ws = mla.workspace(mla.MLA_OP_VERIFY_TREE, B, 12, n, DEV)
+    mla.library().mla_test_stall_next_call()
+    mla.mla_verify_tree(kv, q, mask, inp.sm_scale, ws=ws)
+    assert mla.mla_read_status(ws) == mla.MLA_ERR_TIMEOUT
+    out, lse = mla.mla_verify_tree(kv, q, mask, inp.sm_scale, ws=ws)
+    assert mla.mla_read_status(ws) == 0
+    compare(out, lse, *reference(inp, rows), "after a timed-out call")
+
+
 def test_captured_and_replayed():
     """A captured call reads new queries, masks and lengths when it is replayed, on a side
     stream; two graphs may share a workspace when they run one after the other."""
