@@ -372,7 +372,8 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
  * that holds none either, the token is -1. Weights are rounded to multiples of 2^-43 (a
  * float32 probability above 2^-19 is one already) and shares and sums are whole numbers, so
  * results do not depend on the order of summation. Weights outside [0, 1] count as the nearer
- * end, NaN as 0; so do the uniforms (1 counts as the number just below it).
+ * end; an entry that is NaN in target or draft is neither accepted nor drawn. Uniforms outside
+ * [0, 1) count as the nearest number in it, NaN as 0.
  * A token outside [0, V) or a parent outside [0, j) makes node j no draft (padding): it and
  * what hangs below it are never accepted, and it takes nothing from the draw.
  *   target        device, [B][n][V] float32
@@ -383,7 +384,7 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
  *   out_tokens    device, [B][n] int32: the accepted tokens, the drawn one, then -1
  *   path          device, [B][n] int32: the nodes kept (0 first), then -1: the cache rows to keep
  *   num_accepted  device, [B] int32: drafts accepted (0 .. n - 1)
- * n in 1..64, V in 1..MLA_MAX_VOCAB; the emitted tokens are num_accepted + 1.
+ * n in 1..64, V in 1..MLA_MAX_VOCAB, B up to 65,535; the emitted tokens are num_accepted + 1.
  */
 mla_status_t mla_accept_drafts(const float* target, const int32_t* tokens, const int32_t* parents,
                                const float* draft, const float* uniforms, int B, int n, int V,

@@ -150,6 +150,8 @@ class KVCache:
         for name, t in (("pool", pool), ("page_table", table), ("seq_lens", lens)):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"KVCache.{name} must be a contiguous CUDA tensor")
+            if t.get_device() != pool.get_device():
+                raise ValueError(f"KVCache.{name} must be on the pool's device")
         if pool.dtype is not _U8 or table.dtype is not _I32 or lens.dtype is not _I32:
             raise TypeError("KVCache dtypes: pool uint8, page_table int32, seq_lens int32")
         pages, size, _ = pool.shape
@@ -388,7 +390,7 @@ def _rope_part(t: torch.Tensor, name: str):
         n, H, width = t.shape
         st, sh, sd = t.stride()
         if width == MLA_ROPE and sd == 1:
-            return n, H, st, sh
+            return n, H, st if n > 1 else 0, sh if H > 1 else 0  # (one token, one head: no stride)
     raise ValueError(f"{name} must be a bfloat16 CUDA tensor [n, H, 64] (any token and head "
                      "strides, the 64 RoPE dims contiguous)")
 

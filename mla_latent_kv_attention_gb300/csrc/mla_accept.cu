@@ -110,7 +110,7 @@ __device__ void walk(const AcceptArgs& a, AcSmem& s, int b, bool write) {
     if (par[h] != kNone) {
       pt[h] = target[(int64_t)par[h] * a.V + tok[h]];
       if (DRAFT) qt[h] = a.draft[((int64_t)b * (n - 1) + t - 1) * a.V + tok[h]];
-      up[h] = u[par[h]];
+      up[h] = fminf(fmaxf(u[par[h]], 0.f), 0x1.fffffep-1f);  // in [0, 1), NaN as 0
     }
     s.tok[t] = tok[h];
     s.par[t] = par[h];

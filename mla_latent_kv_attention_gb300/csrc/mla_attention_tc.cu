@@ -1083,7 +1083,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll
               for (int r = 0; r < RH; ++r) {
                 const int j = min(max(ms->row_j[rb + r], 0), nodes - 1);  // (a padding row: any node)
-                if (!(__ldg(half + 2 * j) >> (node & 31) & 1u)) x[r] = -INFINITY;
+                if (!(half[2 * j] >> (node & 31) & 1u)) x[r] = -INFINITY;
               }
             }
           } else {
@@ -1231,7 +1231,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             const uint32_t* half = reinterpret_cast<const uint32_t*>(p.tree_mask) +
                                    2 * ((int64_t)un.b * p.n_q + un.j0) + (node >> 5);
             uint32_t any = 0;
-            for (int j = 0; j * p.H < un.rows; ++j) any |= __ldg(half + 2 * j);
+            for (int j = 0; j * p.H < un.rows; ++j) any |= half[2 * j];
             unseen = !(any >> (node & 31) & 1u);
           }
         }

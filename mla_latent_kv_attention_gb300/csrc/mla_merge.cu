@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
 // 12 us (12,288 rows, most of them in two or three pieces). Bound: one round of dependent L2
 // loads a CTA, then the partials' bytes through L2.
 constexpr int kTreeMergePieces = 2;  // pieces a warp loads at once
-__global__ void __launch_bounds__(kMergeThreads) merge_tree_kernel(AttnParams p, int chunks) {
+__global__ void __launch_bounds__(kMergeThreads, 3) merge_tree_kernel(AttnParams p, int chunks) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = blockIdx.x % chunks;            // eight rows of the group
   const int group = blockIdx.x / chunks % (p.team * p.passes);
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_tree_kernel(AttnParams p,
   };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  float lse_of = lane < count ? __ldg(p.part_lse + at_of(lane)) : -INFINITY;
+  float lse_of = lane < count ? p.part_lse[at_of(lane)] : -INFINITY;
   float4 v[kTreeMergePieces][4];
   auto load = [&](int i0) {
 #pragma unroll
@@ -362,12 +362,12 @@ __global__ void __launch_bounds__(kMergeThreads) merge_tree_kernel(AttnParams p,
       if (i0 + k < count) {
         const float4* src = reinterpret_cast<const float4*>(p.part_out + at_of(i0 + k) * kDV + lane * 16);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[k][e] = __ldg(src + e);
+        for (int e = 0; e < 4; ++e) v[k][e] = src[e];
       }
   };
   load(0);
   float m = lse_of;
-  for (int i = lane + 32; i < count; i += 32) m = fmaxf(m, __ldg(p.part_lse + at_of(i)));
+  for (int i = lane + 32; i < count; i += 32) m = fmaxf(m, p.part_lse[at_of(i)]);
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (m == -INFINITY) {  // no piece saw a key
     out[0] = out[1] = make_uint4(0u, 0u, 0u, 0u);
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_tree_kernel(AttnParams p,
     return;
   }
   float sum = expf(lse_of - m);
-  for (int i = lane + 32; i < count; i += 32) sum += expf(__ldg(p.part_lse + at_of(i)) - m);
+  for (int i = lane + 32; i < count; i += 32) sum += expf(p.part_lse[at_of(i)] - m);
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float lse = m + logf(sum);
   float acc[16];
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_tree_kernel(AttnParams p,
     for (int k = 0; k < kTreeMergePieces; ++k) {
       const int i = i0 + k;
       if (i >= count) break;
-      const float l = i < 32 ? __shfl_sync(0xffffffffu, lse_of, i) : __ldg(p.part_lse + at_of(i));
+      const float l = i < 32 ? __shfl_sync(0xffffffffu, lse_of, i) : p.part_lse[at_of(i)];
       if (l == -INFINITY) continue;  // an empty piece's data was never written
       const float w = expf(l - lse);
 #pragma unroll

@@ -45,8 +45,9 @@ def reference(p, tokens, u, parents=None, q=None):
                     below += int(row[tokens[b, j]])
             else:
                 for j in kids:
+                    ua = np.float32(min(max(u[b, at], 0.0), 1 - 2.0 ** -24)) if u[b, at] == u[b, at] else 0
                     with np.errstate(invalid="ignore"):
-                        if np.float32(u[b, at]) * np.float32(q[b, j - 1, tokens[b, j]]) < p[b, at, tokens[b, j]]:
+                        if np.float32(ua) * np.float32(q[b, j - 1, tokens[b, j]]) < p[b, at, tokens[b, j]]:
                             took = j
             if took is None:
                 break
@@ -143,6 +144,16 @@ def test_acceptance_borders_and_rows_without_weight():
     out, path, count = check(p, tokens, u, q=q)
     assert count.tolist()[:5] == [0] * 5 and count[5] == 1 and out[3, 0] == -1
     assert np.float32(2 / 3) * np.float32(0.75) == np.float32(0.5)
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+def test_uniforms_outside_their_range(drafted):
+    """Below 0 and NaN count as 0 (accepted wherever the target gives anything), 1 and above as the
+    number below 1."""
+    p, tokens, _, _, q = inputs(6, 4, 300, False, drafted, seed=3)
+    bad = torch.tensor([float("nan"), -1.0, float("-inf"), 1.0, 7.0, float("inf")])
+    _, _, count = check(p, tokens, bad[:, None].expand(6, 5).contiguous(), q=q)
+    assert count.tolist()[:3] == [3, 3, 3]
 
 
 def test_odd_trees():

@@ -110,6 +110,19 @@ def test_in_place_and_orders():
     assert torch.equal(x, want)
 
 
+def test_one_token_or_head_of_odd_strides():
+    """Dimensions of size one have no stride, whatever the tensor says."""
+    g = torch.Generator().manual_seed(4)
+    rope = mla.mla_rope_init()
+    a = torch.randn(3, 5, 72, generator=g).bfloat16().to(DEV)
+    one = torch.as_strided(a, (1, 5, 64), (363, 72, 1))
+    got = mla.mla_rope(rope, one, torch.tensor([77], device=DEV))
+    check(got, one, torch.tensor([77]), frequencies(10000.0, 1.0, 0), 1.0, True)
+    head = torch.as_strided(a, (3, 1, 64), (360, 5, 1))
+    got = mla.mla_rope(rope, head, torch.tensor([5, 6, 7], device=DEV))
+    check(got, head, torch.tensor([5, 6, 7]), frequencies(10000.0, 1.0, 0), 1.0, True)
+
+
 def test_special_values_stay_in_their_pair():
     x = torch.ones(2, 1, 64).bfloat16()
     x[0, 0, 4] = float("inf")

@@ -141,6 +141,59 @@ def test_short_and_empty_sequences():
     compare(*run(inp, rows), *ref, "short")
 
 
+@pytest.mark.parametrize("page_size,contiguous", [(128, False), (192, False), (64, True)])
+def test_page_sizes(page_size, contiguous):
+    n = 10
+    inp = W.make_inputs("pages", [1500, 333, n], H=12, n_q=n, seed=page_size, page_size=page_size,
+                        contiguous=contiguous)
+    rows = tree_masks(3, n, seed=2)
+    compare(*run(inp, rows), *reference(inp, rows), f"page_size={page_size}")
+
+
+def test_wide_table_takes_the_same_answers():
+    """The groups follow the page table's width: a short sequence in a wide table (large groups)
+    and in a narrow one (small groups) gives the same rows."""
+    n = 8
+    inp = W.make_inputs("narrow", [700], H=12, n_q=n, seed=3)
+    rows = tree_masks(1, n, seed=3)
+    ref = reference(inp, rows)
+    compare(*run(inp, rows), *ref, "narrow")
+    wide = torch.full((1, 2000), -1, dtype=torch.int32)
+    wide[:, :inp.page_table.shape[1]] = inp.page_table
+    inp.page_table = wide
+    compare(*run(inp, rows), *ref, "wide")
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, give what they give alone; without an
+    lse the outputs are the same."""
+    n = 12
+    a = W.make_inputs("a", [5000, 800], H=12, n_q=n, seed=1)
+    b = W.make_inputs("b", [300] * 20, H=12, n_q=n, seed=2)
+    made = []
+    for inp, seed in ((a, 1), (b, 2)):
+        kv = mla.KVCache.from_inputs(inp, DEV)
+        made.append((kv, inp.q.to(DEV), as_tensor(tree_masks(inp.B, n, seed)).to(DEV),
+                     mla.workspace(mla.MLA_OP_VERIFY_TREE, inp.B, 12, n, DEV)))
+    alone = [mla.mla_verify_tree(kv, q, m, a.sm_scale, ws=ws) for kv, q, m, ws in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for s, (kv, q, m, ws) in zip(streams, made):
+            with torch.cuda.stream(s):
+                got.append(mla.mla_verify_tree(kv, q, m, a.sm_scale, ws=ws))
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, alone):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+    kv, q, m, ws = made[0]
+    out = torch.zeros_like(alone[0][0])
+    assert mla.library().mla_verify_tree(kv.c_struct(), q.data_ptr(), a.B, n, 12, a.sm_scale, m.data_ptr(),
+                                         out.data_ptr(), None, ws.data_ptr(), ws.numel(), None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, alone[0][0])
+
+
 def test_dominant_key_over_a_long_tail():
     """One prefix key far above the others, and siblings whose keys it must not see."""
     inp = W.attention_sink(L=30000, H=12, n_q=7, B=1, seed=3)
