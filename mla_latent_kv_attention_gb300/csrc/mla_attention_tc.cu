@@ -156,6 +156,7 @@ struct Misc {
                         // ahead of the value MMAs when P lives in the stage)
   uint64_t q_full[2];   // query operand buffer holds its unit's terms
   uint64_t q_empty[2];  // the unit that used the buffer has finished its scores
+  uint64_t scale_read[2];  // tree: the softmax warps have read the unit's row_scale (by parity)
   uint64_t q0_done;     // the first unit's query rows are staged (by warps 2.. together)
   uint64_t q1_done;     // the second unit's rows are in this CTA's global query image
   uint64_t wg_bar[3];  // bounded barriers of the softmax warpgroups (128 arrivals)
@@ -549,6 +550,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->q_full[s], 1);
       mbar_init(&ms->q_empty[s], 1);
+      mbar_init(&ms->scale_read[s], 4 * C::kNWG);
     }
     mbar_init(&ms->q0_done, 32 * C::kStageWarps);
     mbar_init(&ms->q1_done, 32 * C::kStageWarps);
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // Ask L2 for the first unit's query rows and page-table entries before the first TMA
     // loads go out: behind the initial burst of key traffic they would arrive late, and
     // both are on the path to the first scores.
-    if (warp >= 2 && ms->plan_b0 < B) {
+    if (warp >= 2 && ms->plan_b0 < B && !(PF == 3 && p.q_staged)) {
       const int b0 = ms->plan_b0;
       const int t = threadIdx.x - 64;
       // 1,152 bytes per row
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   // (staging takes one warp far longer than a unit boundary may last): warps 2.. stage the
   // second unit there before the first key tile lands, the stager warp each later one while
   // the unit before it runs.
-  if (warp >= 2) {
+  if (warp >= 2 && !(PF == 3 && p.q_staged)) {
     Cursor c0 = first_unit<PF>(args, ms);
     while (has_unit<PF>(args, ms, c0) && tiles_in(unit_info<PF>(args, ms, c0)) == 0) c0 = next_unit<PF>(args, c0);
     if (has_unit<PF>(args, ms, c0)) {
@@ -921,13 +923,16 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       const UnitInfo ui = unit_info<PF>(args, ms, cu);
       if (tiles_in(ui) == 0) continue;
       const int slot = k % C::kQB;
-      if (k == 0) {  // staged into shared memory by warps 2.. in the prologue
+      const uint8_t* from = img;
+      if (PF == 3 && p.q_staged) {  // staged by the kernel before: nothing but the copy
+        from = p.qimg + ((int64_t)ui.b * p.team * p.passes + ui.j0 / p.group_nodes) * p.qimg_stride;
+        if (k == 0) fence_proxy_async_global();
+      } else if (k == 0) {  // staged into shared memory by warps 2.. in the prologue
         if (!wait_or_abort(&ms->q0_done, 0, ms, p)) break;
         if (lane == 0) mbar_arrive(&ms->q_full[0]);
         ++k;
         continue;
-      }
-      if (k == 1) {  // staged into the image by warps 2.. in the prologue
+      } else if (k == 1) {  // staged into the image by warps 2.. in the prologue
         if (!wait_or_abort(&ms->q1_done, 0, ms, p)) break;
       } else {
         // the image is free once the previous unit's copy out of it has landed
@@ -939,10 +944,18 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         __syncwarp();
       }
       if (k >= (uint32_t)C::kQB && !wait_or_abort(&ms->q_empty[slot], ((k / C::kQB) - 1) & 1, ms, p)) break;
+      // A unit of one tile may have its scores done before its softmax has begun: the copy for unit
+      // k waits until the softmax warps have seen the copy that used this buffer before (or q_full
+      // would run two phases ahead of them, which a parity cannot tell from none) and read its
+      // row scales (which unit k or the one after it replaces).
+      if (PF == 3 && k >= (uint32_t)C::kQB) {
+        const uint32_t j = k - C::kQB;
+        if (!wait_or_abort(&ms->scale_read[j & 1], (j >> 1) & 1, ms, p)) break;
+      }
       if (lane == 0) {
         mbar_arrive_expect_tx(&ms->q_full[slot], kImgBytes);
-        bulk_g2s(qbuf + slot * C::kQBytes, img, C::kQBytes, &ms->q_full[slot]);
-        bulk_g2s(ms->row_scale[k & 1], img + C::kQBytes, 48 * sizeof(float), &ms->q_full[slot]);
+        bulk_g2s(qbuf + slot * C::kQBytes, from, C::kQBytes, &ms->q_full[slot]);
+        bulk_g2s(ms->row_scale[k & 1], from + C::kQBytes, 48 * sizeof(float), &ms->q_full[slot]);
       }
       __syncwarp();
       ++k;
@@ -1041,6 +1054,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         mo[r] = kNoMax;
         l[r] = 0.f;
       }
+      if (PF == 3) warp_arrive(&ms->scale_read[k & 1]);
       for (int t = 0; t < ntiles; ++t, ++tile) {
         const int sb = tile % C::kSBuf;
         const int s = tile % kStages;
@@ -1421,6 +1435,22 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   }
 }
 
+// Tree verify with more groups than CTAs: every group's query image, one CTA a group, ahead of the
+// attention kernel (a programmatic dependent, which waits for this grid).
+template <int RP>
+__global__ void __launch_bounds__(512) stage_queries_kernel(const __grid_constant__ AttnParams p) {
+  __shared__ int row_off[48];
+  if (threadIdx.x < 48) row_off[threadIdx.x] = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;");
+  __syncthreads();
+  const int groups = p.team * p.passes;
+  const int node0 = (int)(blockIdx.x % groups) * p.group_nodes;
+  const int64_t row0 = ((int64_t)(blockIdx.x / groups) * p.n_q + node0) * p.H;
+  uint8_t* img = p.qimg + (int64_t)blockIdx.x * p.qimg_stride;
+  stage_rows<RP, 16>(p, min(p.group_nodes, p.n_q - node0) * p.H, row_off, p.q + row0 * kD, img,
+                     reinterpret_cast<float*>(img + Cfg<RP>::kQBytes), threadIdx.x >> 5, threadIdx.x & 31);
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -1547,6 +1577,14 @@ cudaError_t launch_tree_tc(const AttnParams& p, cudaStream_t s, int* launches) {
   a.rows = p.R;
   a.status_overwrite = 1;
   cudaError_t e;
+  if (p.q_staged) {
+    const unsigned units = (unsigned)(p.B * p.team);  // (passes x team groups a sequence)
+    auto* stage = a.rows <= 16 ? stage_queries_kernel<16>
+                               : (a.rows <= 32 ? stage_queries_kernel<32> : stage_queries_kernel<48>);
+    stage<<<units, 512, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    ++*launches;
+  }
   if (a.rows <= 16)
     e = launch_rp<16, 3>(a, mm, mt, p.num_ctas, s);
   else if (a.rows <= 32)

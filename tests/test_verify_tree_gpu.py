@@ -141,6 +141,23 @@ def test_short_and_empty_sequences():
     compare(*run(inp, rows), *ref, "short")
 
 
+@pytest.mark.parametrize("B,H,n,top", [(30, 16, 64, 260), (200, 12, 2, 130), (160, 1, 20, 70), (90, 5, 9, 900),
+                                       (25, 11, 31, 400)])
+def test_many_short_sequences(B, H, n, top):
+    """Many units a CTA, most of them one tile long: query images staged ahead, their scales and
+    buffers handed over as soon as the unit before is done (16, 32 and 48 rows a unit)."""
+    r = random.Random(B)
+    lens = [r.choice([0, n, r.randint(n, top), r.randint(n, top)]) for _ in range(B)]
+    inp = W.make_inputs("many", lens, H=H, n_q=n, seed=B)
+    rows = tree_masks(B, n, seed=B)
+    ref = reference(inp, rows)
+    first = run(inp, rows)
+    compare(*first, *ref, f"B={B}")
+    for _ in range(5):  # and the same every time
+        out, lse = run(inp, rows)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
 @pytest.mark.parametrize("page_size,contiguous", [(128, False), (192, False), (64, True)])
 def test_page_sizes(page_size, contiguous):
     n = 10
