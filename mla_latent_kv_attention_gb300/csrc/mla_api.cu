@@ -140,7 +140,7 @@ size_t mla_workspace_size(mla_op_t op, int B, int H, int n_q, int device) {
     const int sms = sm_count(device);
     if (sms <= 0) return 0;
     const mla::TreePlan g = mla::tree_plan(n_q, H, sms, 1, 1 << 30);
-    return mla::ws_layout(B, g.nodes * H, sms, g.images(B, sms)).total;
+    return mla::ws_layout(B, g.nodes * H, sms, g.images(B)).total;
   }
   if (op == MLA_OP_DECODE) n_q = 1;
   if (n_q < 1 || n_q > MLA_MAX_NQ) return 0;
@@ -196,11 +196,10 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
   const int64_t width = kv->page_table_stride < INT32_MAX ? kv->page_table_stride : INT32_MAX;
   const int64_t blocks = (width * kv->page_size + mla::kKeyBlock - 1) / mla::kKeyBlock;
   const mla::TreePlan g = mla::tree_plan(n, H, sms, B, blocks < (1 << 30) ? blocks : 1 << 30);
-  const mla::WsLayout w = mla::ws_layout(B, g.nodes * H, sms, g.images(B, sms));
+  const mla::WsLayout w = mla::ws_layout(B, g.nodes * H, sms, g.images(B));
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE;
   if (B == 0) return MLA_OK;
   mla::AttnParams p = base_params(kv, q, B, n, H, sm_scale, out, lse);
-  p.q_staged = g.images(B, sms) > 0;
   p.B = B * g.passes;
   p.R = p.part_rows = g.nodes * H;
   p.group_nodes = g.nodes;

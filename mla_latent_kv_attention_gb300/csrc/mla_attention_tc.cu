@@ -165,6 +165,7 @@ struct Misc {
   // is sequence b0 (length L0), whose first block sits at pre0
   long long plan_x0, plan_x1, plan_pre0;
   int plan_b0, plan_L0;
+  int plan_seq0, plan_pass0, member;  // tree: b0 = seq0 * passes + pass0; this CTA's place in its team
   int scan[kMaxThreads / 32];
   uint32_t tmem_base;
   int abort;
@@ -204,6 +205,7 @@ struct UnitInfo {
   int rows;       // valid rows of the unit
   int final_out;  // 1: bf16 out + lse directly; 0: normalised partial for the merge
   int slot;       // partial slot (when final_out == 0)
+  int image;      // tree: the unit's query image
 };
 
 // Position in this CTA's list of units. Decode/verify: the sequences whose blocks overlap
@@ -214,6 +216,7 @@ struct Cursor {
   int b;
   long long pre;
   int L;
+  int seq, pass;  // tree: b = seq * passes + pass
 };
 
 __device__ __forceinline__ int seq_len_of(const AttnParams& p, int b) {
@@ -244,31 +247,32 @@ __host__ __device__ constexpr bool is_prefill(int pf) { return pf == 1 || pf == 
 // Tree verify: neighbouring CTAs form teams of p.team, and the plan cuts its cost axis into one
 // range a team. What the plan calls a sequence is a pass over one, in which member m of the team
 // takes group (pass * team + m) of its nodes: the members walk the same keys at the same time,
-// so a tile comes from HBM once and from L2 for the others. The sequence an index of the plan's
-// stands for, the first node of this CTA's group of it, the group's first row of q, out and lse,
-// and its rows (the last group may hold fewer nodes).
+// so a tile comes from HBM once and from L2 for the others. Each group's query image is staged by
+// a kernel of its own (stage_queries_kernel).
+//
+// The plan's indices b in order, with the sequence each stands for (a pass over it, in a tree;
+// counted along, so that no index is divided).
 template <int PF>
-__device__ __forceinline__ int seq_of(const AttnParams& p, int b) {
-  return PF == 3 ? b / p.passes : b;
-}
-template <int PF>
-__device__ __forceinline__ int node0_of(const AttnParams& p, int b) {
-  return PF == 3 ? (b % p.passes * p.team + (int)blockIdx.x % p.team) * p.group_nodes : 0;
-}
-template <int PF>
-__device__ __forceinline__ int row0_of(const AttnParams& p, int b) {
-  if constexpr (PF == 3)
-    return (seq_of<PF>(p, b) * p.n_q + node0_of<PF>(p, b)) * p.H;
-  else
-    return b * p.R;
-}
-template <int PF>
-__device__ __forceinline__ int rows_of(const DecodeArgs& a, int b) {
-  if constexpr (PF == 3)
-    return min(a.p.group_nodes, a.p.n_q - node0_of<PF>(a.p, b)) * a.p.H;
-  else
-    return a.rows;
-}
+struct PlanIndex {
+  int b, seq, pass;
+  __device__ __forceinline__ PlanIndex(const AttnParams& p, int first) : b(first), seq(first), pass(0) {
+    if constexpr (PF == 3) {
+      seq = first / p.passes;
+      pass = first % p.passes;
+    }
+  }
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    ++b;
+    if constexpr (PF == 3) {
+      if (++pass == p.passes) {
+        pass = 0;
+        ++seq;
+      }
+    } else {
+      ++seq;
+    }
+  }
+};
 
 template <int PF>
 __device__ __forceinline__ Cursor first_unit(const DecodeArgs& a, const Misc* ms) {
@@ -277,6 +281,10 @@ __device__ __forceinline__ Cursor first_unit(const DecodeArgs& a, const Misc* ms
   c.b = ms->plan_b0;
   c.pre = ms->plan_pre0;
   c.L = ms->plan_L0;
+  if constexpr (PF == 3) {
+    c.seq = ms->plan_seq0;
+    c.pass = ms->plan_pass0;
+  }
   return c;
 }
 
@@ -296,7 +304,13 @@ __device__ __forceinline__ Cursor next_unit(const DecodeArgs& a, Cursor c) {
   c.pre += blocks_of(c.L);
   do {
     ++c.b;
-    c.L = (c.b < a.p.B) ? seq_len_of(a.p, seq_of<PF>(a.p, c.b)) : 0;
+    if constexpr (PF == 3) {
+      if (++c.pass == a.p.passes) {
+        c.pass = 0;
+        ++c.seq;
+      }
+    }
+    c.L = (c.b < a.p.B) ? seq_len_of(a.p, PF == 3 ? c.seq : c.b) : 0;
   } while (c.b < a.p.B && c.L == 0);
   c.pre += kUnitCost;  // the next sequence's fixed cost precedes its blocks
   return c;
@@ -309,13 +323,21 @@ __device__ __forceinline__ UnitInfo unit_info(const DecodeArgs& a, const Misc* m
   if (!is_prefill(PF)) {
     const long long nb = blocks_of(c.L);
     const long long blo = max(ms->plan_x0, c.pre), bhi = min(ms->plan_x1, c.pre + nb);
-    x.b = seq_of<PF>(p, c.b);
+    x.b = c.b;
     x.L = c.L;
     x.key_lo = (int)(blo - c.pre) * kKeyBlock;
     x.key_hi = (bhi > blo) ? min(c.L, (int)(bhi - c.pre) * kKeyBlock) : x.key_lo;
-    x.qrow0 = row0_of<PF>(p, c.b);
-    x.j0 = node0_of<PF>(p, c.b);
-    x.rows = rows_of<PF>(a, c.b);
+    x.qrow0 = c.b * p.R;
+    x.j0 = 0;
+    x.rows = a.rows;
+    if constexpr (PF == 3) {  // this CTA's group of the sequence's nodes (the last may be short)
+      const int group = c.pass * p.team + ms->member;
+      x.b = c.seq;
+      x.image = c.seq * (p.passes * p.team) + group;
+      x.j0 = group * p.group_nodes;
+      x.qrow0 = (c.seq * p.n_q + x.j0) * p.H;
+      x.rows = min(p.group_nodes, p.n_q - x.j0) * p.H;
+    }
     x.final_out = (blo == c.pre && bhi == c.pre + nb);
     // the CTA's first unit (nothing of an earlier sequence in its range) takes slot 2c
     x.slot = 2 * (int)blockIdx.x + (c.pre - kUnitCost <= ms->plan_x0 ? 0 : 1);
@@ -559,6 +581,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     ms->plan_b0 = args.p.B;  // no unit unless the plan finds one
     ms->plan_x0 = ms->plan_x1 = ms->plan_pre0 = 0;
     ms->plan_L0 = 0;
+    if constexpr (PF == 3) {
+      ms->plan_seq0 = ms->plan_pass0 = 0;
+      ms->member = blockIdx.x % args.p.team;
+    }
     fence_mbar_init();
     prefetch_tensormap(&map_main);
     prefetch_tensormap(&map_tail);
@@ -577,8 +603,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   const uint32_t tmem = ms->tmem_base;
   // Everything above may overlap the previous kernel in the stream (programmatic dependent
   // launch); inputs are read only after it has completed. The merge kernel, a programmatic
-  // dependent of this one, may be scheduled from here on and waits for this grid itself.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // dependent of this one, may be scheduled from here on and waits for this grid itself. (Tree: the
+  // kernel before is stage_queries_kernel, which began when everything before it had completed
+  // and writes query images only; the warp that copies them waits for it.)
+  if constexpr (PF != 3) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   if (trace && threadIdx.x == 0) trace[kTrWaited] = globaltimer_ns();
 
@@ -596,11 +624,11 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const int per = (B + C::kThreads - 1) / C::kThreads;  // sequences per thread, contiguous
     const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
     long long mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const int L = p.seq_lens[seq_of<PF>(p, b)];
+    for (PlanIndex<PF> i(p, b_lo); i.b < b_hi; i.next(p)) {
+      const int L = p.seq_lens[i.seq];
       const int64_t cap = p.pt_stride * (int64_t)p.page_size;
       if (L < 0 || (int64_t)L > cap) report(ms, MLA_ERR_BOUNDS);
-      const int nb = blocks_of(seq_len_of(p, seq_of<PF>(p, b)));
+      const int nb = blocks_of(seq_len_of(p, i.seq));
       mine += nb > 0 ? nb + kUnitCost : 0;
     }
     // exclusive prefix of the per-thread block counts over the CTA
@@ -624,15 +652,19 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const long long c = PF == 3 ? blockIdx.x / p.team : blockIdx.x;
     const long long x0 = total > 0 ? range_lo(c, total, n) : 0;
     const long long x1 = total > 0 ? range_lo(c + 1, total, n) : 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const int nb = blocks_of(seq_len_of(p, seq_of<PF>(p, b)));
+    for (PlanIndex<PF> i(p, b_lo); i.b < b_hi; i.next(p)) {
+      const int nb = blocks_of(seq_len_of(p, i.seq));
       const long long first = pre + kUnitCost;  // the sequence's first block
       // the range's first unit: the sequence whose span holds x0, if the range reaches
       // one of its blocks
       if (nb > 0 && pre <= x0 && x0 < first + nb && first < x1 && x0 < x1) {
-        ms->plan_b0 = b;
+        ms->plan_b0 = i.b;
         ms->plan_pre0 = first;
-        ms->plan_L0 = seq_len_of(p, seq_of<PF>(p, b));
+        ms->plan_L0 = seq_len_of(p, i.seq);
+        if constexpr (PF == 3) {
+          ms->plan_seq0 = i.seq;
+          ms->plan_pass0 = i.pass;
+        }
       }
       if (nb > 0) pre = first + nb;
     }
@@ -645,24 +677,26 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // Ask L2 for the first unit's query rows and page-table entries before the first TMA
     // loads go out: behind the initial burst of key traffic they would arrive late, and
     // both are on the path to the first scores.
-    if (warp >= 2 && ms->plan_b0 < B && !(PF == 3 && p.q_staged)) {
+    if (warp >= 2 && ms->plan_b0 < B) {
       const int b0 = ms->plan_b0;
-      const int t = threadIdx.x - 64;
-      // 1,152 bytes per row
-      if (t < rows_of<PF>(args, b0) * 9)
-        prefetch_l2(reinterpret_cast<const uint8_t*>(
-                        p.q + ((int64_t)row0_of<PF>(p, b0) + ms->row_off[t / 9]) * kD) + (t % 9) * 128);
-      // and the second unit's rows (its sequence follows b0) for the prologue's second pass
-      const Cursor c1 = next_unit<PF>(args, first_unit<PF>(args, ms));
-      if (has_unit<PF>(args, ms, c1) && t < rows_of<PF>(args, c1.b) * 9)
-        prefetch_l2(reinterpret_cast<const uint8_t*>(
-                        p.q + ((int64_t)row0_of<PF>(p, c1.b) + ms->row_off[t / 9]) * kD) + (t % 9) * 128);
+      if constexpr (PF != 3) {
+        const int t = threadIdx.x - 64;
+        const int qlines = args.rows * 9;  // 1,152 bytes per row
+        if (t < qlines)
+          prefetch_l2(reinterpret_cast<const uint8_t*>(
+                          p.q + ((int64_t)b0 * p.R + ms->row_off[t / 9]) * kD) + (t % 9) * 128);
+        // and the second unit's rows (its sequence follows b0) for the prologue's second pass
+        const Cursor c1 = next_unit<PF>(args, first_unit<PF>(args, ms));
+        if (t < qlines && has_unit<PF>(args, ms, c1))
+          prefetch_l2(reinterpret_cast<const uint8_t*>(
+                          p.q + ((int64_t)c1.b * p.R + ms->row_off[t / 9]) * kD) + (t % 9) * 128);
+      }
       // four lines of 32 page-table entries, by the CTA's last four threads (past the
       // query lines: at most 48 rows x 9)
       const int64_t pg0 = max(0ll, ms->plan_x0 - ms->plan_pre0) * kKeyBlock / p.page_size;
       const int tp = (int)threadIdx.x - (C::kThreads - 4);
       const int64_t pg = pg0 + (int64_t)tp * 32;
-      if (tp >= 0 && pg < p.pt_stride) prefetch_l2(p.page_table + (int64_t)seq_of<PF>(p, b0) * p.pt_stride + pg);
+      if (tp >= 0 && pg < p.pt_stride) prefetch_l2(p.page_table + (int64_t)(PF == 3 ? ms->plan_seq0 : b0) * p.pt_stride + pg);
     }
     __syncthreads();
     if (trace && threadIdx.x == 0) trace[kTrPlanPrefetch] = globaltimer_ns();
@@ -737,7 +771,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   // (staging takes one warp far longer than a unit boundary may last): warps 2.. stage the
   // second unit there before the first key tile lands, the stager warp each later one while
   // the unit before it runs.
-  if (warp >= 2 && !(PF == 3 && p.q_staged)) {
+  if (PF != 3 && warp >= 2) {
     Cursor c0 = first_unit<PF>(args, ms);
     while (has_unit<PF>(args, ms, c0) && tiles_in(unit_info<PF>(args, ms, c0)) == 0) c0 = next_unit<PF>(args, c0);
     if (has_unit<PF>(args, ms, c0)) {
@@ -924,9 +958,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       if (tiles_in(ui) == 0) continue;
       const int slot = k % C::kQB;
       const uint8_t* from = img;
-      if (PF == 3 && p.q_staged) {  // staged by the kernel before: nothing but the copy
-        from = p.qimg + ((int64_t)ui.b * p.team * p.passes + ui.j0 / p.group_nodes) * p.qimg_stride;
-        if (k == 0) fence_proxy_async_global();
+      if constexpr (PF == 3) {  // staged by the kernel before: nothing but the copy
+        from = p.qimg + (int64_t)ui.image * p.qimg_stride;
+        if (k == 0) {
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          fence_proxy_async_global();
+        }
       } else if (k == 0) {  // staged into shared memory by warps 2.. in the prologue
         if (!wait_or_abort(&ms->q0_done, 0, ms, p)) break;
         if (lane == 0) mbar_arrive(&ms->q_full[0]);
@@ -1421,6 +1458,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     }
   }
 
+  // (tree: a CTA without units has not waited yet, and this grid must not complete before the one
+  // in front of it)
+  if constexpr (PF == 3) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -1435,8 +1475,11 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   }
 }
 
-// Tree verify with more groups than CTAs: every group's query image, one CTA a group, ahead of the
-// attention kernel (a programmatic dependent, which waits for this grid).
+// Tree verify: every group's query image, one CTA a group. The attention kernel, a programmatic
+// dependent, plans and loads its first keys meanwhile. (Staged by the attention kernel itself, as
+// decode does: 77 KB of its code, fetched cold on the way to the first scores, and one warp for a
+// CTA's later units, 28 us each: 64 sequences of 64 nodes of 16 heads on 100 to 130 keys took
+// 305 us, 175 us this way; 8 nodes of 12 heads on 1,024 keys 22.1 and 20.3 us.)
 template <int RP>
 __global__ void __launch_bounds__(512) stage_queries_kernel(const __grid_constant__ AttnParams p) {
   __shared__ int row_off[48];
@@ -1577,14 +1620,12 @@ cudaError_t launch_tree_tc(const AttnParams& p, cudaStream_t s, int* launches) {
   a.rows = p.R;
   a.status_overwrite = 1;
   cudaError_t e;
-  if (p.q_staged) {
-    const unsigned units = (unsigned)(p.B * p.team);  // (passes x team groups a sequence)
-    auto* stage = a.rows <= 16 ? stage_queries_kernel<16>
-                               : (a.rows <= 32 ? stage_queries_kernel<32> : stage_queries_kernel<48>);
-    stage<<<units, 512, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    ++*launches;
-  }
+  const unsigned units = (unsigned)(p.B * p.team);  // (passes x team groups a sequence)
+  auto* stage = a.rows <= 16 ? stage_queries_kernel<16>
+                             : (a.rows <= 32 ? stage_queries_kernel<32> : stage_queries_kernel<48>);
+  stage<<<units, 512, 0, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  ++*launches;
   if (a.rows <= 16)
     e = launch_rp<16, 3>(a, mm, mt, p.num_ctas, s);
   else if (a.rows <= 32)

@@ -39,7 +39,7 @@ inline size_t qimg_bytes(int rp) { return align_up((size_t)2 * rp * MLA_D + size
 
 // Offsets of the workspace regions for one call.
 //   status:   one word per CTA, written by that CTA at exit (0 or its first error)
-//   qimg:     one staged query image per CTA (a tree's verify with more units than CTAs: per unit)
+//   qimg:     one staged query image per CTA (a tree's verify: per group of nodes)
 //   part_*:   two partial slots per CTA (the first and the last unit of its block range
 //             are the only ones that can hold part of a sequence), R rows each
 struct WsLayout {
@@ -50,7 +50,7 @@ struct WsLayout {
 
 inline WsLayout ws_layout(int B, int rows_per_seq, int num_sms, int64_t images = 0) {
   WsLayout w;
-  if (images < num_sms) images = num_sms;
+  if (images == 0) images = num_sms;
   w.max_slots = 2 * num_sms;
   w.qimg_stride = qimg_bytes(padded_rows(rows_per_seq));
   size_t off = 0;
@@ -78,13 +78,9 @@ struct TreePlan {
   int nodes;   // nodes of a group (the last may hold fewer)
   int team;    // CTAs of a team
   int passes;  // groups a sequence = team * passes
-  // Query images to keep: with more groups than CTAs every group's, staged by a kernel of its own
-  // ahead of the attention (inside it one warp stages a CTA's later units, 28 us each: 64
-  // sequences of 64 nodes of 16 heads on 100 to 130 keys took 305 us, XXX us staged ahead).
-  int64_t images(int64_t B, int num_sms) const {
-    const int64_t units = B * team * passes;
-    return units > num_sms ? units : 0;
-  }
+  // Query images to keep: every group's, staged by a kernel of its own beside the attention
+  // kernel's prologue.
+  int64_t images(int64_t B) const { return B * team * passes; }
 };
 // blocks: key blocks that a sequence can have at all (its page-table row's width; the lengths are
 // on the device). Where even groups of 16 or 32 rows leave every CTA at most one block, the
@@ -151,7 +147,6 @@ struct AttnParams {
   // sequences (`passes` each), R the rows of a full group of group_nodes nodes, n_q all nodes.
   const uint64_t* tree_mask;  // [sequences][n_q]
   int group_nodes, team, passes;
-  int q_staged;               // 1: qimg holds every group's image (TreePlan::images)
   unsigned long long* trace;  // profiling hook: kTraceWords globaltimer stamps per CTA, or null
   int trace_ctas;             // CTAs the trace buffer has room for
 };
