@@ -216,7 +216,9 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
   p.part_out = reinterpret_cast<float*>(base + w.part_out);
   p.qimg = reinterpret_cast<uint8_t*>(base + w.qimg);
   p.qimg_stride = (int64_t)w.qimg_stride;
-  p.num_ctas = sms / g.team * g.team;
+  const unsigned long long teams = (unsigned long long)(sms / g.team);
+  p.teams_inv = teams > 1 ? ~0ull / teams + 1 : 0;
+  p.num_ctas = (int)teams * g.team;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_mark(g_prof_start, s);
   const cudaError_t e = mla::launch_tree_tc(p, s, &g_last_launches);

@@ -144,6 +144,7 @@ struct Misc {
   alignas(16) float row_scale[2][48];  // by unit parity
   alignas(16) float red[2][48 * 4];  // per-tile warp maxima, [row][warp]
   alignas(16) float lred[4][48];
+  alignas(16) float tree_max[2][48];  // tree: running maxima, by parity of the times they moved
   alignas(16) float alpha[48];       // this tile's rescale factors (each warp of a
                                      // warpgroup writes the same values for its rows)
   alignas(16) int grow[2][12];       // per tile parity and warp: some row's max moves
@@ -624,6 +625,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const int per = (B + C::kThreads - 1) / C::kThreads;  // sequences per thread, contiguous
     const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
     long long mine = 0;
+#pragma unroll(PF == 3 ? 1 : 4)
     for (PlanIndex<PF> i(p, b_lo); i.b < b_hi; i.next(p)) {
       const int L = p.seq_lens[i.seq];
       const int64_t cap = p.pt_stride * (int64_t)p.page_size;
@@ -647,11 +649,20 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       total += ms->scan[w];
     }
     long long pre = before + incl - mine;
-    // (a tree's ranges belong to teams of CTAs)
-    const long long n = PF == 3 ? gridDim.x / p.team : gridDim.x;
-    const long long c = PF == 3 ? blockIdx.x / p.team : blockIdx.x;
-    const long long x0 = total > 0 ? range_lo(c, total, n) : 0;
-    const long long x1 = total > 0 ? range_lo(c + 1, total, n) : 0;
+    long long x0, x1;
+    if constexpr (PF == 3) {
+      // A tree's ranges belong to teams of CTAs. range_lo's quotients by the reciprocal: exact, as
+      // c * total is below 2^64 / teams (and less code than 64-bit divisions, which a short
+      // call fetches cold; the same goes for the plan's loops not being unrolled).
+      const unsigned c = blockIdx.x / p.team;
+      x0 = (long long)__umul64hi(c * (unsigned long long)total, p.teams_inv);
+      x1 = p.teams_inv ? (long long)__umul64hi((c + 1) * (unsigned long long)total, p.teams_inv) : total;
+    } else {
+      const long long n = gridDim.x, c = blockIdx.x;
+      x0 = total > 0 ? range_lo(c, total, n) : 0;
+      x1 = total > 0 ? range_lo(c + 1, total, n) : 0;
+    }
+#pragma unroll(PF == 3 ? 1 : 4)
     for (PlanIndex<PF> i(p, b_lo); i.b < b_hi; i.next(p)) {
       const int nb = blocks_of(seq_len_of(p, i.seq));
       const long long first = pre + kUnitCost;  // the sequence's first block
@@ -1010,6 +1021,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const uint32_t lane_addr = (uint32_t)(wq * 32) << 16;
     const float kv_scale = p.kv_scale;
     uint32_t tile = 0, wg_phase = 0, k = 0;  // k: units with work, in order
+    uint32_t moves = 0;  // tree: times a running maximum of the warpgroup has moved
     // PV completions are confirmed in tile order, each before the PV two tiles later can
     // complete (that one needs this warpgroup's next P), so a phase parity names one tile
     // A wait that gives up does not make its lane leave on its own: `ok` collects the
@@ -1091,7 +1103,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         mo[r] = kNoMax;
         l[r] = 0.f;
       }
-      if (PF == 3) warp_arrive(&ms->scale_read[k & 1]);
+      if constexpr (PF == 3) {
+        if (lane < RH) ms->tree_max[moves & 1][rb + lane] = kNoMax;
+        warp_arrive(&ms->scale_read[k & 1]);
+      }
       for (int t = 0; t < ntiles; ++t, ++tile) {
         const int sb = tile % C::kSBuf;
         const int s = tile % kStages;
@@ -1122,21 +1137,22 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         // masking only on tiles that reach past the first new position's last visible key
         if (k0 + kTileKeys - 1 > lim0) {
           if constexpr (PF == 3) {
-            // this thread's key is node `node`'s: the half of each row's mask that holds its bit
+            // this thread's key is node `node`'s: which of its rows see it, node by node of the
+            // unit (a node is H neighbouring rows), from the half of each mask that holds its bit
             const int node = kabs - (L - p.n_q);
-            if (kabs >= un.key_hi) {
-#pragma unroll
-              for (int r = 0; r < RH; ++r) x[r] = -INFINITY;
-            } else if (node >= 0) {
+            uint32_t seen = node < 0 ? ~0u : 0u;
+            if (node >= 0 && kabs < un.key_hi) {
               const uint32_t* half = reinterpret_cast<const uint32_t*>(p.tree_mask) +
                                      2 * ((int64_t)un.b * p.n_q + un.j0) + (node >> 5);
-              const int nodes = p.n_q - un.j0;
-#pragma unroll
-              for (int r = 0; r < RH; ++r) {
-                const int j = min(max(ms->row_j[rb + r], 0), nodes - 1);  // (a padding row: any node)
-                if (!(half[2 * j] >> (node & 31) & 1u)) x[r] = -INFINITY;
-              }
+              const int end = min(rb + RH, R);
+#pragma unroll 1
+              for (int j = rb / p.H; j * p.H < end; ++j)
+                if (half[2 * j] >> (node & 31) & 1u)
+                  seen |= ((1u << min(RH, (j + 1) * p.H - rb)) - 1u) & (~0u << max(0, j * p.H - rb));
             }
+#pragma unroll
+            for (int r = 0; r < RH; ++r)
+              if (!(seen >> r & 1u)) x[r] = -INFINITY;
           } else {
 #pragma unroll
             for (int r = 0; r < RH; ++r) {
@@ -1171,7 +1187,41 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           grow = (gf.x | gf.y | gf.z | gf.w) != 0;
         }
         bool need_rescale = false;
-        if (grow) {
+        if (PF == 3 && grow) {
+          // as below, but a lane takes a row (less code to fetch, and fewer steps): the maxima in
+          // shared memory, read from the side that the time before wrote, written to the other
+          // (each warp of the warpgroup the same values)
+          float* red = &ms->red[tile & 1][0];
+          float v = 0.f;
+#pragma unroll
+          for (int r = 0; r < RH; ++r) {
+            const float w = warp_max(x[r]);
+            if (lane == r) v = w;
+          }
+          if (lane < RH) red[(rb + lane) * 4 + wq] = v;
+          ok &= wg_sync();
+          bool moved = false;
+          if (lane < RH) {
+            const float4 t4 = *reinterpret_cast<const float4*>(&red[(rb + lane) * 4]);
+            const float tm = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
+            float now = ms->tree_max[moves & 1][rb + lane], al = 1.f;
+            if (tm > now + kHeadroom) {
+              al = ex2(now + kPScale - tm);
+              moved = now != kNoMax;
+              now = tm - kPScale;
+            }
+            ms->tree_max[(moves & 1) ^ 1][rb + lane] = now;
+            ms->alpha[rb + lane] = al;
+          }
+          need_rescale = __any_sync(0xffffffffu, moved);
+          __syncwarp();
+          ++moves;
+#pragma unroll
+          for (int r = 0; r < RH; ++r) {
+            mo[r] = ms->tree_max[moves & 1][rb + r];
+            l[r] *= ms->alpha[rb + r];
+          }
+        } else if (grow) {
           // tile max per row: warp max in hardware, then the four warps through shared memory
           float* red = &ms->red[tile & 1][0];
 #pragma unroll
@@ -1333,11 +1383,31 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       }
       if (trace && threadIdx.x == 32 * kSoftmaxWarp0) trace[kTrLastP] = globaltimer_ns();
       // ---- epilogue: row sums, then O / l
+      if constexpr (PF == 3) {
+        // all rows at once: each exchange halves the rows that a lane still adds up
+        float s[RH];
 #pragma unroll
-      for (int r = 0; r < RH; ++r) {
-        float v = l[r];
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) ms->lred[wq][rb + r] = v;
+        for (int r = 0; r < RH; ++r) s[r] = l[r];
+        int row = 0, width = 16;
+#pragma unroll
+        for (int h = RH / 2; h > 0; h >>= 1, width >>= 1) {
+          const bool up = lane & width;
+#pragma unroll
+          for (int r = 0; r < h; ++r) {
+            const float give = up ? s[r] : s[r + h], keep = up ? s[r + h] : s[r];
+            s[r] = keep + __shfl_xor_sync(0xffffffffu, give, width);
+          }
+          row += up ? h : 0;
+        }
+        for (; width > 0; width >>= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], width);
+        ms->lred[wq][rb + row] = s[0];  // (two or four lanes the same)
+      } else {
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+          float v = l[r];
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == 0) ms->lred[wq][rb + r] = v;
+        }
       }
       ok &= wg_sync();
       float inv[RH];

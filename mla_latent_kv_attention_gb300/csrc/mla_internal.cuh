@@ -147,6 +147,7 @@ struct AttnParams {
   // sequences (`passes` each), R the rows of a full group of group_nodes nodes, n_q all nodes.
   const uint64_t* tree_mask;  // [sequences][n_q]
   int group_nodes, team, passes;
+  unsigned long long teams_inv;  // ceil(2^64 / teams), 0 for one team
   unsigned long long* trace;  // profiling hook: kTraceWords globaltimer stamps per CTA, or null
   int trace_ctas;             // CTAs the trace buffer has room for
 };
