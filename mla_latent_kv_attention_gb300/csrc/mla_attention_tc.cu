@@ -536,6 +536,42 @@ __device__ __forceinline__ void stage_rows(const AttnParams& p, int R, const int
   }
 }
 
+// How the two issuing warps run. One thread each: lane 0 alone walks the tiles. Tree: the whole
+// warp does, and an elected lane issues. The control flow and the operands are then the same for
+// every lane as far as the compiler can tell (votes and broadcasts say so), so it keeps the
+// descriptors, of which only the low half moves, in the uniform registers that the MMA
+// reads, instead of moving eight registers there for each one: 32 x 32 nodes over 4K-16K 315 ->
+// 291 us.
+template <bool WARP>
+struct Issuer {
+  uint32_t leader;
+  __device__ __forceinline__ Issuer() : leader(WARP ? elect_one() : 1u) {}
+  __device__ __forceinline__ bool runs(int lane) const { return WARP || lane == 0; }
+  __device__ __forceinline__ bool same(bool v) const {
+    return WARP ? (bool)__all_sync(0xffffffffu, v) : v;
+  }
+  __device__ __forceinline__ uint32_t same(uint32_t v) const {
+    return WARP ? __shfl_sync(0xffffffffu, v, 0) : v;
+  }
+  // a tile's place within a descriptor's base, and the descriptor `off` (16-byte units) past it
+  __device__ __forceinline__ uint32_t place(uint64_t base, uint32_t tile_off) const {
+    return WARP ? same((uint32_t)base + tile_off) : tile_off;
+  }
+  static __device__ __forceinline__ uint64_t at(uint64_t base, uint32_t place, uint32_t off) {
+    return WARP ? ((base >> 32 << 32) | (place + off)) : base + place + off;
+  }
+  __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                      uint32_t accumulate) const {
+    if constexpr (WARP)
+      mma_f8f6f4_by(leader, d, a, b, idesc, accumulate);
+    else
+      mma_f8f6f4(d, a, b, idesc, accumulate);
+  }
+  __device__ __forceinline__ void commit(uint64_t* bar) const {
+    if (!WARP || leader) mma_commit(bar);
+  }
+};
+
 template <int RP, int PF, bool TR>
 __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ DecodeArgs args,
@@ -549,7 +585,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   Misc* ms = reinterpret_cast<Misc*>(smem + C::kOffMisc);
   uint8_t* pbuf = smem + C::kOffP;
   uint8_t* qbuf = smem + C::kOffQ;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = PF == 3 ? __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0) : (int)threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   // profiling hook: this CTA's stamps, or null
   // (TR: a separate instantiation for traced calls, so the usual one carries no stamp code)
   unsigned long long* const trace = (TR && p.trace && (int)blockIdx.x < p.trace_ctas)
@@ -861,7 +898,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // read and its unit's query terms are staged. Values (PV) have their own issuing warp: a
     // single thread spends tens of cycles per tcgen05.mma, so one issuer would serialise the
     // two.
-    if (lane == 0) {
+    const Issuer<PF == 3> by;
+    if (by.runs(lane)) {
       constexpr uint32_t idesc_qk = instr_desc(0, 0, 0, 0, 128, C::NQK);
       const uint64_t a_main0 = smem_desc(smem_addr(smem + C::kOffStages), 16, 1024, Swizzle::k128B);
       const uint64_t a_tail0 = smem_desc(smem_addr(smem + C::kOffStages + C::kTail), 16, 512, Swizzle::k64B);
@@ -869,40 +907,41 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       const uint64_t b_tail0 = smem_desc(smem_addr(qbuf + 4 * (C::NQK * 128)), 16, 512, Swizzle::k64B);
       uint32_t g = 0, units_done = 0;
       bool ok = true;
-      for (Cursor cu = first_unit<PF>(args, ms); has_unit<PF>(args, ms, cu) && ok; cu = next_unit<PF>(args, cu)) {
-        const int n = tiles_in(unit_info<PF>(args, ms, cu));
+      for (Cursor cu = first_unit<PF>(args, ms); by.same(has_unit<PF>(args, ms, cu) && ok);
+           cu = next_unit<PF>(args, cu)) {
+        const int n = (int)by.same((uint32_t)tiles_in(unit_info<PF>(args, ms, cu)));
         if (n == 0) continue;
         const int qslot = units_done % C::kQB;
-        if (!(ok = wait_or_abort(&ms->q_full[qslot], (units_done / C::kQB) & 1, ms, p))) break;
+        if (!(ok = by.same(wait_or_abort(&ms->q_full[qslot], (units_done / C::kQB) & 1, ms, p)))) break;
         const uint32_t qoff = (uint32_t)(qslot * C::kQBytes) >> 4;
         for (int t = 0; t < n; ++t, ++g) {
           const int s = g % kStages, sb = g % C::kSBuf;
           const uint32_t ph = (g / kStages) & 1;
-          if (!(ok = wait_or_abort(&ms->s_empty[sb], ((g / C::kSBuf) & 1) ^ 1, ms, p))) break;
+          if (!(ok = by.same(wait_or_abort(&ms->s_empty[sb], ((g / C::kSBuf) & 1) ^ 1, ms, p)))) break;
           const uint32_t soff = (uint32_t)(s * C::kStageStride) >> 4;
-          const uint32_t d = tmem + C::kSCol + sb * C::NQK;
+          const uint32_t d = by.same(tmem + C::kSCol + sb * C::NQK);
+          const uint32_t am = by.place(a_main0, soff), at = by.place(a_tail0, soff);
+          const uint32_t bm = by.place(b_main0, qoff), bt = by.place(b_tail0, qoff);
           // each latent chunk as soon as it has landed, then the RoPE tail
 #pragma unroll
           for (int c = 0; c < 4 && ok; ++c) {
             if (c == 0 || c == 2) {  // a half has landed
-              if (!(ok = wait_or_abort(&ms->kv_full[s][part_of_chunk(c)], ph, ms, p))) break;
+              if (!(ok = by.same(wait_or_abort(&ms->kv_full[s][part_of_chunk(c)], ph, ms, p)))) break;
               tc_fence_after();
             }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f8f6f4(d, a_main0 + soff + ((c * kChunkBytes + kk * 32) >> 4),
-                         b_main0 + qoff + ((c * (C::NQK * 128) + kk * 32) >> 4), idesc_qk,
-                         (c | kk) != 0);
+              by.mma(d, by.at(a_main0, am, (c * kChunkBytes + kk * 32) >> 4),
+                     by.at(b_main0, bm, (c * (C::NQK * 128) + kk * 32) >> 4), idesc_qk, (c | kk) != 0);
           }
           if (!ok) break;  // the tail belongs to the second half, landed by now
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
-            mma_f8f6f4(d, a_tail0 + soff + ((kk * 32) >> 4), b_tail0 + qoff + ((kk * 32) >> 4),
-                       idesc_qk, 1);
-          mma_commit(&ms->s_full[sb]);
+            by.mma(d, by.at(a_tail0, at, (kk * 32) >> 4), by.at(b_tail0, bt, (kk * 32) >> 4), idesc_qk, 1);
+          by.commit(&ms->s_full[sb]);
         }
         if (!ok) break;
-        mma_commit(&ms->q_empty[qslot]);  // that query buffer is free once these complete
+        by.commit(&ms->q_empty[qslot]);  // that query buffer is free once these complete
         ++units_done;
       }
     }
@@ -911,7 +950,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // PV of every tile the moment its probabilities are in shared memory; completion hands
     // the KV stage back to the producer, part by part, and lets the softmax reuse P and
     // rescale O.
-    if (lane == 0) {
+    const Issuer<PF == 3> by;
+    if (by.runs(lane)) {
       // A = V^T as e4m3 codes, B = P^T as e5m2 terms (kind::f8f6f4 takes each operand's
       // format from its own descriptor field), both MN-major
       constexpr uint32_t idesc_stacked = instr_desc(kFmtE4M3, kFmtE5M2, 1, 1, 128, 3 * RP);
@@ -922,14 +962,16 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                                     128, 2048, Swizzle::kNone);
       uint32_t g = 0;
       bool ok = true;
-      for (Cursor cu = first_unit<PF>(args, ms); has_unit<PF>(args, ms, cu) && ok; cu = next_unit<PF>(args, cu)) {
-        const int n = tiles_in(unit_info<PF>(args, ms, cu));
+      for (Cursor cu = first_unit<PF>(args, ms); by.same(has_unit<PF>(args, ms, cu) && ok);
+           cu = next_unit<PF>(args, cu)) {
+        const int n = (int)by.same((uint32_t)tiles_in(unit_info<PF>(args, ms, cu)));
         for (int t = 0; t < n; ++t, ++g) {
-          if (!(ok = wait_or_abort(&ms->p_full[g & 1], (g >> 1) & 1, ms, p))) break;
+          if (!(ok = by.same(wait_or_abort(&ms->p_full[g & 1], (g >> 1) & 1, ms, p)))) break;
           tc_fence_after();
           const int s = g % kStages;
           const uint32_t soff = (uint32_t)(s * C::kStageStride) >> 4;
           const uint32_t poff = C::kPInStage ? soff : 0u;
+          const uint32_t o = by.same(tmem), av = by.place(a0, soff), bp = by.place(b0, poff);
           // chunk by chunk, each freed for the next tile's load once its own MMAs complete
           // (back-to-back MMAs into one accumulator cost no more than alternating ones)
           // chunk by chunk (back-to-back MMAs into one accumulator cost no more than
@@ -940,18 +982,17 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           for (int c = 0; c < 4; ++c) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-              const uint64_t a = a0 + soff + ((c * kChunkBytes + ks * 4096) >> 4);
+              const uint64_t a = by.at(a0, av, (c * kChunkBytes + ks * 4096) >> 4);
               if (C::oterms(c) == 3) {  // stacked: one MMA over all three terms' rows
-                mma_f8f6f4(tmem + C::ocol(c), a, b0 + poff + ((ks * 512) >> 4), idesc_stacked,
-                           t > 0 || ks > 0);
+                by.mma(o + C::ocol(c), a, by.at(b0, bp, (ks * 512) >> 4), idesc_stacked, t > 0 || ks > 0);
               } else {  // summed: one MMA per term into the same accumulator
 #pragma unroll
                 for (int term = 0; term < 3; ++term)
-                  mma_f8f6f4(tmem + C::ocol(c), a, b0 + poff + ((C::pterm(term) + ks * 512) >> 4),
-                             idesc_term, t > 0 || ks > 0 || term > 0);
+                  by.mma(o + C::ocol(c), a, by.at(b0, bp, (C::pterm(term) + ks * 512) >> 4), idesc_term,
+                         t > 0 || ks > 0 || term > 0);
               }
             }
-            if (c == 1 || c == 3) mma_commit(&ms->kv_free[s][part_of_chunk(c)]);
+            if (c == 1 || c == 3) by.commit(&ms->kv_free[s][part_of_chunk(c)]);
           }
         }
       }
