@@ -61,13 +61,29 @@ constexpr int kStageBytes = 4 * kChunkBytes + 2 * 4096;  // 73,728 bytes loaded 
 // next tile's first half loads while the second is still being read. (Every
 // tcgen05.commit costs the issuing thread time: measured, five parts ran slower than one,
 // two fastest.)
-constexpr int kParts = 2;
-__host__ __device__ constexpr int part_of_chunk(int c) { return c / 2; }
-constexpr int kTailPart = 1;
-__host__ __device__ constexpr int part_bytes(int part) {
-  return part == 0 ? 2 * kChunkBytes : 2 * kChunkBytes + 2 * 4096;
+// Tree verify (pf = 3, the kernel's PF): the second half once more in two, chunk 2, then chunk 3
+// with the tail (its MMAs are issued fast enough for the commit: 32 x 32 nodes over 4K-16K 291.7
+// -> 287.7 us; four parts or 3 + 1 chunks ran slower).
+constexpr int kMaxParts = 3;
+__host__ __device__ constexpr int num_parts(int pf) { return pf == 3 ? 3 : 2; }
+__host__ __device__ constexpr int part_of_chunk(int c, int pf) {
+  return c < 2 ? 0 : (pf == 3 ? c - 1 : 1);
 }
-static_assert(part_bytes(0) + part_bytes(1) == kStageBytes, "the halves make up the stage");
+__host__ __device__ constexpr int tail_part(int pf) { return num_parts(pf) - 1; }
+__host__ __device__ constexpr bool part_begins(int c, int pf) {
+  return c == 0 || part_of_chunk(c, pf) != part_of_chunk(c - 1, pf);
+}
+__host__ __device__ constexpr bool part_ends(int c, int pf) {
+  return c == 3 || part_of_chunk(c, pf) != part_of_chunk(c + 1, pf);
+}
+__host__ __device__ constexpr int part_bytes(int part, int pf) {
+  int bytes = part == tail_part(pf) ? 2 * 4096 : 0;
+  for (int c = 0; c < 4; ++c) bytes += part_of_chunk(c, pf) == part ? kChunkBytes : 0;
+  return bytes;
+}
+static_assert(part_bytes(0, 0) + part_bytes(1, 0) == kStageBytes &&
+                  part_bytes(0, 3) + part_bytes(1, 3) + part_bytes(2, 3) == kStageBytes,
+              "the parts make up the stage");
 constexpr int kMaxThreads = 512;  // producer, 2 MMA issuers, query stager, 2-3 softmax warpgroups
 constexpr int kSoftmaxWarp0 = 4;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;        // 1 s
@@ -150,8 +166,8 @@ struct Misc {
   alignas(16) int grow[2][12];       // per tile parity and warp: some row's max moves
   alignas(16) int row_j[48];         // new-position index j of each row (very negative for padding)
   alignas(16) int row_off[48];       // j * H + h: the row's index among its sequence's rows
-  alignas(8) uint64_t kv_full[kStages][kParts];  // part landed (TMA transaction bytes)
-  uint64_t kv_free[kStages][kParts];             // part no longer read by any MMA
+  alignas(8) uint64_t kv_full[kStages][kMaxParts];  // part landed (TMA transaction bytes)
+  uint64_t kv_free[kStages][kMaxParts];             // part no longer read by any MMA
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2];   // P of tile g is written: p_full[g % 2] (the softmax may run a tile
                         // ahead of the value MMAs when P lives in the stage)
@@ -596,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s)
-      for (int c = 0; c < kParts; ++c) {
+      for (int c = 0; c < num_parts(PF); ++c) {
         mbar_init(&ms->kv_full[s][c], 1);
         mbar_init(&ms->kv_free[s][c], 1);
       }
@@ -774,11 +790,11 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     }
 #pragma unroll
     for (int c = 0; c < 5; ++c) {  // chunks 0..3, then the tail
-      const int part = c < 4 ? part_of_chunk(c) : kTailPart;
+      const int part = c < 4 ? part_of_chunk(c, PF) : tail_part(PF);
       uint64_t* full = &ms->kv_full[s][part];
-      if (c == 0 || c == 2) {  // a half begins
+      if (c < 4 && part_begins(c, PF)) {  // a part begins
         if (!wait_or_abort(&ms->kv_free[s][part], (n & 1) ^ 1, ms, p)) return false;
-        mbar_arrive_expect_tx(full, part_bytes(part));
+        mbar_arrive_expect_tx(full, part_bytes(part, PF));
       }
       if (c < 4) {
 #pragma unroll
@@ -889,7 +905,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       }
       // Drain: wait (bounded) until the consumers released every part still holding a load.
       for (uint32_t f = (fill > kStages ? fill - kStages : 0); f < fill; ++f)
-        for (int c = 0; c < kParts; ++c)
+        for (int c = 0; c < num_parts(PF); ++c)
           mbar_wait(&ms->kv_free[f % kStages][c], (f / kStages) & 1, kWaitLimitNs);
     }
   } else if (warp == 1) {
@@ -925,8 +941,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           // each latent chunk as soon as it has landed, then the RoPE tail
 #pragma unroll
           for (int c = 0; c < 4 && ok; ++c) {
-            if (c == 0 || c == 2) {  // a half has landed
-              if (!(ok = by.same(wait_or_abort(&ms->kv_full[s][part_of_chunk(c)], ph, ms, p)))) break;
+            if (part_begins(c, PF)) {  // a part has landed
+              if (!(ok = by.same(wait_or_abort(&ms->kv_full[s][part_of_chunk(c, PF)], ph, ms, p)))) break;
               tc_fence_after();
             }
 #pragma unroll
@@ -934,7 +950,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
               by.mma(d, by.at(a_main0, am, (c * kChunkBytes + kk * 32) >> 4),
                      by.at(b_main0, bm, (c * (C::NQK * 128) + kk * 32) >> 4), idesc_qk, (c | kk) != 0);
           }
-          if (!ok) break;  // the tail belongs to the second half, landed by now
+          if (!ok) break;  // the tail belongs to the last part, landed by now
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
             by.mma(d, by.at(a_tail0, at, (kk * 32) >> 4), by.at(b_tail0, bt, (kk * 32) >> 4), idesc_qk, 1);
@@ -992,7 +1008,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                          t > 0 || ks > 0 || term > 0);
               }
             }
-            if (c == 1 || c == 3) by.commit(&ms->kv_free[s][part_of_chunk(c)]);
+            if (part_ends(c, PF)) by.commit(&ms->kv_free[s][part_of_chunk(c, PF)]);
           }
         }
       }
@@ -1082,7 +1098,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     int pv_seen = -1;
     auto wait_pv_upto = [&](int target) -> bool {
       for (int g = pv_seen + 1; g <= target; ++g) {
-        if (!warp_wait(&ms->kv_free[g % kStages][kParts - 1], (g / kStages) & 1)) return false;
+        if (!warp_wait(&ms->kv_free[g % kStages][tail_part(PF)], (g / kStages) & 1)) return false;
         pv_seen = g;
       }
       return true;
