@@ -390,12 +390,16 @@ __global__ void __launch_bounds__(kAcThreads, 2) accept_kernel(const __grid_cons
 
 }  // namespace
 
-cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s) {
+cudaError_t launch_accept(const AcceptArgs& a, int num_sms, cudaStream_t s) {
   const bool vec = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.target) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(a.draft) % 16 == 0;
-  // CTAs a sequence: a warp has at least one step of its own
+  // CTAs a sequence: eight, fewer where all sequences' would not run at once (two an SM: the walk
+  // and the exchange are waited for once a wave; 64 sequences of 129,280 tokens with draft
+  // probabilities: 20.5 us a call with eight, 18.4 us with four) or where a warp would have no step of
+  // its own
   const int steps = (a.V + kAcStep - 1) / kAcStep;
-  const int ctas = min(kAcCluster, (steps + kAcWarps - 1) / kAcWarps);
+  int ctas = kAcCluster;
+  while (ctas > 1 && ((int64_t)a.B * ctas > 2 * num_sms || (ctas / 2) * kAcWarps >= steps)) ctas /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas, (unsigned)a.B);
   cfg.blockDim = dim3(kAcThreads);

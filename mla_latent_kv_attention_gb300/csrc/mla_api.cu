@@ -524,7 +524,12 @@ mla_status_t mla_accept_drafts(const float* target, const int32_t* tokens, const
   a.out_tokens = out_tokens;
   a.path = path;
   a.num_accepted = num_accepted;
-  if (mla::launch_accept(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+  int dev;
+  mla_status_t st = current_device(&dev);
+  if (st != MLA_OK) return st;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return MLA_ERR_CUDA;
+  if (mla::launch_accept(a, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;
   }

@@ -276,7 +276,7 @@ struct AcceptArgs {
   int32_t* path;           // [B][n]
   int32_t* num_accepted;   // [B]
 };
-cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s);
+cudaError_t launch_accept(const AcceptArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_mha_prefill(const MhaArgs& a, int num_sms, cudaStream_t s, int* launches);
 cudaError_t launch_mha_projection(const void* latent, const void* w, void* kvup, int L, int H,
                                   float kv_scale, int precise, unsigned* status, cudaStream_t s);
