@@ -552,12 +552,13 @@ __device__ __forceinline__ void stage_rows(const AttnParams& p, int R, const int
   }
 }
 
-// How the two issuing warps run. One thread each: lane 0 alone walks the tiles. Tree: the whole
-// warp does, and an elected lane issues. The control flow and the operands are then the same for
-// every lane as far as the compiler can tell (votes and broadcasts say so), so it keeps the
-// descriptors, of which only the low half moves, in the uniform registers that the MMA
-// reads, instead of moving eight registers there for each one: 32 x 32 nodes over 4K-16K 315 ->
-// 291 us.
+// How the producer and the two issuing warps run. One thread each: lane 0 alone walks the tiles.
+// Tree: the whole warp does, and an elected lane issues. The control flow and the operands are
+// then the same for every lane as far as the compiler can tell (votes and broadcasts say so), so
+// it keeps them (of a descriptor only the low half moves) in the uniform registers that the MMA
+// and the TMA read, instead of moving up to eight registers there for each one. All three lie on
+// the chain of a key stage (values done, load, scores): 32 x 32 nodes over 4K-16K 315 -> 291 us
+// for the MMAs, 281 -> 270 us for the loads.
 template <bool WARP>
 struct Issuer {
   uint32_t leader;
@@ -582,6 +583,13 @@ struct Issuer {
       mma_f8f6f4_by(leader, d, a, b, idesc, accumulate);
     else
       mma_f8f6f4(d, a, b, idesc, accumulate);
+  }
+  __device__ __forceinline__ void load(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                       uint64_t policy) const {
+    if constexpr (WARP)
+      tma_load_2d_hint_by(leader, dst, map, x, y, bar, policy);
+    else
+      tma_load_2d_hint(dst, map, x, y, bar, policy);
   }
   __device__ __forceinline__ void commit(uint64_t* bar) const {
     if (!WARP || leader) mma_commit(bar);
@@ -770,7 +778,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   // held it have released it.
   const int64_t rows64 = p.num_pages * (int64_t)p.page_size;
   const int total_rows = rows64 > 0x7fffff00 ? 0x7fffff00 : (int)rows64;
-  auto issue_tile = [&](const UnitInfo& un, int k0, uint32_t fill, uint64_t policy) -> bool {
+  auto issue_tile = [&](const Issuer<PF == 3>& by, const UnitInfo& un, int k0, uint32_t fill,
+                        uint64_t policy) -> bool {
     const int s = fill % kStages;
     const uint32_t n = fill / kStages;
     uint8_t* st = smem + C::kOffStages + s * C::kStageStride;
@@ -787,23 +796,24 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         else
           report(ms, MLA_ERR_BOUNDS);
       }
+      y[h] = (int)by.same((uint32_t)y[h]);
     }
 #pragma unroll
     for (int c = 0; c < 5; ++c) {  // chunks 0..3, then the tail
       const int part = c < 4 ? part_of_chunk(c, PF) : tail_part(PF);
       uint64_t* full = &ms->kv_full[s][part];
       if (c < 4 && part_begins(c, PF)) {  // a part begins
-        if (!wait_or_abort(&ms->kv_free[s][part], (n & 1) ^ 1, ms, p)) return false;
-        mbar_arrive_expect_tx(full, part_bytes(part, PF));
+        if (!by.same(wait_or_abort(&ms->kv_free[s][part], (n & 1) ^ 1, ms, p))) return false;
+        if (by.leader) mbar_arrive_expect_tx(full, part_bytes(part, PF));
       }
       if (c < 4) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          tma_load_2d_hint(st + c * kChunkBytes + h * 8192, &map_main, c * 128, y[h], full, policy);
+          by.load(st + c * kChunkBytes + h * 8192, &map_main, c * 128, y[h], full, policy);
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          tma_load_2d_hint(st + C::kTail + h * 4096, &map_tail, 0, y[h], full, policy);
+          by.load(st + C::kTail + h * 4096, &map_tail, 0, y[h], full, policy);
       }
     }
     return true;
@@ -815,14 +825,16 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   const uint64_t read_once = (is_prefill(PF) || (PF == 3 && p.team * p.passes > 1)) ? l2_policy_evict_normal()
                                                                           : l2_policy_evict_first();
   // The first unit's first tiles go out from here, straight after the plan: on the way to
-  // the producer's loop a cold kernel spends microseconds fetching instructions.
+  // the producer's loop a cold kernel spends microseconds fetching instructions. (Tree: nothing
+  // stands between the two, and 10 KB less code, which the tile loops compete with for the
+  // instruction caches, is worth more: 32 x 32 nodes 288 -> 281 us.)
   uint32_t early = 0;
-  if (threadIdx.x == 0 && !p.test_stall) {
+  if (PF != 3 && threadIdx.x == 0 && !p.test_stall) {
     const Cursor c0 = first_unit<PF>(args, ms);
     if (has_unit<PF>(args, ms, c0)) {
       const UnitInfo u0 = unit_info<PF>(args, ms, c0);
       for (int k0 = u0.key_lo; k0 < u0.key_hi && early < (uint32_t)kStages; k0 += kTileKeys) {
-        if (!issue_tile(u0, k0, early, read_once)) break;
+        if (!issue_tile(Issuer<PF == 3>(), u0, k0, early, read_once)) break;
         ++early;
       }
     }
@@ -859,7 +871,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    const Issuer<PF == 3> by;
+    if (by.runs(lane)) {
       uint32_t fill = 0;  // tiles issued so far (the first `early` ones in the prologue)
       // L2 prefetch cursor: runs kPrefetchTiles tiles ahead of the TMA loads so that they
       // find their pages in L2 (deeper than the two shared-memory stages allow). The first
@@ -883,7 +896,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
               const int phys = p.page_table[(int64_t)pu.b * p.pt_stride + kk / p.page_size];
               if (phys >= 0 && phys < p.num_pages) {
                 const int rows = min(64, pu.key_hi - kk);
-                bulk_prefetch_l2(p.pool + ((int64_t)phys * p.page_size + kk % p.page_size) * kD,
+                if (by.leader) bulk_prefetch_l2(p.pool + ((int64_t)phys * p.page_size + kk % p.page_size) * kD,
                                  (uint32_t)rows * kD);
               }
             }
@@ -893,11 +906,13 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         }
       };
       prefetch_upto(kStages, false);
-      for (Cursor cu = first_unit<PF>(args, ms); has_unit<PF>(args, ms, cu) && !aborted(ms) && !p.test_stall;
+      for (Cursor cu = first_unit<PF>(args, ms);
+           by.same(has_unit<PF>(args, ms, cu) && !aborted(ms) && !p.test_stall);
            cu = next_unit<PF>(args, cu)) {
         const UnitInfo un = unit_info<PF>(args, ms, cu);
-        for (int k0 = un.key_lo; k0 < un.key_hi; k0 += kTileKeys) {
-          const bool ok = fill < early || issue_tile(un, k0, fill, read_once);
+        const int key_hi = (int)by.same((uint32_t)un.key_hi);
+        for (int k0 = (int)by.same((uint32_t)un.key_lo); k0 < key_hi; k0 += kTileKeys) {
+          const bool ok = fill < early || issue_tile(by, un, k0, fill, read_once);
           if (!ok) break;
           ++fill;
           prefetch_upto(fill + kPrefetchTiles, true);

@@ -129,6 +129,17 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// tma_load_2d_hint by the lane whose `issue` is set, in code that the whole warp runs.
+__device__ __forceinline__ void tma_load_2d_hint_by(uint32_t issue, void* dst, const CUtensorMap* map,
+                                                    int x, int y, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %6, 0;\n"
+      " @q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;\n}\n" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(policy), "r"(issue)
+      : "memory");
+}
+
 // L2 policy for data read once: its lines are the first to go when L2 needs room.
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t policy;
