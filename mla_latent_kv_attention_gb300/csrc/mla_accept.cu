@@ -260,21 +260,21 @@ __global__ void __launch_bounds__(kAcThreads, 2) accept_kernel(const __grid_cons
   __syncwarp();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   for (int round = 0;; ++round) {
-    int hi = 0, lo = 0;
     long long sum = 0;
     for (int at = w0; at < w1; at += kSteps * kAcStep) {
       float w[kSteps][4];
       load(at, w);
+      int hi = 0, lo = 0;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // (at most 2^7 a lane: 2^27 and 2^29)
+        for (int e = 0; e < 4; ++e) {  // (32 at most, each within 2^20 and 2^22)
           const Weight x = split_weight(w[k][e]);
           hi += x.hi;
           lo += x.lo;
         }
+      sum += whole_weight({hi, lo});
     }
-    sum = whole_weight({hi, lo});
     if (lane == 0)
       for (unsigned long long m = out_of_span; m; m &= m - 1)
         sum -= whole_weight(split_weight(prow[s.kid[__ffsll((long long)m) - 1]]));

@@ -108,6 +108,20 @@ def test_vocabularies(V):
     check(*inputs(2, 5, V, True, False, seed=2))
 
 
+@pytest.mark.parametrize("B", [1, 40, 310])
+@pytest.mark.parametrize("w", [2.0 ** -21 * (1 - 2.0 ** -10), 2.0 ** -21 * (1 + 2.0 ** -10), 2.0 ** -19])
+def test_largest_rows_of_equal_weights(B, w):
+    """Every weight of a row of 2^19 the same, where the fine halves of the sums are largest (to
+    either side); one CTA a sequence, several, eight."""
+    V = 1 << 19
+    p = torch.full((B, 1, V), w, device=DEV)
+    u = torch.rand(B, 2, generator=torch.Generator().manual_seed(B))
+    out, _, _ = mla.mla_accept_drafts(p, torch.zeros(B, 1, dtype=torch.int32, device=DEV), u.to(DEV))
+    W = int(weight(np.float32(w)))
+    want = [(V * W * uniform(x, 31) >> 31) // W for x in u[:, 1].numpy()]
+    assert out[:, 0].tolist() == want
+
+
 def test_many_sequences():
     _, _, count = check(*inputs(300, 6, 2000, False, True, seed=3))
     assert 0 < count.mean() < 5 and count.max() == 5  # every outcome, all drafts accepted among them
