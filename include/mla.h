@@ -93,7 +93,8 @@ typedef struct mla_kv {
 /*
  * Bytes of workspace the given call needs on `device` (a CUDA ordinal). The workspace
  * holds the per-split partial outputs, staged query rows and one status word per CTA (it
- * depends on H, n_q and the SM count, not on B); it must be 256-byte aligned and stay untouched until the call's
+ * depends on H, n_q and the SM count, not on B, except for MLA_OP_VERIFY_TREE, which stages every
+ * query row, in groups of 16, 32 or 48: 1.2 KB a row of a full group); it must be 256-byte aligned and stay untouched until the call's
  * work has finished on its stream. Its contents need no initialisation: every call
  * rewrites all it later reads (zero-fill it once if mla_read_status may run before the
  * first call). For MLA_OP_PREFILL pass B = 1 and n_q = T, for MLA_OP_VERIFY_TREE n_q = the
@@ -347,7 +348,8 @@ mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
  *   lse        device, [B][n][H] float32, or NULL
  *   workspace  mla_workspace_size(MLA_OP_VERIFY_TREE, B, H, n, device) bytes
  * Numerics, errors and the split of long sequences as mla_verify. More than 48 rows (n * H)
- * run as groups of whole nodes, each of which reads the sequence's keys.
+ * run as groups of whole nodes, each of which walks the sequence's keys beside the others.
+ * Three launches: the query rows staged for the tensor cores, the attention, the merge.
  */
 mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, int H, float sm_scale,
                              const uint64_t* tree_mask, void* out, float* lse, void* workspace,

@@ -147,11 +147,12 @@ class KVCache:
 
     def c_struct(self) -> mla_kv_t:
         pool, table, lens = self.pool, self.page_table, self.seq_lens
-        for name, t in (("pool", pool), ("page_table", table), ("seq_lens", lens)):
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"KVCache.{name} must be a contiguous CUDA tensor")
-            if t.get_device() != pool.get_device():
-                raise ValueError(f"KVCache.{name} must be on the pool's device")
+        if not (pool.is_contiguous() and table.is_contiguous() and lens.is_contiguous() and
+                pool.get_device() == table.get_device() == lens.get_device() >= 0):
+            for name, t in (("pool", pool), ("page_table", table), ("seq_lens", lens)):
+                if not t.is_cuda or not t.is_contiguous():
+                    raise ValueError(f"KVCache.{name} must be a contiguous CUDA tensor")
+            raise ValueError("KVCache tensors must be on one device")
         if pool.dtype is not _U8 or table.dtype is not _I32 or lens.dtype is not _I32:
             raise TypeError("KVCache dtypes: pool uint8, page_table int32, seq_lens int32")
         pages, size, _ = pool.shape
@@ -479,11 +480,12 @@ def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_sc
         lse = torch.empty((B, n, H), dtype=_F32, device=dev)
     else:
         _dense(lse, "lse", _F32, (B, n, H), dev)
-    ws = workspace(MLA_OP_VERIFY_TREE, B, H, n, dev) if ws is None else ws
+    if ws is None:
+        ws = workspace(MLA_OP_VERIFY_TREE, B, H, n, dev)
+    elif ws.dtype is not _U8 or not ws.is_contiguous() or ws.device != dev:
+        raise ValueError("ws must be a contiguous uint8 tensor on q's device")
     if kv.seq_lens.shape[0] < B or kv.page_table.shape[0] < B or kv.pool.device != dev:
         raise ValueError("kv must describe q's sequences, on q's device")
-    if not ws.is_contiguous() or ws.dtype is not _U8 or ws.device != dev:
-        raise ValueError("ws must be a contiguous uint8 tensor on q's device")
     _check("mla_verify_tree", library().mla_verify_tree(
         kv.c_struct(), q.data_ptr(), B, n, H, sm_scale,
         _dense(tree_mask, "tree_mask", _I64, (B, n), dev), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
