@@ -1632,6 +1632,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 // decode does: 77 KB of its code, fetched cold on the way to the first scores, and one warp for a
 // CTA's later units, 28 us each: 64 sequences of 64 nodes of 16 heads on 100 to 130 keys took
 // 305 us, 175 us this way; 8 nodes of 12 heads on 1,024 keys 22.1 and 20.3 us.)
+// Bound: one round of loads and cold code (32 groups of 48 rows 6.9 us alone with cold caches,
+// behind which the attention kernel's start hides most).
 template <int RP>
 __global__ void __launch_bounds__(512) stage_queries_kernel(const __grid_constant__ AttnParams p) {
   __shared__ int row_off[48];
