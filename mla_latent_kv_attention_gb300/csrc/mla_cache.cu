@@ -69,9 +69,9 @@ __global__ void __launch_bounds__(256) cache_append_kernel(uint8_t* __restrict__
 //
 // The frequencies lie in the parameters, where the 32 lanes' different addresses are read one
 // after another: one warp of the CTA copies them to shared memory while every warp's row is on
-// its way (8,192 rows 5.3 -> 4.3 us; copied before the loads 5.1). Bound: 32,768 rows take 11.2 us
-// (56.6 MB, 5.0 TB/s), 8,192 take 4.3 (3.3 TB/s, the launch and a round of loads among it), 32
-// take 2.1, the launch.
+// its way (8,192 rows 5.3 -> 4.3 us; copied before the loads 5.1). Bound: L2 or HBM for many rows
+// (32,768 in L2: 11.2 us, 56.6 MB, 5.0 TB/s), the launch and a round of loads for fewer (8,192
+// 4.3 us in L2 and 6.6 us from HBM), the launch alone for 32 (2.1 us).
 __global__ void __launch_bounds__(256, 4)  // (four: 8,192 rows 4.3 us; left open 4.85, six 4.9)
     cache_append_rope_kernel(const __grid_constant__ AppendRopeArgs a,
                              const __grid_constant__ mla_rope_t rope) {

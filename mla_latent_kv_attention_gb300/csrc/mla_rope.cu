@@ -4,8 +4,8 @@
 // A thread takes a quarter of a token's 64 dims (eight pairs, two 16-byte vectors) and turns it
 // in several heads: the eight angles belong to the token, so their cosines and sines are
 // computed once for all the heads that the thread takes. Bound: 256 bytes a head through L2 and
-// HBM when there are many tokens (8,192 of 12 heads: 25.2 MB in 4.4 to 5.4 us by layout, 4.6 to 5.7
-// TB/s), the launch when there are few (32: 1.9 us).
+// HBM when there are many tokens (8,192 of 12 heads, 25.2 MB: 4.5 us in L2, 6.5 us and 3.9 TB/s
+// from HBM), the launch when there are few (32: 1.9 us).
 #include <cuda_bf16.h>
 #include <math.h>
 
