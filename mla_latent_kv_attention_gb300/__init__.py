@@ -2,7 +2,10 @@
 
 A thin ctypes binding over ``libmla.so`` (C ABI in ``include/mla.h``). The functions
 carry the C names and only marshal arguments: torch CUDA tensors become device
-pointers, the current torch stream becomes the ``cudaStream_t``. Every step of the
+pointers, the current torch stream becomes the ``cudaStream_t``. mla_rope,
+mla_cache_append_rope, mla_cache_gather, mla_verify_tree and mla_accept_drafts, when given
+a ``stream``, make it the current one for the call: what they allocate belongs to it, as
+after ``with torch.cuda.stream(stream)``. Every step of the
 attention runs in the library's CUDA kernels; there is no other implementation, and
 every entry point raises ImportError when the library is missing (the seeded workload
 and accounting modules import without it).
@@ -349,11 +352,16 @@ def mla_top_k_renorm_prob(probs: torch.Tensor, top_k, out: Optional[torch.Tensor
     return out
 
 
-def _on(dev: torch.device, stream) -> int:
-    """The raw stream for a call on tensors of device `dev` (which has to be the current one:
-    the library launches on the current device)."""
-    if stream is not None:
-        return _stream(stream)
+def _current(stream):
+    """Makes `stream` (a torch stream or a raw handle) and its device the current ones, so that
+    what a call allocates belongs to the stream that the call runs on."""
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
+                             torch.cuda.ExternalStream(int(stream)))
+
+
+def _on(dev: torch.device) -> int:
+    """The raw current stream for a call on tensors of device `dev` (which has to be the current
+    one: the library launches on the current device)."""
     index = torch._C._cuda_getDevice()
     if dev.index != index:
         raise ValueError(f"tensors on {dev}, but cuda:{index} is the current device "
@@ -400,6 +408,9 @@ def mla_rope(rope: mla_rope_t, x: torch.Tensor, positions: torch.Tensor, out=Non
              stream=None) -> torch.Tensor:
     """Rotate x [n, H, 64] bf16 (a view of the RoPE dims, e.g. q[..., 512:] or q_mha[..., 128:])
     to positions int64 [n]. `out` may be another such view, or x itself (in place)."""
+    if stream is not None:
+        with _current(stream):
+            return mla_rope(rope, x, positions, out)
     n, H, xt, xh = _rope_part(x, "x")
     dev = x.device
     if out is None:
@@ -409,7 +420,7 @@ def mla_rope(rope: mla_rope_t, x: torch.Tensor, positions: torch.Tensor, out=Non
         raise ValueError("out must have x's shape and device, and a place of its own for every element")
     _check("mla_rope", library().mla_rope(
         rope, x.data_ptr(), xt, xh, _dense(positions, "positions", _I64, (n,), dev), n, H,
-        out.data_ptr(), ot, oh, _on(dev, stream)))
+        out.data_ptr(), ot, oh, _on(dev)))
     return out
 
 
@@ -421,6 +432,9 @@ def mla_cache_append_rope(pool: torch.Tensor, x: torch.Tensor, slots: torch.Tens
     latent is normalised by its root mean square and weighted with norm_weight [512] bf16
     (None: as it is), the 64 RoPE dims are turned to positions int64 [n] (rope None: as they
     are), and both are quantised in one pass. x may be a slice of a wider projection's rows."""
+    if stream is not None:
+        with _current(stream):
+            return mla_cache_append_rope(pool, x, slots, kv_scale, rope, positions, norm_weight, eps, status)
     if pool.dtype is not _U8 or pool.dim() != 3 or not pool.is_contiguous() or not pool.is_cuda or \
             pool.shape[2] != MLA_D:
         raise ValueError("pool must be a contiguous uint8 CUDA tensor [num_pages, page_size, 576]")
@@ -437,7 +451,7 @@ def mla_cache_append_rope(pool: torch.Tensor, x: torch.Tensor, slots: torch.Tens
         _dense(slots, "slots", _I64, (n,), dev), n, kv_scale,
         None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, (MLA_DV,), dev),
         eps, rope, None if positions is None else _dense(positions, "positions", _I64, (n,), dev),
-        _status_ptr(status, dev), _on(dev, stream)))
+        _status_ptr(status, dev), _on(dev)))
 
 
 def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optional[torch.Tensor] = None,
@@ -446,6 +460,9 @@ def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optiona
     """Cached rows read back and dequantised: rows cu_rows[b] .. cu_rows[b + 1] - 1 of out
     [n, 576] (bf16 or float32) are positions starts[b], starts[b] + 1, ... of sequence b.
     cu_rows int64 [B + 1], starts int32 [B] (None: 0); rows outside them stay as they were."""
+    if stream is not None:
+        with _current(stream):
+            return mla_cache_gather(kv, cu_rows, n, starts, out, dtype, status)
     c = kv.c_struct()
     dev = kv.pool.device
     B = cu_rows.shape[0] - 1
@@ -461,7 +478,7 @@ def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optiona
         _dense(out, "out", _F32 if f32 else _BF16, (n, MLA_D), dev)
     _check("mla_cache_gather", library().mla_cache_gather(
         c, B, None if starts is None else _dense(starts, "starts", _I32, (B,), dev), cu_ptr, n,
-        out.data_ptr(), f32, _status_ptr(status, dev), _on(dev, stream)))
+        out.data_ptr(), f32, _status_ptr(status, dev), _on(dev)))
     return out
 
 
@@ -469,6 +486,9 @@ def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_sc
                     lse=None, ws=None, stream=None):
     """q [B, n, H, 576] bf16 of a tree's n <= 64 nodes -> (out [B, n, H, 512] bf16, lse [B, n, H]
     fp32). Every node sees the prefix and the nodes whose bit its tree_mask (int64 [B, n]) sets."""
+    if stream is not None:
+        with _current(stream):
+            return mla_verify_tree(kv, q, tree_mask, sm_scale, out, lse, ws)
     _q_check(q, 4)
     B, n, H, _ = q.shape
     dev = q.device
@@ -489,7 +509,7 @@ def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_sc
     _check("mla_verify_tree", library().mla_verify_tree(
         kv.c_struct(), q.data_ptr(), B, n, H, sm_scale,
         _dense(tree_mask, "tree_mask", _I64, (B, n), dev), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-        ws.numel(), _on(dev, stream)))
+        ws.numel(), _on(dev)))
     return out, lse
 
 
@@ -501,6 +521,9 @@ def mla_accept_drafts(target_probs: torch.Tensor, tokens: torch.Tensor, uniforms
     uniforms float32 [B, n + 1] in [0, 1), parents int32 [B, n] (None: a chain), draft_probs
     float32 [B, n - 1, V] (chains: what tokens[:, 1:] were drawn from). Returns int32 tensors
     (out_tokens [B, n], path [B, n], num_accepted [B]); unused places hold -1."""
+    if stream is not None:
+        with _current(stream):
+            return mla_accept_drafts(target_probs, tokens, uniforms, parents, draft_probs)
     if target_probs.dim() != 3 or not target_probs.is_cuda:
         raise ValueError("target_probs must be a CUDA tensor [B, n, V]")
     B, n, V = target_probs.shape
@@ -514,7 +537,7 @@ def mla_accept_drafts(target_probs: torch.Tensor, tokens: torch.Tensor, uniforms
         None if parents is None else _dense(parents, "parents", _I32, (B, n), dev),
         None if draft_probs is None else _dense(draft_probs, "draft_probs", _F32, (B, n - 1, V), dev),
         _dense(uniforms, "uniforms", _F32, (B, n + 1), dev), B, n, V, out_tokens.data_ptr(),
-        path.data_ptr(), num_accepted.data_ptr(), _on(dev, stream)))
+        path.data_ptr(), num_accepted.data_ptr(), _on(dev)))
     return out_tokens, path, num_accepted
 
 
