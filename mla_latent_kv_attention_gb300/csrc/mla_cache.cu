@@ -150,14 +150,14 @@ __global__ void __launch_bounds__(256, 4)  // (four: 8,192 rows 4.3 us; left ope
 
 // Cached rows back into a dense array. A CTA takes 32 consecutive output rows: first a thread a
 // row finds its sequence (binary search in cu_rows), its page and the pool row, then the threads
-// move the rows 8 codes at a time (72 pieces a row, 4 rows a round), every load of a thread in
-// flight before its first store. HBM-bound: 576 bytes read and 1,152 (bf16) or 2,304 (float32)
-// written a row; 8 x 32,768 rows to bf16 in 70 us (453 MB, 6.5 TB/s, 0.95 of the measured copy),
-// 8 x 333 in 3.9 us (the launch and three dependent loads).
+// move the rows 16 bytes of output at a time (8 codes to bf16, four rows a round, or 4 codes to
+// float32, two rows a round: a warp's stores are whole lines), every load of a thread in flight
+// before its first store. HBM-bound: 576 bytes read and 1,152 (bf16) or 2,304 (float32) written a
+// row: 8 x 32,768 rows to bf16 in 70 us (453 MB, 6.5 TB/s, 0.95 of the measured copy), 66,000 rows
+// to float32 in 32.8 us (190 MB, 5.8 TB/s; with 8 codes a thread, two stores each, 44.2 us), 8 x
+// 333 to bf16 in 3.9 us (the launch and three dependent loads).
 constexpr int kGatherRows = 32;
-constexpr int kGatherPieces = kD / 8;                // 8-code pieces of a row
-constexpr int kGatherThreads = 4 * kGatherPieces;    // four rows a round
-constexpr int kGatherRounds = kGatherRows / 4;
+constexpr int kGatherThreads = 288;
 constexpr int64_t kRowSkip = -1, kRowBad = -2;
 
 template <typename Out>
@@ -190,30 +190,42 @@ __global__ void __launch_bounds__(kGatherThreads)
     s_row[threadIdx.x] = from;
   }
   __syncthreads();
-  const int r = threadIdx.x / kGatherPieces, piece = threadIdx.x % kGatherPieces;
-  uint2 code[kGatherRounds];
+  constexpr int kCodes = 16 / sizeof(Out);          // a thread's piece of a row
+  constexpr int kPieces = kD / kCodes;
+  constexpr int kAtOnce = kGatherThreads / kPieces;  // rows a round
+  constexpr int kRounds = kGatherRows / kAtOnce;
+  const int r = threadIdx.x / kPieces, piece = threadIdx.x % kPieces;
+  uint32_t code[kRounds][kCodes / 4];
 #pragma unroll
-  for (int k = 0; k < kGatherRounds; ++k) {
-    const int64_t from = s_row[4 * k + r];
-    code[k] = make_uint2(0u, 0u);
-    if (from >= 0) code[k] = __ldcs(reinterpret_cast<const uint2*>(kv.pool + from * kD) + piece);
+  for (int k = 0; k < kRounds; ++k) {
+    const int64_t from = s_row[kAtOnce * k + r];
+#pragma unroll
+    for (int e = 0; e < kCodes / 4; ++e) code[k][e] = 0u;
+    if (from < 0) continue;
+    const uint8_t* src = kv.pool + from * kD + kCodes * piece;
+    if constexpr (kCodes == 8) {
+      const uint2 c = __ldcs(reinterpret_cast<const uint2*>(src));
+      code[k][0] = c.x;
+      code[k][kCodes / 4 - 1] = c.y;
+    } else {
+      code[k][0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
+    }
   }
 #pragma unroll
-  for (int k = 0; k < kGatherRounds; ++k) {
-    if (s_row[4 * k + r] == kRowSkip) continue;
-    const uint32_t w[4] = {code[k].x & 0xFFFFu, code[k].x >> 16, code[k].y & 0xFFFFu, code[k].y >> 16};
-    float2 v[4];
+  for (int k = 0; k < kRounds; ++k) {
+    if (s_row[kAtOnce * k + r] == kRowSkip) continue;
+    float2 v[kCodes / 2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[e], __NV_E4M3);
+    for (int e = 0; e < kCodes / 2; ++e) {
+      const uint32_t two = (e & 1) ? code[k][e / 2] >> 16 : code[k][e / 2] & 0xFFFFu;
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
       v[e] = __half22float2(*reinterpret_cast<const __half2*>(&h));
       v[e].x *= kv.kv_scale;
       v[e].y *= kv.kv_scale;
     }
-    Out* dst = out + (row0 + 4 * k + r) * kD + 8 * piece;
-    if constexpr (sizeof(Out) == 4) {
+    Out* dst = out + (row0 + kAtOnce * k + r) * kD + kCodes * piece;
+    if constexpr (kCodes == 4) {
       __stcs(reinterpret_cast<float4*>(dst), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
-      __stcs(reinterpret_cast<float4*>(dst) + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
     } else {
       uint32_t o[4];
 #pragma unroll
