@@ -217,7 +217,9 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
   p.qimg = reinterpret_cast<uint8_t*>(base + w.qimg);
   p.qimg_stride = (int64_t)w.qimg_stride;
   const unsigned long long teams = (unsigned long long)(sms / g.team);
+  const unsigned long long fewer = (unsigned long long)mla::fewer_ranges((int)teams);
   p.teams_inv = teams > 1 ? ~0ull / teams + 1 : 0;
+  p.fewer_inv = fewer > 1 ? ~0ull / fewer + 1 : 0;
   p.num_ctas = (int)teams * g.team;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_mark(g_prof_start, s);

@@ -722,12 +722,15 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     long long pre = before + incl - mine;
     long long x0, x1;
     if constexpr (PF == 3) {
-      // A tree's ranges belong to teams of CTAs. range_lo's quotients by the reciprocal: exact, as
-      // c * total is below 2^64 / teams (and less code than 64-bit divisions, which a short
-      // call fetches cold; the same goes for the plan's loops not being unrolled).
-      const unsigned c = blockIdx.x / p.team;
-      x0 = (long long)__umul64hi(c * (unsigned long long)total, p.teams_inv);
-      x1 = p.teams_inv ? (long long)__umul64hi((c + 1) * (unsigned long long)total, p.teams_inv) : total;
+      // A tree's ranges belong to teams of CTAs (tree_ranges). range_lo's quotients by the
+      // reciprocal: exact, as c * total is below 2^64 / teams (and less code than 64-bit divisions,
+      // which a short call fetches cold; the same goes for the plan's loops not being unrolled).
+      const unsigned c = blockIdx.x / p.team, teams = gridDim.x / p.team;
+      const unsigned n = tree_ranges(total, teams);
+      const unsigned long long inv = n == teams ? p.teams_inv : p.fewer_inv;
+      x0 = (long long)__umul64hi(c * (unsigned long long)total, inv);
+      x1 = inv ? (long long)__umul64hi((c + 1) * (unsigned long long)total, inv) : total;
+      if (c >= n) x0 = x1 = total;  // a team without a range
     } else {
       const long long n = gridDim.x, c = blockIdx.x;
       x0 = total > 0 ? range_lo(c, total, n) : 0;

@@ -149,7 +149,7 @@ struct AttnParams {
   // sequences (`passes` each), R the rows of a full group of group_nodes nodes, n_q all nodes.
   const uint64_t* tree_mask;  // [sequences][n_q]
   int group_nodes, team, passes;
-  unsigned long long teams_inv;  // ceil(2^64 / teams), 0 for one team
+  unsigned long long teams_inv, fewer_inv;  // ceil(2^64 / n), 0 for n = 1: n = teams, n = fewer_ranges
   unsigned long long* trace;  // profiling hook: kTraceWords globaltimer stamps per CTA, or null
   int trace_ctas;             // CTAs the trace buffer has room for
 };
@@ -175,6 +175,17 @@ __host__ __device__ __forceinline__ int64_t range_lo(int64_t c, int64_t total, i
 }
 __host__ __device__ __forceinline__ int64_t range_of(int64_t x, int64_t total, int64_t n) {
   return ((x + 1) * n + total - 1) / total - 1;
+}
+
+// Ranges of a tree's cost axis: one a team, or two teams in three where that leaves a range less
+// than kFewCost units: the merge then has fewer pieces, and starts on the SMs that are left. In us
+// with all teams / two in three (12 heads): 8 nodes on 1,024 keys 19.0 / 16.8, 8 sequences of 8 on
+// 2K keys 29.9 / 25.5, 12 of 4 on 6K (4.1 units a range) 36.2 / 32.8, 24 of 6 (8 heads) on 3K (4.6)
+// 33.1 / 33.1; 17 of 20 on 0.2K to 0.8K (5.3) 31.0 / 32.3, 64 of 4 on 1.2K (6.3) 34.1 / 37.5.
+constexpr int kFewCost = 5;
+__host__ __device__ __forceinline__ int fewer_ranges(int teams) { return (2 * teams + 2) / 3; }
+__host__ __device__ __forceinline__ int tree_ranges(int64_t total, int teams) {
+  return total < (int64_t)kFewCost * teams ? fewer_ranges(teams) : teams;
 }
 
 // Up-projected 16-bit columns per head in kvup: bf16 form 128 key + 128 value columns;

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
     if (gt == 0 && chunk == 0 && lse_out) *lse_out = -INFINITY;
     return;
   }
-  const int64_t n = TREE ? p.num_ctas / p.team : p.num_ctas;
+  const int64_t n = TREE ? tree_ranges(total, p.num_ctas / p.team) : p.num_ctas;
   const int64_t first = pre + kUnitCost;  // the sequence's first block
   // pieces: one per CTA range the sequence's blocks overlap (with fewer blocks than CTAs
   // every range holds at most one block)
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_tree_kernel(AttnParams
     return;
   }
   // the pieces and their slots, as in merge_split_kernel
-  const int64_t n = p.num_ctas / p.team;
+  const int64_t n = tree_ranges(total, p.num_ctas / p.team);
   const int64_t first = pre + kUnitCost;
   const int64_t c0 = range_of(first, total, n);
   const int count = (total >= n) ? (int)(range_of(first + num_blocks - 1, total, n) - c0 + 1)
@@ -501,9 +501,11 @@ cudaError_t launch_merge_tree(const AttnParams& p, int sequences, cudaStream_t s
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  // (a warp a row takes its pieces two at a time: with more than eight or so of them, eight warps
-  // a row; 192 rows of 38 pieces: 22 us against 8 us)
-  if (vec == 16 && p.num_ctas / p.team <= 8 * p.B) {
+  // (a warp a row takes its pieces two at a time: with more than a dozen of them, eight warps a
+  // row. Whole calls in us, this / that: 9 pieces a row 32.6 / 35.1 and 24.6 / 30.8, 13 pieces, or
+  // 9 of them where fewer_ranges applies, 39.4 / 38.2 and 30.5 / 34.0, 19 pieces 24.4 / 22.8 and 48.7
+  // / 37.9)
+  if (vec == 16 && p.num_ctas / p.team <= 13 * p.B) {
     const int chunks = (p.R + kMergeWarps - 1) / kMergeWarps;
     cfg.gridDim = dim3((unsigned)sequences * p.team * p.passes * chunks);
     return cudaLaunchKernelEx(&cfg, merge_tree_kernel, p, chunks);

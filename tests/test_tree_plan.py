@@ -64,6 +64,35 @@ def test_groups_teams_and_slots(seed):
                 assert all(a[2] == b[1] for a, b in zip(mine, mine[1:]))
 
 
+def tree_ranges(total, teams):
+    return (2 * teams + 2) // 3 if total < 5 * teams else teams
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_fewer_ranges_than_teams(seed):
+    """Little work in all: the axis cut into a range for two teams in three. The ranges, units and
+    merged pieces of that many; the teams from there on hold nothing."""
+    rng = random.Random(100 + seed)
+    few = 0
+    for _ in range(150):
+        B = rng.choice([1, 2, 3, 8, 40])
+        lens = [rng.choice([0, rng.randint(1, 300), rng.randint(1, 6000)]) for _ in range(B)]
+        teams = rng.choice([1, 2, 3, 4, 11, 19, 38, 50, 76, 152])
+        total = sum(blocks_of(L) + 5 for L in lens if L)
+        n = tree_ranges(total, teams)
+        assert 1 <= n <= teams and (n == teams or total < 5 * teams)
+        few += n < teams
+        check_decode(lens, n)
+        inv = (2 ** 64 - 1) // n + 1 if n > 1 else 0
+        for c in range(teams):
+            lo, hi = c * total * inv >> 64, ((c + 1) * total * inv >> 64) if inv else total
+            if c < n:
+                assert (lo, hi) == (c * total // n, (c + 1) * total // n)
+            else:
+                assert c * total < 2 ** 64  # (and the kernel replaces the range by an empty one)
+    assert 30 < few < 120
+
+
 def test_quotients_by_the_reciprocal():
     """floor(c * total / teams) as the high half of a 64-bit product with ceil(2^64 / teams)."""
     rng = random.Random(1)
