@@ -354,9 +354,12 @@ def mla_top_k_renorm_prob(probs: torch.Tensor, top_k, out: Optional[torch.Tensor
 
 def _current(stream):
     """Makes `stream` (a torch stream or a raw handle) and its device the current ones, so that
-    what a call allocates belongs to the stream that the call runs on."""
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
-                             torch.cuda.ExternalStream(int(stream)))
+    what a call allocates belongs to the stream that the call runs on. The handles 0 and 1
+    (cudaStreamLegacy) are the default stream's; torch would take a new stream from its pool for 0."""
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _on(dev: torch.device) -> int:
