@@ -169,7 +169,7 @@ __device__ __forceinline__ int plan_blocks(const AttnParams& p, int b) {
 // alone, where each of its rows' pieces sit: the lengths are inputs of the call, complete
 // before the attention kernel passed its own wait on the kernels before it, and only then
 // could this grid start. So after the wait the partials are loaded at once, and rows with
-// nothing to merge never wait. A following attention call launched the same way may be
+// nothing to merge (but the first CTA's) never wait. A following attention call launched the same way may be
 // scheduled from the wait on (its prologue overlaps this kernel, its inputs are read only
 // after this grid has completed).
 // Minimum resident CTAs an SM (register budget) of each instantiation, measured: two rows
@@ -246,8 +246,14 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
     total += s_red[w][0];
     pre += s_red[w][1 + g];
   }
-  if (TREE && blockIdx.x + blockIdx.y == 0)  // (as merge_tree_kernel)
+  // The first CTA waits for the attention grid whatever it has to merge: this grid must not
+  // complete before that one, for the sake of a programmatic dependent that waits for this one
+  // (the next call's attention kernel, which may use the same workspace). The dependent is let go
+  // first: it starts as the attention kernel's CTAs leave, as it does behind CTAs without work.
+  if (blockIdx.x + blockIdx.y == 0) {
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   const int64_t row = row0 + g;  // b * R + r
   if (row >= rows) return;
   const int chunk = blockIdx.y;
