@@ -183,7 +183,7 @@ struct Misc {
                         // ahead of the value MMAs when P lives in the stage)
   uint64_t q_full[2];   // query operand buffer holds its unit's terms
   uint64_t q_empty[2];  // the unit that used the buffer has finished its scores
-  uint64_t scale_read[2];  // tree: the softmax warps have read the unit's row_scale (by parity)
+  uint64_t scale_read[2];  // the softmax warps have read the unit's row_scale (by parity)
   uint64_t q0_done;     // the first unit's query rows are staged (by warps 2.. together)
   uint64_t q1_done;     // the second unit's rows are in this CTA's global query image
   uint64_t wg_bar[3];  // bounded barriers of the softmax warpgroups (128 arrivals)
@@ -1081,7 +1081,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       // k waits until the softmax warps have seen the copy that used this buffer before (or q_full
       // would run two phases ahead of them, which a parity cannot tell from none) and read its
       // row scales (which unit k or the one after it replaces).
-      if (PF == 3 && k >= (uint32_t)C::kQB) {
+      if (k >= (uint32_t)C::kQB) {
         const uint32_t j = k - C::kQB;
         if (!wait_or_abort(&ms->scale_read[j & 1], (j >> 1) & 1, ms, p)) break;
       }
@@ -1188,10 +1188,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         mo[r] = kNoMax;
         l[r] = 0.f;
       }
-      if constexpr (PF == 3) {
-        if (lane < RH) ms->tree_max[moves & 1][rb + lane] = kNoMax;
-        warp_arrive(&ms->scale_read[k & 1]);
-      }
+      if (PF == 3 && lane < RH) ms->tree_max[moves & 1][rb + lane] = kNoMax;
+      warp_arrive(&ms->scale_read[k & 1]);
       for (int t = 0; t < ntiles; ++t, ++tile) {
         const int sb = tile % C::kSBuf;
         const int s = tile % kStages;
