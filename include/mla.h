@@ -108,6 +108,7 @@ size_t mla_workspace_size(mla_op_t op, int B, int H, int n_q, int device);
  *   q    device, [B][H][576] bfloat16, 16-byte aligned
  *   out  device, [B][H][512] bfloat16
  *   lse  device, [B][H] float32 (natural log); may be NULL if not wanted
+ * A row whose query, or any cached row that it sees, holds NaN comes out as NaN, its lse too.
  * The key axis of long sequences is split across the GPU's SMs; per-split results are
  * combined with the log-sum-exp merge ("Scaling Kimi K3 ...", section
  * "缓存可复用，还要能一致地恢复": partial attention merged by normalisation statistics).
@@ -221,7 +222,7 @@ mla_status_t mla_prefill_mha_bf16(const mla_kv_t* kv, int L, const void* q, int 
  * Log-sum-exp merge of S partial results per row ("Scaling Kimi K3 ...", section
  * "缓存可复用，还要能一致地恢复"): lse = ln sum_s exp(lse_s),
  * out = sum_s exp(lse_s - lse) * out_s. Partials with lse_s = -inf carry weight 0; a row
- * whose partials are all -inf gets out = 0, lse = -inf.
+ * whose partials are all -inf gets out = 0, lse = -inf; one with a NaN lse_s is NaN.
  *   part_out  device, [S][R][512] float32 (each partial already normalised)
  *   part_lse  device, [S][R] float32 (natural log)
  *   out       device, [R][512] bfloat16

@@ -1499,7 +1499,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         const int rr = rb + r;
         const float lt = ms->lred[0][rr] + ms->lred[1][rr] + ms->lred[2][rr] + ms->lred[3][rr];
         l[r] = lt;
-        inv[r] = lt > 0.f ? kv_scale / lt : 0.f;
+        inv[r] = lt == 0.f ? 0.f : kv_scale / lt;  // (a row that saw a NaN: its sum is NaN, so is it)
       }
       ok &= wait_pv_upto((int)tile - 1);
       if (PF == 3 ? wg_any(!ok) : !__all_sync(0xffffffffu, ok)) {
@@ -1594,7 +1594,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             lt = l[r];
             mm = mo[r];
           }
-        const float lse = (lt > 0.f) ? 0.6931471805599453f * (mm + log2f(lt)) : -INFINITY;
+        const float lse = (lt == 0.f) ? -INFINITY : 0.6931471805599453f * (mm + log2f(lt));
         const int roff = ms->row_off[rb + i];
         if (final_out) {
           if (p.lse) p.lse[(int64_t)un.qrow0 + roff] = lse;

@@ -113,17 +113,19 @@ __device__ void merge_row_chunk(const float* __restrict__ po, const float* __res
   }
   float mw = m;
   for (int o = 16; o > 0; o >>= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
-  sum = (m == -INFINITY) ? 0.f : sum * expf(m - mw);
+  if (m != -INFINITY) sum *= expf(m - mw);  // (else 0, or NaN past 256 pieces)
 #pragma unroll
   for (int j = 0; j < kLse; ++j)
     if (lv[j] != -INFINITY) sum += expf(lv[j] - mw);
   m = mw;
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float lse = (m == -INFINITY) ? -INFINITY : m + logf(sum);
+  // a NaN piece, which the maxima pass over, makes the sum NaN, and so the row
+  const bool none = m == -INFINITY && sum == 0.f;
+  const float lse = none ? -INFINITY : m + logf(sum);
   float acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  if (m != -INFINITY) {
+  if (!none) {
     for (int i0 = warp;;) {
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
@@ -375,14 +377,17 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_tree_kernel(AttnParams
   float m = lse_of;
   for (int i = lane + 32; i < count; i += 32) m = fmaxf(m, p.part_lse[at_of(i)]);
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (m == -INFINITY) {  // no piece saw a key
+  float sum = lse_of == -INFINITY ? 0.f : expf(lse_of - m);
+  for (int i = lane + 32; i < count; i += 32) {
+    const float l = p.part_lse[at_of(i)];
+    if (l != -INFINITY) sum += expf(l - m);
+  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (m == -INFINITY && sum == 0.f) {  // no piece saw a key (a NaN piece: the sum is NaN)
     out[0] = out[1] = make_uint4(0u, 0u, 0u, 0u);
     if (lane == 0 && p.lse) p.lse[row] = -INFINITY;
     return;
   }
-  float sum = expf(lse_of - m);
-  for (int i = lane + 32; i < count; i += 32) sum += expf(p.part_lse[at_of(i)] - m);
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float lse = m + logf(sum);
   float acc[16];
 #pragma unroll
