@@ -342,7 +342,8 @@ mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
  * the nodes i whose bit i is set in tree_mask[b][j]: for a draft tree its ancestors and
  * itself. Any mask is allowed (a prefix mask, separate documents, nothing at all); bits at or
  * above n are ignored. A node that sees no key gives out = 0, lse = -inf. With fewer than n
- * cached positions the missing ones are the first nodes' keys.
+ * cached positions the missing ones are the first nodes' keys. A key that a mask hides cannot
+ * reach the node, whatever its row holds: rows of nodes that pad a tree need not be written.
  *   q          device, [B][n][H][576] bfloat16, 16-byte aligned
  *   tree_mask  device, [B][n] uint64, 8-byte aligned
  *   out        device, [B][n][H][512] bfloat16

@@ -427,6 +427,11 @@ __device__ __forceinline__ float2 from_e4m3x2(uint16_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
+// four e4m3 codes, NaN ones (0x7F, 0xFF) as zero
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+  return w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -1218,8 +1223,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           if (k == 1) trace[kTrUnit2Scores] = globaltimer_ns();
         }
         // masking only on tiles that reach past the first new position's last visible key
+        bool odd_key = false;  // tree: this thread's key may hold NaN codes, and not every row sees it
         if (k0 + kTileKeys - 1 > lim0) {
           if constexpr (PF == 3) {
+            odd_key = x[0] != x[0];
             // this thread's key is node `node`'s: which of its rows see it, node by node of the
             // unit (a node is H neighbouring rows), from the half of each mask that holds its bit
             const int node = kabs - (L - p.n_q);
@@ -1405,27 +1412,26 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             tmem_wait_st();
           }
         }
-        // keys past this unit's range: zero their V bytes so 0 * garbage cannot be NaN; in a
-        // tree also the keys that none of the unit's nodes sees (nodes that pad a batch, whose
-        // cache rows nobody wrote)
-        bool unseen = kabs >= un.key_hi;
-        if constexpr (PF == 3) {
-          const int node = kabs - (L - p.n_q);
-          if (wg == 0 && !unseen && node >= 0) {
-            const uint32_t* half = reinterpret_cast<const uint32_t*>(p.tree_mask) +
-                                   2 * ((int64_t)un.b * p.n_q + un.j0) + (node >> 5);
-            uint32_t any = 0;
-            for (int j = 0; j * p.H < un.rows; ++j) any |= half[2 * j];
-            unseen = !(any >> (node & 31) & 1u);
-          }
-        }
-        if (wg == 0 && unseen) {
+        // keys past this unit's range: zero their V bytes so 0 * garbage cannot be NaN
+        if (wg == 0 && kabs >= un.key_hi) {
           uint8_t* st = smem + C::kOffStages + s * C::kStageStride + (i >> 6) * 8192 + (i & 63) * 128;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               reinterpret_cast<uint4*>(st + c * kChunkBytes)[e] = make_uint4(0, 0, 0, 0);
+        } else if (PF == 3 && wg == 0 && odd_key) {
+          // Tree: a node's key is hidden from some rows (P = 0) and seen by others. NaN codes among
+          // its values would reach them all as 0 * NaN, so they are zeroed: a row that sees the key
+          // has NaN from its score, whose product holds the same codes. That score is also how they
+          // are found (NaN for every query, the unit's first one too).
+          uint8_t* st = smem + C::kOffStages + s * C::kStageStride + (i >> 6) * 8192 + (i & 63) * 128;
+#pragma unroll 1
+          for (int e = 0; e < 32; ++e) {
+            uint4* at = reinterpret_cast<uint4*>(st + (e >> 3) * kChunkBytes) + (e & 7);
+            const uint4 v = *at;
+            *at = make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
+          }
         }
         // P^T: MN-major, 16 rows x 8 keys core matrices; term t, row group g at
         // pterm(t) + g * 2048, key i at (i / 8) * 128 + (i % 8) * 16, row r at byte r % 16.
