@@ -120,7 +120,10 @@ mla_status_t mla_decode(const mla_kv_t* kv, const void* q, int B, int H, float s
 /*
  * Speculative verify: n_q in 1..4 new positions per sequence, causal among themselves
  * ("Scaling Kimi K3 ...", section "并行度必须适配真正的形状": four verify positions per
- * sequence). n_q = 1 is exactly mla_decode.
+ * sequence). n_q = 1 is exactly mla_decode. The new positions' cached rows must hold no NaN
+ * codes if the positions before them are to be used: NaN there may reach those of its sequence
+ * too (mla_verify_tree keeps it from them; here, and in mla_prefill for the positions of its
+ * block, the check costs 3 % of every call).
  *   q    device, [B][n_q][H][576] bfloat16
  *   out  device, [B][n_q][H][512] bfloat16
  *   lse  device, [B][n_q][H] float32, or NULL
