@@ -500,7 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f1 = (m1 == -INFINITY) ? 0.f : ex2(m1 - mm);
       const float lt = ms->red_sum[0][row] * f0 + ms->red_sum[1][row] * f1;
       // a key chunk can hold no visible key for a row: partial 0 with lse -inf (weight 0)
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
+      // (a row that saw a NaN: its sum is NaN, and so are its weights)
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
       const float w0 = f0 * inv, w1 = f1 * inv;
       uint16_t* orow = p.out + ((int64_t)t * p.H + x.h) * 128 + wg * 64;
       const uint32_t oa = tmem + lane_addr + kColO + wg * 64;  // O0, dims of this warpgroup
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (wg == 0 && wk.slot >= 0)
         p.part_lse[((int64_t)wk.slot * 2 + rank) * kBM + row] =
-            lt > 0.f ? 0.6931471805599453f * (mm + log2f(lt)) : -INFINITY;
+            lt == 0.f ? -INFINITY : 0.6931471805599453f * (mm + log2f(lt));
       else if (wg == 0 && x.write && t < p.T && p.lse)
         p.lse[(int64_t)t * p.H + x.h] = 0.6931471805599453f * (mm + log2f(lt));
       tc_fence_before();
@@ -591,12 +592,12 @@ __global__ void __launch_bounds__(256) mha_chunk_merge_kernel(const MhaParams p,
     acc.w += w * v.w;
     sum += w;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   const __nv_bfloat162 h1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(p.out + ((int64_t)t * p.H + x.h) * 128 + 4 * lane) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-  if (lane == 0 && p.lse) p.lse[(int64_t)t * p.H + x.h] = sum > 0.f ? m + logf(sum) : -INFINITY;
+  if (lane == 0 && p.lse) p.lse[(int64_t)t * p.H + x.h] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
 // Cached rows -> latent [L][512] bf16 (the e4m3 values; exact) and RoPE rows [L][64] bf16

@@ -122,3 +122,27 @@ def test_merge(S, R):
     got, got_lse = mla.mla_merge_lse(out.to(DEV), lse.to(DEV))
     assert torch.isnan(want_lse).any() and torch.isnan(want[torch.isnan(want_lse)]).all()
     compare(got, got_lse, want.numpy(), want_lse.numpy(), f"S={S} R={R}")
+
+
+@pytest.mark.parametrize("T,prefix,H", [(200, 300, 2), (300, 0, 3), (1280, 1000, 16)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_mha_prefill(T, prefix, H, bf16):
+    """Query rows with NaN alone are NaN, the others bit for bit what they are without; then a
+    prefix row that every position sees. (In the largest some units are cut along the keys.)"""
+    m = W.mha_prefill_inputs(T, prefix, H=H, seed=T)
+    w, q = m.w_ukv.to(DEV), m.q.to(DEV)
+
+    def call():
+        return mla.mla_prefill_mha(mla.KVCache.from_inputs(m.cache, DEV), q, w, m.cache.sm_scale, bf16=bf16)
+
+    out, lse = call()
+    bad = torch.zeros(T, H, dtype=torch.bool, device=DEV)
+    bad[[0, T // 2, T - 1], [0, H // 2, H - 1]] = bad[T // 3] = True
+    q[..., 150] = torch.where(bad, float("nan"), q[..., 150])
+    got, got_lse = call()
+    assert torch.isnan(got[bad]).all() and torch.isnan(got_lse[bad]).all()
+    assert torch.equal(got[~bad], out[~bad]) and torch.equal(got_lse[~bad], lse[~bad])
+    if prefix:
+        cached(m.cache, 0, prefix // 2)[17] = 0x7F
+        got, got_lse = call()
+        assert torch.isnan(got).all() and torch.isnan(got_lse).all()
