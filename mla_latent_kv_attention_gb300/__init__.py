@@ -2,10 +2,9 @@
 
 A thin ctypes binding over ``libmla.so`` (C ABI in ``include/mla.h``). The functions
 carry the C names and only marshal arguments: torch CUDA tensors become device
-pointers, the current torch stream becomes the ``cudaStream_t``. mla_rope,
-mla_cache_append_rope, mla_cache_gather, mla_verify_tree and mla_accept_drafts, when given
-a ``stream``, make it the current one for the call: what they allocate belongs to it, as
-after ``with torch.cuda.stream(stream)``. Every step of the
+pointers, the current torch stream becomes the ``cudaStream_t``. A call that is given a
+``stream`` makes it the current one for what it allocates (outputs, a workspace), as
+``with torch.cuda.stream(stream)`` does: that memory belongs to it. Every step of the
 attention runs in the library's CUDA kernels; there is no other implementation, and
 every entry point raises ImportError when the library is missing (the seeded workload
 and accounting modules import without it).
@@ -207,6 +206,9 @@ def _q_check(q: torch.Tensor, ndim: int) -> None:
 def mla_decode(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None, ws=None,
                stream=None):
     """q [B, H, 576] bf16 -> (out [B, H, 512] bf16, lse [B, H] fp32)."""
+    if stream is not None and (out is None or lse is None or ws is None):
+        with _current(stream):
+            return mla_decode(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 3)
     B, H = q.shape[0], q.shape[1]
     out = torch.empty(B, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
@@ -222,6 +224,9 @@ def mla_decode(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None
 def mla_verify(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None, ws=None,
                stream=None):
     """q [B, n_q, H, 576] bf16 -> (out [B, n_q, H, 512] bf16, lse [B, n_q, H] fp32)."""
+    if stream is not None and (out is None or lse is None or ws is None):
+        with _current(stream):
+            return mla_verify(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 4)
     B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
     out = torch.empty(B, n_q, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
@@ -241,6 +246,9 @@ def mla_prefill_mha(kv: KVCache, q: torch.Tensor, w_ukv: torch.Tensor, sm_scale:
     -> (out [T, H, 128] bf16, lse [T, H] fp32). L (cached positions incl. the T new ones)
     defaults to kv.seq_lens[0]. bf16=True calls mla_prefill_mha_bf16 (every tensor-core
     operand in bf16: faster, looser)."""
+    if stream is not None and (L is None or out is None or lse is None or ws is None):
+        with _current(stream):
+            return mla_prefill_mha(kv, q, w_ukv, sm_scale, L, out, lse, ws, bf16=bf16)
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != 192 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bfloat16 tensor [T, H, 192]")
     T, H = q.shape[0], q.shape[1]
@@ -268,6 +276,9 @@ def mla_verify_f32(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=
     """As mla_verify with a float32 output [B, n_q, H, 512], for results merged later.
     visible_shift > 0 moves every new position's causal limit that many keys later
     (mla_verify_f32_shard; n_q - 1 makes every key of the view visible to all of them)."""
+    if stream is not None and (out is None or lse is None or ws is None):
+        with _current(stream):
+            return mla_verify_f32(kv, q, sm_scale, out, lse, ws, visible_shift=visible_shift)
     _q_check(q, 4)
     B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
     out = torch.empty(B, n_q, H, MLA_DV, dtype=torch.float32, device=q.device) if out is None else out
@@ -290,6 +301,9 @@ def mla_verify_f32(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=
 def mla_prefill(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None, ws=None,
                 stream=None):
     """q [T, H, 576] bf16 of one sequence -> (out [T, H, 512] bf16, lse [T, H] fp32)."""
+    if stream is not None and (out is None or lse is None or ws is None):
+        with _current(stream):
+            return mla_prefill(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 3)
     T, H = q.shape[0], q.shape[1]
     out = torch.empty(T, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
@@ -305,6 +319,9 @@ def mla_prefill(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=Non
 def mla_merge_lse(part_out: torch.Tensor, part_lse: torch.Tensor, out=None, lse=None,
                   stream=None):
     """part_out [S, R, 512] fp32, part_lse [S, R] fp32 -> (out [R, 512] bf16, lse [R] fp32)."""
+    if stream is not None and (out is None or lse is None):
+        with _current(stream):
+            return mla_merge_lse(part_out, part_lse, out, lse)
     if part_out.dtype != torch.float32 or part_lse.dtype != torch.float32 or \
             not part_out.is_contiguous() or not part_lse.is_contiguous():
         raise ValueError("partials must be contiguous float32 CUDA tensors")
@@ -337,6 +354,9 @@ def mla_top_k_renorm_prob(probs: torch.Tensor, top_k, out: Optional[torch.Tensor
                           stream=None) -> torch.Tensor:
     """probs float32 [B, V] -> top-k renormalised copy; top_k an int (all rows) or an int32
     CUDA tensor [B]."""
+    if stream is not None and out is None:
+        with _current(stream):
+            return mla_top_k_renorm_prob(probs, top_k)
     if probs.dtype != torch.float32 or probs.dim() != 2 or not probs.is_contiguous():
         raise ValueError("probs must be a contiguous float32 tensor [B, V]")
     B, V = probs.shape

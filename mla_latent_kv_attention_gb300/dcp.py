@@ -30,7 +30,7 @@ from typing import List, Optional, Sequence, Tuple
 import numpy as np
 import torch
 
-from . import MLA_DV, KVCache, mla_merge_lse, mla_verify_f32
+from . import MLA_DV, KVCache, _current, mla_merge_lse, mla_verify_f32
 
 
 @dataclasses.dataclass
@@ -117,6 +117,9 @@ def rank_partials(views, q: torch.Tensor, sm_scale: float,
                   part_lse: Optional[torch.Tensor] = None, stream=None):
     """This rank's partials from its views (rank_views): part_out [parts, B, n_q, H, 512]
     float32 and part_lse [parts, B, n_q, H], each the normalised attention over the shard."""
+    if stream is not None:
+        with _current(stream):
+            return rank_partials(views, q, sm_scale, part_out, part_lse)
     B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
     P = len(views)
     if P != (1 if n_q == 1 else 2):
@@ -128,8 +131,7 @@ def rank_partials(views, q: torch.Tensor, sm_scale: float,
     for i, (view, shift) in enumerate(views):
         if view.seq_lens.shape[0] != B:
             raise ValueError("views do not match q's batch")
-        mla_verify_f32(view, q, sm_scale, out=part_out[i], lse=part_lse[i], stream=stream,
-                       visible_shift=shift)
+        mla_verify_f32(view, q, sm_scale, out=part_out[i], lse=part_lse[i], visible_shift=shift)
     return part_out, part_lse
 
 
@@ -151,11 +153,14 @@ def gather_partials(part_out: torch.Tensor, part_lse: torch.Tensor, group=None):
 def merge_partials(part_out: torch.Tensor, part_lse: torch.Tensor, stream=None):
     """[S, B, n_q, H, 512] float32 partials and [S, B, n_q, H] lse -> (out [B, n_q, H, 512]
     bf16, lse [B, n_q, H]) through mla_merge_lse."""
+    if stream is not None:
+        with _current(stream):
+            return merge_partials(part_out, part_lse)
     S = part_out.shape[0]
     shape = part_lse.shape[1:]
     R = int(np.prod(shape))
     out, lse = mla_merge_lse(part_out.reshape(S, R, MLA_DV).contiguous(),
-                             part_lse.reshape(S, R).contiguous(), stream=stream)
+                             part_lse.reshape(S, R).contiguous())
     return out.view(*shape, MLA_DV), lse.view(*shape)
 
 
@@ -166,19 +171,22 @@ def dcp_attention(kv: KVCache, q: torch.Tensor, sm_scale: float, world: int,
     With a process group, this process is rank `group.rank()` of `world`: it attends to its
     own shard and all-gathers the partials in host memory. Without one, this process plays
     every rank in turn on its device (the shards' attention calls are independent launches)
-    and the gather is a stack in device memory."""
+    and the gather is a stack in device memory. Given a stream, all of it runs there."""
+    if stream is not None:
+        with _current(stream):
+            return dcp_attention(kv, q, sm_scale, world, group)
     B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
     plan = shard_plan(kv.seq_lens.cpu().tolist(), kv.pool.shape[1], world, n_q)
     P = plan[0].parts
     if group is not None:
         import torch.distributed as dist
         mine = plan[dist.get_rank(group)]
-        po, pl = rank_partials(rank_views(kv, mine), q, sm_scale, stream=stream)
+        po, pl = rank_partials(rank_views(kv, mine), q, sm_scale)
         po, pl = gather_partials(po, pl, group)
     else:
         po = torch.empty(world * P, B, n_q, H, MLA_DV, dtype=torch.float32, device=q.device)
         pl = torch.empty(world * P, B, n_q, H, dtype=torch.float32, device=q.device)
         for r, sh in enumerate(plan):
             rank_partials(rank_views(kv, sh), q, sm_scale, po[r * P:(r + 1) * P],
-                          pl[r * P:(r + 1) * P], stream=stream)
-    return merge_partials(po, pl, stream=stream)
+                          pl[r * P:(r + 1) * P])
+    return merge_partials(po, pl)
