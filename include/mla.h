@@ -379,7 +379,7 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
  * that holds none either, the token is -1. Weights are rounded to multiples of 2^-43 (a
  * float32 probability above 2^-19 is one already) and shares and sums are whole numbers, so
  * results do not depend on the order of summation. Weights outside [0, 1] count as the nearer
- * end; an entry that is NaN in target or draft is neither accepted nor drawn. Uniforms outside
+ * end, target's and draft's each before they are compared or subtracted; an entry that is NaN in target or draft is neither accepted nor drawn. Uniforms outside
  * [0, 1) count as the nearest number in it, NaN as 0.
  * A token outside [0, V) or a parent outside [0, j) makes node j no draft (padding): it and
  * what hangs below it are never accepted, and it takes nothing from the draw.

@@ -71,6 +71,10 @@ __device__ __forceinline__ Weight split_weight(float w) {
 }
 __device__ __forceinline__ long long whole_weight(Weight w) { return ((long long)w.hi << 23) + w.lo; }
 
+// A draft probability within [0, 1]; NaN is 1, which leaves nothing of the target's to draw.
+// (A clamp by fminf, then fmaxf, says the same, but compiled to one whose NaN is 0.)
+__device__ __forceinline__ float draft_weight(float q) { return q == q ? __saturatef(q) : 1.f; }
+
 // A uniform number in steps of 2^-BITS, in [0, 2^BITS).
 template <int BITS>
 __device__ __forceinline__ long long uniform_of(float u) {
@@ -129,7 +133,8 @@ __device__ void walk(const AcceptArgs& a, AcSmem& s, int b, bool write) {
   bool taken[2];
   if (DRAFT) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) taken[h] = par[h] != kNone && __fmul_rn(up[h], qt[h]) < pt[h];
+    for (int h = 0; h < 2; ++h)  // (a NaN pt is 0: nothing is below it)
+      taken[h] = par[h] != kNone && qt[h] == qt[h] && __fmul_rn(up[h], draft_weight(qt[h])) < __saturatef(pt[h]);
   } else {
     long long below[2] = {0, 0}, share[2];
 #pragma unroll
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(kAcThreads, 2) accept_kernel(const __grid_cons
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[k][e] -= q[k][e];
+        for (int e = 0; e < 4; ++e) w[k][e] = __saturatef(w[k][e]) - draft_weight(q[k][e]);
     }
   };
   // children's tokens in this warp's span: left out of the draw (a bit a child)
