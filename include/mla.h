@@ -281,7 +281,8 @@ typedef struct mla_rope {
  * with a linear ramp between the two pair indices (rounded outwards to whole ones). amplitude is
  * the model's attention factor for that stretch (1 where it is folded into sm_scale).
  * MLA_ERR_INVALID_ARG: base <= 1, factor <= 0, original_positions < 0, not
- * beta_fast > beta_slow > 0 (YaRN), or anything not finite.
+ * beta_fast > beta_slow > 0 (YaRN), or anything not finite, an f_i / factor among it (what *rope
+ * then holds is not to be used).
  */
 mla_status_t mla_rope_init(mla_rope_t* rope, double base, double factor, int original_positions,
                            double beta_fast, double beta_slow, float amplitude, int interleaved);
