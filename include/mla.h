@@ -262,9 +262,11 @@ mla_status_t mla_cache_append(uint8_t* pool, int64_t num_pages, int32_t page_siz
  * m * f_i and is scaled by `amplitude`:
  *     (a, b) -> amplitude * (a cos - b sin, a sin + b cos).
  * interleaved != 0: pair i is dims (2i, 2i + 1); otherwise (half layout) dims (i, i + 32).
- * turns[i] is f_i / (2 pi), the turns a position adds, in units of 2^-64: the phase of any
- * position is the integer product m * turns[i] modulo 2^64, so it loses nothing at far
- * positions (a float32 product is off by 0.06 rad at position 10^6). Filled by
+ * turns[i] is f_i / (2 pi), the turns a position adds, in units of 2^-64, rounded to nearest from
+ * float64: the phase of any position is the integer product m * turns[i] modulo 2^64, which is
+ * exact, so a phase is off by m times the frequency's own error (2^-65 turns and 2^-50 of the
+ * frequency at most: 9e-10 rad at position 10^6 for the fastest pair; a float32 product is off by
+ * 0.06 rad there). Filled by
  * mla_rope_init; read on the host when a call is made (a captured graph keeps the values).
  */
 typedef struct mla_rope {
@@ -278,7 +280,8 @@ typedef struct mla_rope {
  * factor = 1 leaves them; original_positions = 0 divides every f_i by factor (linear position
  * interpolation); original_positions > 0 is YaRN: pairs that turn more than beta_fast times over
  * the original positions keep f_i, those that turn less than beta_slow times get f_i / factor,
- * with a linear ramp between the two pair indices (rounded outwards to whole ones). amplitude is
+ * with a linear ramp between the two pair indices (rounded outwards to whole ones, the lower at
+ * least 0, the upper at most 63, the ramp at least 0.001 wide). amplitude is
  * the model's attention factor for that stretch (1 where it is folded into sm_scale).
  * MLA_ERR_INVALID_ARG: base <= 1, factor <= 0, original_positions < 0, not
  * beta_fast > beta_slow > 0 (YaRN), or anything not finite, an f_i / factor among it (what *rope
@@ -380,8 +383,9 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
  * that holds none either, the token is -1. Weights are rounded to multiples of 2^-43 (a
  * float32 probability above 2^-19 is one already) and shares and sums are whole numbers, so
  * results do not depend on the order of summation. Weights outside [0, 1] count as the nearer
- * end, target's and draft's each before they are compared or subtracted; an entry that is NaN in target or draft is neither accepted nor drawn. Uniforms outside
- * [0, 1) count as the nearest number in it, NaN as 0.
+ * end, target's and draft's each before they are compared or subtracted; an entry that is NaN in
+ * target or draft is neither accepted nor drawn. Uniforms outside [0, 1) count as the nearest
+ * number in it, NaN as 0.
  * A token outside [0, V) or a parent outside [0, j) makes node j no draft (padding): it and
  * what hangs below it are never accepted, and it takes nothing from the draw.
  *   target        device, [B][n][V] float32

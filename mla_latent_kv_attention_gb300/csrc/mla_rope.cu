@@ -136,8 +136,9 @@ extern "C" mla_status_t mla_rope_init(mla_rope_t* rope, double base, double fact
     if (original_positions > 0) stretched = fmin(fmax((i - low) / fmax(high - low, 0.001), 0.0), 1.0);
     const double turn = (f / factor * stretched + f * (1.0 - stretched)) / (2.0 * kPi);
     if (!isfinite(turn)) return MLA_ERR_INVALID_ARG;  // f / factor is past float64
-    // whole turns drop out (positions are whole); the rest lies in [0, 1)
-    rope->turns[i] = (uint64_t)ldexp(turn - floor(turn), 64);
+    // whole turns drop out (positions are whole); the rest lies in [0, 1) and is rounded to nearest
+    // (from 2^-11 up it is a multiple of 2^-64 already)
+    rope->turns[i] = (uint64_t)nearbyint(ldexp(turn - floor(turn), 64));
   }
   rope->amplitude = amplitude;
   rope->interleaved = interleaved != 0;
