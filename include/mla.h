@@ -109,6 +109,7 @@ size_t mla_workspace_size(mla_op_t op, int B, int H, int n_q, int device);
  *   out  device, [B][H][512] bfloat16
  *   lse  device, [B][H] float32 (natural log); may be NULL if not wanted
  * A row whose query, or any cached row that it sees, holds NaN comes out as NaN, its lse too.
+ * Infinite query entries are not supported (they saturate), here and in mla_verify and mla_prefill.
  * The key axis of long sequences is split across the GPU's SMs; per-split results are
  * combined with the log-sum-exp merge ("Scaling Kimi K3 ...", section
  * "缓存可复用，还要能一致地恢复": partial attention merged by normalisation statistics).
@@ -350,7 +351,8 @@ mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
  * itself. Any mask is allowed (a prefix mask, separate documents, nothing at all); bits at or
  * above n are ignored. A node that sees no key gives out = 0, lse = -inf. With fewer than n
  * cached positions the missing ones are the first nodes' keys. A key that a mask hides cannot
- * reach the node, whatever its row holds: rows of nodes that pad a tree need not be written.
+ * reach the node, whatever its row holds: rows of nodes that pad a tree need not be written. A
+ * query row with an infinite entry is NaN, as it is by the formula.
  *   q          device, [B][n][H][576] bfloat16, 16-byte aligned
  *   tree_mask  device, [B][n] uint64, 8-byte aligned
  *   out        device, [B][n][H][512] bfloat16

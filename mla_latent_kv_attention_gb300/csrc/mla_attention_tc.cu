@@ -481,7 +481,11 @@ __device__ __forceinline__ int q_offset(int n, int w16) {
 // rounded: exact for entries down to 2^-14.8 of the row's largest magnitude, within
 // 2^-21.8 of it below), and the rows' score scales into row_scale[]. Rows at or past R are
 // written as zeros.
-template <int RP, int NW>
+//
+// INF: a row with an infinite entry, which saturates to 448, gets a NaN scale: its scores are then
+// NaN, as its softmax is by the formula. (In the attention kernels themselves that one addition
+// moved the 48-row code enough to cost verify 1 %: 69.3 -> 70.0 us.)
+template <int RP, int NW, bool INF = false>
 __device__ __forceinline__ void stage_rows(const AttnParams& p, int R, const int* row_off,
                                        const uint16_t* qseq, uint8_t* qdst, float* row_scale,
                                        int w0, int lane) {
@@ -539,7 +543,11 @@ __device__ __forceinline__ void stage_rows(const AttnParams& p, int R, const int
       }
       const float up = __int_as_float((127 + ex) << 23);    // 2^ex, exact
       const float down = __int_as_float((127 - ex) << 23);  // 2^-ex, exact
-      if (lane == 0) row_scale[r] = real ? p.sm_scale * kv_scale * down * kLog2e : 0.f;
+      if (lane == 0) {
+        float scale = real ? p.sm_scale * kv_scale * down * kLog2e : 0.f;
+        if (INF) scale += amax - amax;  // 0, or NaN
+        row_scale[r] = scale;
+      }
       // two terms per value, packed 16 codes per 16-byte group
       auto emit = [&](const float* x, int w16) {
         uint32_t t1w[4], t2w[4];
@@ -1651,8 +1659,8 @@ __global__ void __launch_bounds__(512) stage_queries_kernel(const __grid_constan
   const int node0 = (int)(blockIdx.x % groups) * p.group_nodes;
   const int64_t row0 = ((int64_t)(blockIdx.x / groups) * p.n_q + node0) * p.H;
   uint8_t* img = p.qimg + (int64_t)blockIdx.x * p.qimg_stride;
-  stage_rows<RP, 16>(p, min(p.group_nodes, p.n_q - node0) * p.H, row_off, p.q + row0 * kD, img,
-                     reinterpret_cast<float*>(img + Cfg<RP>::kQBytes), threadIdx.x >> 5, threadIdx.x & 31);
+  stage_rows<RP, 16, true>(p, min(p.group_nodes, p.n_q - node0) * p.H, row_off, p.q + row0 * kD, img,
+                           reinterpret_cast<float*>(img + Cfg<RP>::kQBytes), threadIdx.x >> 5, threadIdx.x & 31);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
