@@ -182,8 +182,8 @@ struct Misc {
   uint64_t p_full[2];   // P of tile g is written: p_full[g % 2] (the softmax may run a tile
                         // ahead of the value MMAs when P lives in the stage)
   uint64_t q_full[2];   // query operand buffer holds its unit's terms
-  uint64_t q_empty[2];  // the unit that used the buffer has finished its scores
-  uint64_t scale_read[2];  // the softmax warps have read the unit's row_scale (by parity)
+  uint64_t q_empty[2];  // the unit that used the buffer has finished its scores, and the softmax
+                        // warps have read its row_scale
   uint64_t q0_done;     // the first unit's query rows are staged (by warps 2.. together)
   uint64_t q1_done;     // the second unit's rows are in this CTA's global query image
   uint64_t wg_bar[3];  // bounded barriers of the softmax warpgroups (128 arrivals)
@@ -656,8 +656,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     mbar_init(&ms->p_full[1], 4 * C::kNWG);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->q_full[s], 1);
-      mbar_init(&ms->q_empty[s], 1);
-      mbar_init(&ms->scale_read[s], 4 * C::kNWG);
+      mbar_init(&ms->q_empty[s], 1 + 4 * C::kNWG);
     }
     mbar_init(&ms->q0_done, 32 * C::kStageWarps);
     mbar_init(&ms->q1_done, 32 * C::kStageWarps);
@@ -1089,15 +1088,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         fence_proxy_async_global();
         __syncwarp();
       }
+      // The copy for unit k waits until the unit before in this buffer has its scores, and until the
+      // softmax warps have seen that unit's copy and read its row scales: a unit of one tile may
+      // have its scores done before its softmax has begun, and q_full would run two phases ahead of
+      // those warps, which a parity cannot tell from none (and unit k or the one after it replaces
+      // the scales). One barrier for both: a second one took verify 69.1 us to this one's 68.8.
       if (k >= (uint32_t)C::kQB && !wait_or_abort(&ms->q_empty[slot], ((k / C::kQB) - 1) & 1, ms, p)) break;
-      // A unit of one tile may have its scores done before its softmax has begun: the copy for unit
-      // k waits until the softmax warps have seen the copy that used this buffer before (or q_full
-      // would run two phases ahead of them, which a parity cannot tell from none) and read its
-      // row scales (which unit k or the one after it replaces).
-      if (k >= (uint32_t)C::kQB) {
-        const uint32_t j = k - C::kQB;
-        if (!wait_or_abort(&ms->scale_read[j & 1], (j >> 1) & 1, ms, p)) break;
-      }
       if (lane == 0) {
         mbar_arrive_expect_tx(&ms->q_full[slot], kImgBytes);
         bulk_g2s(qbuf + slot * C::kQBytes, from, C::kQBytes, &ms->q_full[slot]);
@@ -1202,7 +1198,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         l[r] = 0.f;
       }
       if (PF == 3 && lane < RH) ms->tree_max[moves & 1][rb + lane] = kNoMax;
-      warp_arrive(&ms->scale_read[k & 1]);
+      warp_arrive(&ms->q_empty[k % C::kQB]);
       for (int t = 0; t < ntiles; ++t, ++tile) {
         const int sb = tile % C::kSBuf;
         const int s = tile % kStages;
