@@ -157,12 +157,12 @@ class KVCache:
             raise ValueError("KVCache tensors must be on one device")
         if pool.dtype is not _U8 or table.dtype is not _I32 or lens.dtype is not _I32:
             raise TypeError("KVCache dtypes: pool uint8, page_table int32, seq_lens int32")
-        shape = pool.shape
-        if len(shape) < 3 or shape[2:].numel() != MLA_D:
+        shape, rows = pool.shape, table.shape
+        if (len(shape) != 3 or shape[2] != MLA_D) and (len(shape) < 3 or shape[2:].numel() != MLA_D):
             raise ValueError(f"KVCache.pool must be [num_pages, page_size, {MLA_D}], got {tuple(shape)}")
-        if table.dim() < 2 or table.shape[2:].numel() != 1:
-            raise ValueError(f"KVCache.page_table must be [B, stride], got {tuple(table.shape)}")
-        return mla_kv_t(pool.data_ptr(), shape[0], shape[1], table.data_ptr(), table.shape[1],
+        if len(rows) != 2 and (len(rows) < 2 or rows[2:].numel() != 1):
+            raise ValueError(f"KVCache.page_table must be [B, stride], got {tuple(rows)}")
+        return mla_kv_t(pool.data_ptr(), shape[0], shape[1], table.data_ptr(), rows[1],
                         lens.data_ptr(), float(self.kv_scale))
 
     @staticmethod
