@@ -400,10 +400,12 @@ cudaError_t launch_accept(const AcceptArgs& a, int num_sms, cudaStream_t s) {
   // 16-byte loads where rows start on 16 bytes (64 x 129,280: 9.9 us, 10.1 an entry at a time)
   const bool vec = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.target) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(a.draft) % 16 == 0;
-  // CTAs a sequence: eight, fewer where all sequences' would not run at once (two an SM: the walk
-  // and the exchange are waited for once a wave; 64 sequences of 129,280 tokens with draft
-  // probabilities: 20.5 us a call with eight, 18.4 us with four) or where a warp would have no step of
-  // its own
+  // CTAs a sequence: eight, halved where all sequences' would not run at once (two an SM: the walk
+  // and the exchange are waited for once a wave) or where a warp would have no step of its own.
+  // Single replays from HBM in us with 8 / 4 / 2 CTAs (129,280 tokens, draft probabilities): 25
+  // sequences 15.6 / 17.5 / 23.7, 38 21.7 / 19.6 / 23.7, 39 22.7 / 19.6 / 23.7, 64 of seven drafts 27.8
+  // / 25.7 / 29.8, 77 31.9 / 31.9 / 29.8, 152 42.1 / 40.1 / 38.0. The sizes between fill more places
+  // and gain nothing (39: six 19.6, seven 22.7; 50: four 21.6, six 25.8), but for three at 77 (27.8).
   const int steps = (a.V + kAcStep - 1) / kAcStep;
   int ctas = kAcCluster;
   while (ctas > 1 && ((int64_t)a.B * ctas > 2 * num_sms || (ctas / 2) * kAcWarps >= steps)) ctas /= 2;

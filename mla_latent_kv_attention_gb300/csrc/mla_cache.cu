@@ -70,8 +70,10 @@ __global__ void __launch_bounds__(256) cache_append_kernel(uint8_t* __restrict__
 // The frequencies lie in the parameters, where the 32 lanes' different addresses are read one
 // after another: one warp of the CTA copies them to shared memory while every warp's row is on
 // its way (8,192 rows 5.3 -> 4.3 us; copied before the loads 5.1). Bound: L2 or HBM for many rows
-// (32,768 in L2: 11.2 us, 56.6 MB, 5.0 TB/s), the launch and a round of loads for fewer (8,192
-// 4.3 us in L2 and 6.6 us from HBM), the launch alone for 32 (2.1 us).
+// (32,768, 56.6 MB: 10.9 us in L2, 14.2 us and 4.0 TB/s from HBM), the launch and two rounds of CTAs
+// for fewer (8,192 rows are 1,024 CTAs, of which 608 run at once, each a chain of load, norm and
+// write: 4.2 us in L2, 6.0 us from HBM), the launch alone for 32 (1.9 us). The half layout's two-byte
+// loads and byte exchange add 0.4 to 0.6 us.
 __global__ void __launch_bounds__(256, 4)  // (four: 8,192 rows 4.3 us; left open 4.85, six 4.9)
     cache_append_rope_kernel(const __grid_constant__ AppendRopeArgs a,
                              const __grid_constant__ mla_rope_t rope) {
@@ -154,8 +156,8 @@ __global__ void __launch_bounds__(256, 4)  // (four: 8,192 rows 4.3 us; left ope
 // float32, two rows a round: a warp's stores are whole lines), every load of a thread in flight
 // before its first store. HBM-bound: 576 bytes read and 1,152 (bf16) or 2,304 (float32) written a
 // row: 8 x 32,768 rows to bf16 in 70 us (453 MB, 6.5 TB/s, 0.95 of the measured copy), 66,000 rows
-// to float32 in 32.8 us (190 MB, 5.8 TB/s; with 8 codes a thread, two stores each, 44.2 us), 8 x
-// 333 to bf16 in 3.9 us (the launch and three dependent loads).
+// to float32 in 31.4 us (190 MB, 6.1 TB/s; with 8 codes a thread, two stores each, 44.2 us), 8 x
+// 333 to bf16 in 4.1 us (the launch and three dependent loads).
 constexpr int kGatherRows = 32;
 constexpr int kGatherThreads = 288;
 constexpr int64_t kRowSkip = -1, kRowBad = -2;
@@ -242,7 +244,8 @@ __global__ void __launch_bounds__(kGatherThreads)
 
 cudaError_t launch_cache_append_rope(const AppendRopeArgs& a, const mla_rope_t& rope, int num_sms,
                                      cudaStream_t s) {
-  const int64_t blocks = (a.n * 32 + 255) / 256;  // one warp per row, at most 8 CTAs per SM
+  // one warp per row, at most 8 CTAs per SM (of which four run at once)
+  const int64_t blocks = (a.n * 32 + 255) / 256;
   const int grid = (int)(blocks < (int64_t)num_sms * 8 ? blocks : (int64_t)num_sms * 8);
   cache_append_rope_kernel<<<grid, 256, 0, s>>>(a, rope);
   return cudaGetLastError();

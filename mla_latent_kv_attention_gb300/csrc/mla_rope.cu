@@ -4,8 +4,8 @@
 // A thread takes a quarter of a token's 64 dims (eight pairs, two 16-byte vectors) and turns it
 // in several heads: the eight angles belong to the token, so their cosines and sines are
 // computed once for all the heads that the thread takes. Bound: 256 bytes a head through L2 and
-// HBM when there are many tokens (8,192 of 12 heads, 25.2 MB: 4.5 us in L2, 6.5 us and 3.9 TB/s
-// from HBM), the launch when there are few (32: 1.9 us).
+// HBM when there are many tokens (8,192 of 12 heads, 25.2 MB: 6.5 us and 3.9 TB/s from HBM; in L2
+// 4.5 us in the half layout, 5.4 us interleaved), the launch when there are few (32: 1.8 us).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -85,7 +85,7 @@ cudaError_t launch_rope(const mla_rope_t& rope, const uint16_t* x, int64_t x_tok
                         int64_t out_head, int num_sms, cudaStream_t s) {
   // Four heads a thread share their angles. Where that would leave an SM with less than two
   // warps, one head a thread: more threads, each with a shorter wait. In us, one / four, at 12
-  // heads: 32 tokens 1.9 / 2.3, 512 2.2 / 2.3, 1,024 2.4 / 2.4, 4,096 4.3 / 3.8, 8,192 7.0 / 5.4;
+  // heads, interleaved, in L2: 32 tokens 1.9 / 2.3, 512 2.2 / 2.3, 1,024 2.4 / 2.4, 4,096 4.3 / 3.8, 8,192 7.0 / 5.4;
   // 8 heads cross at 1,024 tokens too, 16 heads at 800.
   const bool many = n * ((H + 3) / 4) * 4 >= (int64_t)num_sms * 2 * 32;
   const int heads = many ? 4 : 1;
