@@ -47,6 +47,7 @@ extern "C" {
 #define MLA_ROPE 64     /* RoPE dims per row: the last 64 of its 576 codes        */
 #define MLA_MAX_TREE 64 /* drafted nodes per sequence (tree verify, acceptance)   */
 #define MLA_MAX_VOCAB (1 << 19) /* probabilities per row of mla_accept_drafts     */
+#define MLA_MAX_AXES 4  /* position axes of mla_rope_axes                         */
 
 typedef enum {
   MLA_OK = 0,
@@ -306,6 +307,41 @@ mla_status_t mla_rope(const mla_rope_t* rope, const void* x, int64_t x_token_str
                       int64_t out_token_stride, int64_t out_head_stride, void* stream);
 
 /*
+ * Positions with several axes, as image and video tokens have them (time, height, width): pair i
+ * of the 32 turns by its own axis' position, at the frequency that mla_rope_t gives pair i:
+ *     angle_i = positions[axis[i]][token] * f_i.
+ * A token whose axes all hold the same position turns as mla_rope turns it.
+ *   axis    the axis of each pair, below n_axes
+ *   n_axes  1 .. MLA_MAX_AXES
+ * Read on the host when a call is made, as mla_rope_t is.
+ */
+typedef struct mla_rope_axes {
+  uint8_t axis[MLA_ROPE / 2];
+  int32_t n_axes;
+} mla_rope_axes_t;
+
+/*
+ * Fill a mla_rope_axes_t (host only) from the number of pairs of each axis, 32 in all.
+ * interleaved = 0: the first sections[0] pairs are axis 0's, the next sections[1] axis 1's, ...;
+ * otherwise the axes take pairs in turn (0, 1, .., 0, 1, ..), each while it has pairs left.
+ * MLA_ERR_INVALID_ARG: a null pointer, n_axes outside 1 .. MLA_MAX_AXES, a negative section,
+ * sections that do not add up to 32 (*axes is then left as it was).
+ */
+mla_status_t mla_rope_axes_init(mla_rope_axes_t* axes, const int32_t* sections, int n_axes,
+                                int interleaved);
+
+/*
+ * mla_rope for positions with several axes.
+ *   axes       which axis each pair turns by (an axis[i] not below n_axes: MLA_ERR_INVALID_ARG)
+ *   positions  device, [axes->n_axes][n] int64 (any sign)
+ * All else as mla_rope.
+ */
+mla_status_t mla_rope_axes(const mla_rope_t* rope, const mla_rope_axes_t* axes, const void* x,
+                           int64_t x_token_stride, int64_t x_head_stride, const int64_t* positions,
+                           int64_t n, int H, void* out, int64_t out_token_stride,
+                           int64_t out_head_stride, void* stream);
+
+/*
  * mla_cache_append for rows as the latent projection leaves them: row i is (c, r), c the 512
  * latent entries before their norm and r the 64 RoPE entries before their rotation. Cache row
  * slots[i] becomes the e4m3 codes of y * (1 / kv_scale), where
@@ -325,6 +361,17 @@ mla_status_t mla_cache_append_rope(uint8_t* pool, int64_t num_pages, int32_t pag
                                    float kv_scale, const void* norm_weight, float eps,
                                    const mla_rope_t* rope, const int64_t* positions,
                                    unsigned* status, void* stream);
+
+/*
+ * mla_cache_append_rope for positions with several axes.
+ *   rope, axes, positions  all given; positions: device, [axes->n_axes][n] int64
+ * All else as mla_cache_append_rope.
+ */
+mla_status_t mla_cache_append_rope_axes(uint8_t* pool, int64_t num_pages, int32_t page_size,
+                                        const void* x, int64_t x_stride, const int64_t* slots,
+                                        int64_t n, float kv_scale, const void* norm_weight, float eps,
+                                        const mla_rope_t* rope, const mla_rope_axes_t* axes,
+                                        const int64_t* positions, unsigned* status, void* stream);
 
 /*
  * Read cached rows back: positions starts[b], starts[b] + 1, ... of sequence b, dequantised

@@ -26,6 +26,7 @@ MLA_DV = 512
 MLA_ROPE = 64
 MLA_MAX_TREE = 64
 MLA_MAX_VOCAB = 1 << 19
+MLA_MAX_AXES = 4
 MLA_OP_DECODE, MLA_OP_VERIFY, MLA_OP_PREFILL, MLA_OP_VERIFY_TREE = 0, 1, 2, 3
 (MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_WORKSPACE, MLA_ERR_CUDA,
  MLA_ERR_TIMEOUT, MLA_ERR_BOUNDS) = range(7)
@@ -40,7 +41,8 @@ EXPORTS = ("mla_workspace_size", "mla_decode", "mla_verify", "mla_prefill", "mla
            "mla_prefill_mha_workspace_size", "mla_test_stall_next_call",
            "mla_read_status_static", "mla_set_trace_buffer", "mla_verify_f32_shard",
            "mla_prefill_mha_bf16", "mla_rope_init", "mla_rope", "mla_cache_append_rope",
-           "mla_cache_gather", "mla_verify_tree", "mla_accept_drafts")
+           "mla_cache_gather", "mla_verify_tree", "mla_accept_drafts", "mla_rope_axes_init",
+           "mla_rope_axes", "mla_cache_append_rope_axes")
 
 
 _U8, _I32, _I64, _F32, _BF16 = (torch.uint8, torch.int32, torch.int64, torch.float32,
@@ -65,6 +67,11 @@ class mla_rope_t(ctypes.Structure):
     """Rotary frequencies as mla_rope_init fills them (see include/mla.h)."""
     _fields_ = [("turns", ctypes.c_uint64 * (MLA_ROPE // 2)), ("amplitude", ctypes.c_float),
                 ("interleaved", ctypes.c_int32)]
+
+
+class mla_rope_axes_t(ctypes.Structure):
+    """The position axis of each RoPE pair as mla_rope_axes_init fills it (see include/mla.h)."""
+    _fields_ = [("axis", ctypes.c_uint8 * (MLA_ROPE // 2)), ("n_axes", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -117,8 +124,13 @@ def _load() -> ctypes.CDLL:
     lib.mla_cache_gather.argtypes = [KV, i32, P, P, i64, P, i32, P, P]
     lib.mla_verify_tree.argtypes = [KV, P, i32, i32, i32, f32, P, P, P, P, sz, P]
     lib.mla_accept_drafts.argtypes = [P, P, P, P, P, i32, i32, i32, P, P, P, P]
+    AXES = ctypes.POINTER(mla_rope_axes_t)
+    lib.mla_rope_axes_init.argtypes = [AXES, ctypes.POINTER(ctypes.c_int32), i32, i32]
+    lib.mla_rope_axes.argtypes = [ROPE, AXES, P, i64, i64, P, i64, i32, P, i64, i64, P]
+    lib.mla_cache_append_rope_axes.argtypes = [P, i64, i32, P, i64, P, i64, f32, P, f32, ROPE, AXES, P, P, P]
     for name in ("mla_rope_init", "mla_rope", "mla_cache_append_rope", "mla_cache_gather",
-                 "mla_verify_tree", "mla_accept_drafts"):
+                 "mla_verify_tree", "mla_accept_drafts", "mla_rope_axes_init", "mla_rope_axes",
+                 "mla_cache_append_rope_axes"):
         getattr(lib, name).restype = i32
     for name in ("mla_decode", "mla_verify", "mla_prefill", "mla_merge_lse", "mla_read_status",
                  "mla_last_launch_count"):
@@ -420,6 +432,28 @@ def mla_rope_init(base: float = 10000.0, factor: float = 1.0, original_positions
     return rope
 
 
+def mla_rope_axes_init(sections, interleaved: bool = False) -> mla_rope_axes_t:
+    """Positions with several axes (time, height, width): `sections` gives the number of RoPE pairs
+    (32 in all) that each axis turns, one section after the other or, interleaved, the axes taking
+    pairs in turn while they have any left. Kept by the caller and handed to mla_rope and the cache
+    writes with positions int64 [len(sections), n]."""
+    axes = mla_rope_axes_t()
+    sections = [int(k) for k in sections]
+    _check("mla_rope_axes_init", library().mla_rope_axes_init(
+        axes, (ctypes.c_int32 * len(sections))(*sections), len(sections), int(interleaved)))
+    return axes
+
+
+def _positions_ptr(positions: Optional[torch.Tensor], axes: Optional[mla_rope_axes_t], n: int,
+                   dev: torch.device) -> Optional[int]:
+    """Pointer of positions int64 [n], or [axes, n]."""
+    if positions is None:
+        if axes is not None:
+            raise ValueError("axes need positions")
+        return None
+    return _dense(positions, "positions", _I64, (n,) if axes is None else (axes.n_axes, n), dev)
+
+
 def _rope_part(t: torch.Tensor, name: str):
     """Shape and strides of a view of the RoPE dims."""
     if t.dtype is _BF16 and t.dim() == 3 and t.is_cuda:
@@ -432,12 +466,13 @@ def _rope_part(t: torch.Tensor, name: str):
 
 
 def mla_rope(rope: mla_rope_t, x: torch.Tensor, positions: torch.Tensor, out=None,
-             stream=None) -> torch.Tensor:
+             stream=None, axes: Optional[mla_rope_axes_t] = None) -> torch.Tensor:
     """Rotate x [n, H, 64] bf16 (a view of the RoPE dims, e.g. q[..., 512:] or q_mha[..., 128:])
-    to positions int64 [n]. `out` may be another such view, or x itself (in place)."""
+    to positions int64 [n], or [axes.n_axes, n] where `axes` says which axis each pair turns by.
+    `out` may be another such view, or x itself (in place)."""
     if stream is not None:
         with _current(stream):
-            return mla_rope(rope, x, positions, out)
+            return mla_rope(rope, x, positions, out, axes=axes)
     n, H, xt, xh = _rope_part(x, "x")
     dev = x.device
     if out is None:
@@ -445,40 +480,55 @@ def mla_rope(rope: mla_rope_t, x: torch.Tensor, positions: torch.Tensor, out=Non
     m, G, ot, oh = _rope_part(out, "out")
     if m != n or G != H or out.device != dev or (n > 1 and ot == 0) or (H > 1 and oh == 0):
         raise ValueError("out must have x's shape and device, and a place of its own for every element")
-    _check("mla_rope", library().mla_rope(
-        rope, x.data_ptr(), xt, xh, _dense(positions, "positions", _I64, (n,), dev), n, H,
-        out.data_ptr(), ot, oh, _on(dev)))
+    if axes is None:
+        _check("mla_rope", library().mla_rope(
+            rope, x.data_ptr(), xt, xh, _dense(positions, "positions", _I64, (n,), dev), n, H,
+            out.data_ptr(), ot, oh, _on(dev)))
+    else:
+        _check("mla_rope_axes", library().mla_rope_axes(
+            rope, axes, x.data_ptr(), xt, xh, _positions_ptr(positions, axes, n, dev), n, H,
+            out.data_ptr(), ot, oh, _on(dev)))
     return out
 
 
 def mla_cache_append_rope(pool: torch.Tensor, x: torch.Tensor, slots: torch.Tensor, kv_scale: float,
                           rope: Optional[mla_rope_t] = None, positions: Optional[torch.Tensor] = None,
                           norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
-                          status: Optional[torch.Tensor] = None, stream=None) -> None:
+                          status: Optional[torch.Tensor] = None, stream=None,
+                          axes: Optional[mla_rope_axes_t] = None) -> None:
     """mla_cache_append for rows x [n, 576] bf16 as the latent projection leaves them: the
     latent is normalised by its root mean square and weighted with norm_weight [512] bf16
-    (None: as it is), the 64 RoPE dims are turned to positions int64 [n] (rope None: as they
-    are), and both are quantised in one pass. x may be a slice of a wider projection's rows."""
+    (None: as it is), the 64 RoPE dims are turned to positions int64 [n] (with `axes`,
+    [axes.n_axes, n]; rope None: as they are), and both are quantised in one pass. x may be a
+    slice of a wider projection's rows."""
     if stream is not None:
         with _current(stream):
-            return mla_cache_append_rope(pool, x, slots, kv_scale, rope, positions, norm_weight, eps, status)
+            return mla_cache_append_rope(pool, x, slots, kv_scale, rope, positions, norm_weight, eps, status,
+                                         axes=axes)
     if pool.dtype is not _U8 or pool.dim() != 3 or not pool.is_contiguous() or not pool.is_cuda or \
             pool.shape[2] != MLA_D:
         raise ValueError("pool must be a contiguous uint8 CUDA tensor [num_pages, page_size, 576]")
     pages, size, _ = pool.shape
     dev = pool.device
+    n, stride = _latent_rows(x, dev)
+    if (rope is None) != (positions is None):
+        raise ValueError("give rope and positions together, or neither")
+    args = (pool.data_ptr(), pages, size, x.data_ptr(), stride, _dense(slots, "slots", _I64, (n,), dev), n, kv_scale,
+            None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, (MLA_DV,), dev), eps, rope)
+    at, word = _positions_ptr(positions, axes, n, dev), _status_ptr(status, dev)
+    if axes is None:
+        _check("mla_cache_append_rope", library().mla_cache_append_rope(*args, at, word, _on(dev)))
+    else:
+        _check("mla_cache_append_rope_axes", library().mla_cache_append_rope_axes(*args, axes, at, word, _on(dev)))
+
+
+def _latent_rows(x: torch.Tensor, dev: torch.device):
+    """Number and stride of rows x [n, 576] that a cache write takes."""
     if x.dtype is not _BF16 or x.dim() != 2 or x.shape[1] != MLA_D or x.stride(1) != 1 or \
             x.device != dev:
         raise ValueError("x must be a bfloat16 tensor [n, 576] on the pool's device, its rows contiguous")
-    if (rope is None) != (positions is None):
-        raise ValueError("give rope and positions together, or neither")
     n = x.shape[0]
-    _check("mla_cache_append_rope", library().mla_cache_append_rope(
-        pool.data_ptr(), pages, size, x.data_ptr(), x.stride(0) if n > 1 else MLA_D,
-        _dense(slots, "slots", _I64, (n,), dev), n, kv_scale,
-        None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, (MLA_DV,), dev),
-        eps, rope, None if positions is None else _dense(positions, "positions", _I64, (n,), dev),
-        _status_ptr(status, dev), _on(dev)))
+    return n, x.stride(0) if n > 1 else MLA_D
 
 
 def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optional[torch.Tensor] = None,

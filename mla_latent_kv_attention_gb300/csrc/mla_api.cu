@@ -71,6 +71,17 @@ mla_status_t current_device(int* dev) {
   return MLA_OK;
 }
 
+// The axes of the pairs in the kernels' form; false: n_axes or an axis out of range.
+bool pair_axes(const mla_rope_axes_t* axes, mla::PairAxes* out) {
+  if (!axes || axes->n_axes < 1 || axes->n_axes > MLA_MAX_AXES) return false;
+  out->bits = 0;
+  for (int i = 0; i < MLA_ROPE / 2; ++i) {
+    if (axes->axis[i] >= axes->n_axes) return false;
+    out->bits |= (uint64_t)axes->axis[i] << (2 * i);
+  }
+  return true;
+}
+
 // Set by mla_test_stall_next_call; consumed (and cleared) by the next decode/verify call on
 // this thread.
 thread_local int g_test_stall = 0;
@@ -407,10 +418,11 @@ mla_status_t mla_cache_append(uint8_t* pool, int64_t num_pages, int32_t page_siz
   return MLA_OK;
 }
 
-mla_status_t mla_rope(const mla_rope_t* rope, const void* x, int64_t x_token_stride,
+namespace {
+
+mla_status_t run_rope(const mla_rope_t* rope, const mla::PairAxes* axes, const void* x, int64_t x_token_stride,
                       int64_t x_head_stride, const int64_t* positions, int64_t n, int H, void* out,
                       int64_t out_token_stride, int64_t out_head_stride, void* stream) {
-  g_last_launches = 0;
   if (!rope || n < 0 || H < 0) return MLA_ERR_INVALID_ARG;
   if (n == 0 || H == 0) return MLA_OK;
   if (!x || !out || !positions) return MLA_ERR_INVALID_ARG;
@@ -423,7 +435,7 @@ mla_status_t mla_rope(const mla_rope_t* rope, const void* x, int64_t x_token_str
   if (st != MLA_OK) return st;
   const int sms = sm_count(dev);
   if (sms <= 0) return MLA_ERR_CUDA;
-  if (mla::launch_rope(*rope, static_cast<const uint16_t*>(x), x_token_stride, x_head_stride,
+  if (mla::launch_rope(*rope, axes, static_cast<const uint16_t*>(x), x_token_stride, x_head_stride,
                        positions, n, H, static_cast<uint16_t*>(out), out_token_stride,
                        out_head_stride, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
@@ -433,19 +445,18 @@ mla_status_t mla_rope(const mla_rope_t* rope, const void* x, int64_t x_token_str
   return MLA_OK;
 }
 
-mla_status_t mla_cache_append_rope(uint8_t* pool, int64_t num_pages, int32_t page_size,
-                                   const void* x, int64_t x_stride, const int64_t* slots, int64_t n,
-                                   float kv_scale, const void* norm_weight, float eps,
-                                   const mla_rope_t* rope, const int64_t* positions,
-                                   unsigned* status, void* stream) {
-  g_last_launches = 0;
+mla_status_t run_append_rope(uint8_t* pool, int64_t num_pages, int32_t page_size, const void* x,
+                             int64_t x_stride, const int64_t* slots, int64_t n, float kv_scale,
+                             const void* norm_weight, float eps, const mla_rope_t* rope,
+                             const mla::PairAxes* axes, const int64_t* positions, unsigned* status,
+                             void* stream) {
   if (n < 0 || num_pages < 0 || page_size <= 0) return MLA_ERR_INVALID_ARG;
   if (!(kv_scale > 0.f) || !(kv_scale < INFINITY)) return MLA_ERR_INVALID_ARG;
   if (norm_weight && (!(eps >= 0.f) || !(eps < INFINITY))) return MLA_ERR_INVALID_ARG;
   if ((rope == nullptr) != (positions == nullptr) && n > 0) return MLA_ERR_INVALID_ARG;
   if (x_stride < MLA_D || x_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
   if (n == 0) return MLA_OK;
-  if (!pool || !x || !slots) return MLA_ERR_INVALID_ARG;
+  if (!pool || !x || !slots || (axes && !rope)) return MLA_ERR_INVALID_ARG;
   if (!aligned(pool, 16) || !aligned(x, 16) || !aligned(slots, 8) || !aligned(norm_weight, 16) ||
       !aligned(positions, 8) || !aligned(status, 4))
     return MLA_ERR_INVALID_ARG;
@@ -468,13 +479,56 @@ mla_status_t mla_cache_append_rope(uint8_t* pool, int64_t num_pages, int32_t pag
   a.status = status;
   mla_rope_t none = {};
   none.interleaved = 1;
-  if (mla::launch_cache_append_rope(a, rope ? *rope : none, sms, static_cast<cudaStream_t>(stream)) !=
+  if (mla::launch_cache_append_rope(a, rope ? *rope : none, axes, sms, static_cast<cudaStream_t>(stream)) !=
       cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;
   }
   ++g_last_launches;
   return MLA_OK;
+}
+
+}  // namespace
+
+mla_status_t mla_rope(const mla_rope_t* rope, const void* x, int64_t x_token_stride,
+                      int64_t x_head_stride, const int64_t* positions, int64_t n, int H, void* out,
+                      int64_t out_token_stride, int64_t out_head_stride, void* stream) {
+  g_last_launches = 0;
+  return run_rope(rope, nullptr, x, x_token_stride, x_head_stride, positions, n, H, out, out_token_stride,
+                  out_head_stride, stream);
+}
+
+mla_status_t mla_rope_axes(const mla_rope_t* rope, const mla_rope_axes_t* axes, const void* x,
+                           int64_t x_token_stride, int64_t x_head_stride, const int64_t* positions,
+                           int64_t n, int H, void* out, int64_t out_token_stride,
+                           int64_t out_head_stride, void* stream) {
+  g_last_launches = 0;
+  mla::PairAxes pairs;
+  if (!pair_axes(axes, &pairs)) return MLA_ERR_INVALID_ARG;
+  return run_rope(rope, &pairs, x, x_token_stride, x_head_stride, positions, n, H, out, out_token_stride,
+                  out_head_stride, stream);
+}
+
+mla_status_t mla_cache_append_rope(uint8_t* pool, int64_t num_pages, int32_t page_size,
+                                   const void* x, int64_t x_stride, const int64_t* slots, int64_t n,
+                                   float kv_scale, const void* norm_weight, float eps,
+                                   const mla_rope_t* rope, const int64_t* positions,
+                                   unsigned* status, void* stream) {
+  g_last_launches = 0;
+  return run_append_rope(pool, num_pages, page_size, x, x_stride, slots, n, kv_scale, norm_weight, eps, rope,
+                         nullptr, positions, status, stream);
+}
+
+mla_status_t mla_cache_append_rope_axes(uint8_t* pool, int64_t num_pages, int32_t page_size,
+                                        const void* x, int64_t x_stride, const int64_t* slots,
+                                        int64_t n, float kv_scale, const void* norm_weight, float eps,
+                                        const mla_rope_t* rope, const mla_rope_axes_t* axes,
+                                        const int64_t* positions, unsigned* status, void* stream) {
+  g_last_launches = 0;
+  mla::PairAxes pairs;
+  if (!pair_axes(axes, &pairs)) return MLA_ERR_INVALID_ARG;
+  return run_append_rope(pool, num_pages, page_size, x, x_stride, slots, n, kv_scale, norm_weight, eps, rope,
+                         &pairs, positions, status, stream);
 }
 
 mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,

@@ -74,9 +74,11 @@ __global__ void __launch_bounds__(256) cache_append_kernel(uint8_t* __restrict__
 // for fewer (8,192 rows are 1,024 CTAs, of which 608 run at once, each a chain of load, norm and
 // write: 4.2 us in L2, 6.0 us from HBM), the launch alone for 32 (1.9 us). The half layout's two-byte
 // loads and byte exchange add 0.4 to 0.6 us.
+// AXES: positions [axes][n], lane l's pair by its own axis'.
+template <bool AXES>
 __global__ void __launch_bounds__(256, 4)  // (four: 8,192 rows 4.3 us; left open 4.85, six 4.9)
     cache_append_rope_kernel(const __grid_constant__ AppendRopeArgs a,
-                             const __grid_constant__ mla_rope_t rope) {
+                             const __grid_constant__ mla_rope_t rope, const PairAxes axes) {
   __shared__ uint64_t s_turns[MLA_ROPE / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = blockDim.x >> 5;
@@ -90,7 +92,10 @@ __global__ void __launch_bounds__(256, 4)  // (four: 8,192 rows 4.3 us; left ope
     uint32_t pair = 0;  // this lane's RoPE pair, the first entry in the low half
     if (i < a.n) {
       slot = a.slots[i];
-      if (a.positions) position = a.positions[i];
+      if (AXES)
+        position = a.positions[axes.of(lane) * a.n + i];
+      else if (a.positions)
+        position = a.positions[i];
       const uint16_t* row = a.x + i * a.x_stride;
       const uint4* src = reinterpret_cast<const uint4*>(row) + 2 * lane;
       v0 = src[0], v1 = src[1];
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(256, 4)  // (four: 8,192 rows 4.3 us; left ope
       }
     }
     float2 pe = make_float2(__uint_as_float(pair << 16), __uint_as_float(pair & 0xFFFF0000u));
-    if (a.positions)
+    if (AXES || a.positions)
       pe = rope_turn(pe.x, pe.y, rope_cos_sin(s_turns[lane], position, rope.amplitude));
     uint32_t code[4];
 #pragma unroll
@@ -242,12 +247,15 @@ __global__ void __launch_bounds__(kGatherThreads)
 
 }  // namespace
 
-cudaError_t launch_cache_append_rope(const AppendRopeArgs& a, const mla_rope_t& rope, int num_sms,
-                                     cudaStream_t s) {
+cudaError_t launch_cache_append_rope(const AppendRopeArgs& a, const mla_rope_t& rope, const PairAxes* axes,
+                                     int num_sms, cudaStream_t s) {
   // one warp per row, at most 8 CTAs per SM (of which four run at once)
   const int64_t blocks = (a.n * 32 + 255) / 256;
   const int grid = (int)(blocks < (int64_t)num_sms * 8 ? blocks : (int64_t)num_sms * 8);
-  cache_append_rope_kernel<<<grid, 256, 0, s>>>(a, rope);
+  if (axes)
+    cache_append_rope_kernel<true><<<grid, 256, 0, s>>>(a, rope, *axes);
+  else
+    cache_append_rope_kernel<false><<<grid, 256, 0, s>>>(a, rope, PairAxes{0});
   return cudaGetLastError();
 }
 

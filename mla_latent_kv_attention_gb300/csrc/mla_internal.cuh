@@ -257,9 +257,15 @@ cudaError_t launch_merge_standalone(const float* part_out, const float* part_lse
 cudaError_t launch_cache_append(uint8_t* pool, int64_t pool_rows, const uint16_t* x,
                                 const int64_t* slots, int64_t n, float inv, unsigned* status,
                                 int num_sms, cudaStream_t s);
-cudaError_t launch_rope(const mla_rope_t& rope, const uint16_t* x, int64_t x_token, int64_t x_head,
-                        const int64_t* positions, int64_t n, int H, uint16_t* out, int64_t out_token,
-                        int64_t out_head, int num_sms, cudaStream_t s);
+// The axes of the 32 RoPE pairs, two bits a pair from the lowest up (MLA_MAX_AXES is 4).
+struct PairAxes {
+  uint64_t bits;
+  __host__ __device__ __forceinline__ int of(int pair) const { return (int)(bits >> (2 * pair)) & 3; }
+};
+// positions: [n], or [axes][n] where `axes` is given
+cudaError_t launch_rope(const mla_rope_t& rope, const PairAxes* axes, const uint16_t* x, int64_t x_token,
+                        int64_t x_head, const int64_t* positions, int64_t n, int H, uint16_t* out,
+                        int64_t out_token, int64_t out_head, int num_sms, cudaStream_t s);
 struct AppendRopeArgs {
   uint8_t* pool;
   int64_t pool_rows;
@@ -270,11 +276,11 @@ struct AppendRopeArgs {
   float inv;               // 1 / kv_scale
   const uint16_t* weight;  // [512] bf16, or null: the latent is not normalised
   float eps;
-  const int64_t* positions;  // [n], or null: no rotation
+  const int64_t* positions;  // [n], or null: no rotation; [axes][n] where the launch is given axes
   unsigned* status;        // or null
 };
-cudaError_t launch_cache_append_rope(const AppendRopeArgs& a, const mla_rope_t& rope, int num_sms,
-                                     cudaStream_t s);
+cudaError_t launch_cache_append_rope(const AppendRopeArgs& a, const mla_rope_t& rope, const PairAxes* axes,
+                                     int num_sms, cudaStream_t s);
 cudaError_t launch_cache_gather(const mla_kv_t& kv, int B, const int32_t* starts,
                                 const int64_t* cu_rows, int64_t n, void* out, int out_f32,
                                 unsigned* status, cudaStream_t s);

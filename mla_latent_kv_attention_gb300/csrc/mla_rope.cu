@@ -25,10 +25,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // HEADS: heads a thread turns (loads of all of them in flight together).
-template <bool INTERLEAVED, int HEADS>
+// AXES: positions [axes][n], each pair by its own axis' (its position is loaded where it is used:
+// the quarter's eight pairs read at most four words, the first of each from L2, in flight with x).
+template <bool INTERLEAVED, int HEADS, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_kernel(const __grid_constant__ mla_rope_t rope, const uint16_t* x, int64_t x_token,
-                int64_t x_head, const int64_t* __restrict__ positions, int64_t n, int H,
+    rope_kernel(const __grid_constant__ mla_rope_t rope, const PairAxes axes, const uint16_t* x,
+                int64_t x_token, int64_t x_head, const int64_t* __restrict__ positions, int64_t n, int H,
                 uint16_t* out, int64_t out_token, int64_t out_head) {
   const int parts = (H + HEADS - 1) / HEADS;
   const int64_t item = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 2;
@@ -48,10 +50,18 @@ __global__ void __launch_bounds__(kRopeThreads)
       a[h] = *reinterpret_cast<const uint4*>(src + h * x_head + d0);
       b[h] = *reinterpret_cast<const uint4*>(src + h * x_head + d1);
     }
-  const int64_t position = positions[token];
   float2 cs[8];
+  if constexpr (AXES) {
+    int64_t position[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = rope_cos_sin(rope.turns[8 * quarter + i], position, rope.amplitude);
+    for (int i = 0; i < 8; ++i) position[i] = positions[axes.of(8 * quarter + i) * n + token];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = rope_cos_sin(rope.turns[8 * quarter + i], position[i], rope.amplitude);
+  } else {
+    const int64_t position = positions[token];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = rope_cos_sin(rope.turns[8 * quarter + i], position, rope.amplitude);
+  }
 #pragma unroll
   for (int h = 0; h < HEADS; ++h) {
     if (h0 + h >= H) break;
@@ -80,9 +90,10 @@ __global__ void __launch_bounds__(kRopeThreads)
 
 }  // namespace
 
-cudaError_t launch_rope(const mla_rope_t& rope, const uint16_t* x, int64_t x_token, int64_t x_head,
-                        const int64_t* positions, int64_t n, int H, uint16_t* out, int64_t out_token,
-                        int64_t out_head, int num_sms, cudaStream_t s) {
+template <bool AXES>
+static cudaError_t launch_rope_with(const mla_rope_t& rope, PairAxes axes, const uint16_t* x, int64_t x_token,
+                                    int64_t x_head, const int64_t* positions, int64_t n, int H, uint16_t* out,
+                                    int64_t out_token, int64_t out_head, int num_sms, cudaStream_t s) {
   // Four heads a thread share their angles. Where that would leave an SM with less than two
   // warps, one head a thread: more threads, each with a shorter wait. In us, one / four, at 12
   // heads, interleaved, in L2: 32 tokens 1.9 / 2.3, 512 2.2 / 2.3, 1,024 2.4 / 2.4, 4,096 4.3 / 3.8, 8,192 7.0 / 5.4;
@@ -92,21 +103,31 @@ cudaError_t launch_rope(const mla_rope_t& rope, const uint16_t* x, int64_t x_tok
   const int64_t threads = n * ((H + heads - 1) / heads) * 4;
   const unsigned grid = (unsigned)((threads + kRopeThreads - 1) / kRopeThreads);
   auto go = [&](auto kernel) {
-    kernel<<<grid, kRopeThreads, 0, s>>>(rope, x, x_token, x_head, positions, n, H, out, out_token,
+    kernel<<<grid, kRopeThreads, 0, s>>>(rope, axes, x, x_token, x_head, positions, n, H, out, out_token,
                                          out_head);
   };
   if (rope.interleaved) {
     if (many)
-      go(rope_kernel<true, 4>);
+      go(rope_kernel<true, 4, AXES>);
     else
-      go(rope_kernel<true, 1>);
+      go(rope_kernel<true, 1, AXES>);
   } else {
     if (many)
-      go(rope_kernel<false, 4>);
+      go(rope_kernel<false, 4, AXES>);
     else
-      go(rope_kernel<false, 1>);
+      go(rope_kernel<false, 1, AXES>);
   }
   return cudaGetLastError();
+}
+
+cudaError_t launch_rope(const mla_rope_t& rope, const PairAxes* axes, const uint16_t* x, int64_t x_token,
+                        int64_t x_head, const int64_t* positions, int64_t n, int H, uint16_t* out,
+                        int64_t out_token, int64_t out_head, int num_sms, cudaStream_t s) {
+  if (axes)
+    return launch_rope_with<true>(rope, *axes, x, x_token, x_head, positions, n, H, out, out_token, out_head,
+                                  num_sms, s);
+  return launch_rope_with<false>(rope, PairAxes{0}, x, x_token, x_head, positions, n, H, out, out_token,
+                                 out_head, num_sms, s);
 }
 
 }  // namespace mla
@@ -142,5 +163,27 @@ extern "C" mla_status_t mla_rope_init(mla_rope_t* rope, double base, double fact
   }
   rope->amplitude = amplitude;
   rope->interleaved = interleaved != 0;
+  return MLA_OK;
+}
+
+extern "C" mla_status_t mla_rope_axes_init(mla_rope_axes_t* axes, const int32_t* sections, int n_axes,
+                                           int interleaved) {
+  constexpr int kPairs = MLA_ROPE / 2;
+  if (!axes || !sections || n_axes < 1 || n_axes > MLA_MAX_AXES) return MLA_ERR_INVALID_ARG;
+  int left[MLA_MAX_AXES] = {0}, sum = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (sections[a] < 0 || sections[a] > kPairs) return MLA_ERR_INVALID_ARG;
+    left[a] = sections[a];
+    sum += sections[a];
+  }
+  if (sum != kPairs) return MLA_ERR_INVALID_ARG;
+  int a = interleaved ? n_axes - 1 : 0;  // the axis of the pair before
+  for (int i = 0; i < kPairs; ++i) {
+    if (interleaved) a = (a + 1) % n_axes;
+    while (left[a] == 0) a = (a + 1) % n_axes;
+    axes->axis[i] = (uint8_t)a;
+    --left[a];
+  }
+  axes->n_axes = n_axes;
   return MLA_OK;
 }
