@@ -92,6 +92,22 @@ typedef struct mla_kv {
 } mla_kv_t;
 
 /*
+ * Scales of a cache that keeps one for each block of positions instead of one for the whole tensor
+ * (one latent serves all heads, so a block has one scale, not one a head): a cached value is
+ *     e4m3(code) * scale[(page * page_size + offset in the page) / block].
+ *   scale  device, [num_pages * page_size / block] float32, 4-byte aligned
+ *   block  positions that share a scale: 1, 2, 4, .. 64 (a page is a multiple of 64, so a block
+ *          lies in one page)
+ * The calls that take scales (mla_*_scaled) do not read kv->kv_scale. mla_cache_append_scaled writes
+ * powers of two; others may hold any float32 from 2^-60 to 2^60. A scale outside that range (zero,
+ * NaN, infinite, negative) makes the rows that see one of its positions NaN.
+ */
+typedef struct mla_scales {
+  float* scale;
+  int32_t block;
+} mla_scales_t;
+
+/*
  * Bytes of workspace the given call needs on `device` (a CUDA ordinal). The workspace
  * holds the per-split partial outputs, staged query rows and one status word per CTA (it
  * depends on H, n_q and the SM count, not on B, except for MLA_OP_VERIFY_TREE, which stages every
@@ -389,6 +405,50 @@ mla_status_t mla_cache_append_rope_axes(uint8_t* pool, int64_t num_pages, int32_
 mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
                               const int64_t* cu_rows, int64_t n, void* out, int out_is_f32,
                               unsigned* status, void* stream);
+
+/*
+ * Append new latent rows to a cache with a scale for each block of positions, choosing the scales:
+ * the last m = cu_rows[b + 1] - cu_rows[b] of sequence b's seq_lens[b] cached positions are new, and
+ * x's rows cu_rows[b] .. cu_rows[b + 1] - 1 are theirs. y, the row that is cached, comes from x as in
+ * mla_cache_append_rope (norm, rotation; axes may be given). A block that new positions fall into
+ * gets the scale
+ *     s = max(s_old, 2^ceil(log2(max |y| / 448)))   over its new rows' finite entries,
+ * s_old being its scale if it holds earlier positions of the sequence (a block that begins with a
+ * new position starts afresh), the power of two clamped to 2^-60 .. 2^60 (2^-60 where all is zero).
+ * The new codes are e4m3(y / s), rounded to nearest even, infinities and anything past the clamp
+ * saturating, NaN kept; where s > s_old the earlier positions' codes become e4m3(code * s_old / s).
+ * With powers of two that shifts their exponents: what was rounded once is not rounded again, but
+ * for entries that reach e4m3's subnormals (2^-7 s and below). Earlier positions whose s_old is no scale (see
+ * mla_scales_t) become NaN. Codes behind the sequence's last position stay as they were.
+ *   kv           the cache (the pool is written); seq_lens includes the new positions, whose pages
+ *                are in the table
+ *   scales       written
+ *   x            device, rows of 576 bfloat16 x_stride elements apart (>= 576, a multiple of 8),
+ *                16-byte aligned
+ *   cu_rows      device, [B + 1] int64, non-decreasing; x's rows outside cu_rows[0] ..
+ *                cu_rows[B] - 1 are not read
+ *   n            rows of x
+ *   norm_weight  device, [512] bfloat16, 16-byte aligned, or NULL; eps as mla_cache_append_rope
+ *   rope, positions  both given, or both NULL: no rotation. positions: device, [n] int64, or
+ *                [axes->n_axes][n] where axes is given
+ *   status       device word or NULL: set to MLA_ERR_BOUNDS (if it held 0) for a sequence with more
+ *                new rows than positions, longer than its table, or with rows outside x (none of
+ *                it is written), and for a page outside the pool (its positions are not written)
+ * No two sequences may hold new positions in the same block. One launch.
+ */
+mla_status_t mla_cache_append_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* x,
+                                     int64_t x_stride, const int64_t* cu_rows, int B, int64_t n,
+                                     const void* norm_weight, float eps, const mla_rope_t* rope,
+                                     const mla_rope_axes_t* axes, const int64_t* positions,
+                                     unsigned* status, void* stream);
+
+/*
+ * mla_cache_gather from a cache with block scales: values are e4m3(code) * scale (one float32
+ * product, then rounded to the output's type).
+ */
+mla_status_t mla_cache_gather_scaled(const mla_kv_t* kv, const mla_scales_t* scales, int B,
+                                     const int32_t* starts, const int64_t* cu_rows, int64_t n,
+                                     void* out, int out_is_f32, unsigned* status, void* stream);
 
 /*
  * mla_verify for a tree of drafted tokens: n nodes per sequence (1..64), their rows the last n

@@ -42,9 +42,11 @@ EXPORTS = ("mla_workspace_size", "mla_decode", "mla_verify", "mla_prefill", "mla
            "mla_read_status_static", "mla_set_trace_buffer", "mla_verify_f32_shard",
            "mla_prefill_mha_bf16", "mla_rope_init", "mla_rope", "mla_cache_append_rope",
            "mla_cache_gather", "mla_verify_tree", "mla_accept_drafts", "mla_rope_axes_init",
-           "mla_rope_axes", "mla_cache_append_rope_axes")
+           "mla_rope_axes", "mla_cache_append_rope_axes", "mla_cache_append_scaled",
+           "mla_cache_gather_scaled")
 
 
+_BLOCKS = (1, 2, 4, 8, 16, 32, 64)
 _U8, _I32, _I64, _F32, _BF16 = (torch.uint8, torch.int32, torch.int64, torch.float32,
                                 torch.bfloat16)
 
@@ -61,6 +63,10 @@ class mla_kv_t(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("page_table", ctypes.c_void_p),
                 ("page_table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
                 ("kv_scale", ctypes.c_float)]
+
+
+class mla_scales_t(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_void_p), ("block", ctypes.c_int32)]
 
 
 class mla_rope_t(ctypes.Structure):
@@ -128,9 +134,12 @@ def _load() -> ctypes.CDLL:
     lib.mla_rope_axes_init.argtypes = [AXES, ctypes.POINTER(ctypes.c_int32), i32, i32]
     lib.mla_rope_axes.argtypes = [ROPE, AXES, P, i64, i64, P, i64, i32, P, i64, i64, P]
     lib.mla_cache_append_rope_axes.argtypes = [P, i64, i32, P, i64, P, i64, f32, P, f32, ROPE, AXES, P, P, P]
+    SCALES = ctypes.POINTER(mla_scales_t)
+    lib.mla_cache_append_scaled.argtypes = [KV, SCALES, P, i64, P, i32, i64, P, f32, ROPE, AXES, P, P, P]
+    lib.mla_cache_gather_scaled.argtypes = [KV, SCALES, i32, P, P, i64, P, i32, P, P]
     for name in ("mla_rope_init", "mla_rope", "mla_cache_append_rope", "mla_cache_gather",
                  "mla_verify_tree", "mla_accept_drafts", "mla_rope_axes_init", "mla_rope_axes",
-                 "mla_cache_append_rope_axes"):
+                 "mla_cache_append_rope_axes", "mla_cache_append_scaled", "mla_cache_gather_scaled"):
         getattr(lib, name).restype = i32
     for name in ("mla_decode", "mla_verify", "mla_prefill", "mla_merge_lse", "mla_read_status",
                  "mla_last_launch_count"):
@@ -152,12 +161,31 @@ def library() -> ctypes.CDLL:
 @dataclasses.dataclass
 class KVCache:
     """Device-resident paged latent cache (see ``mla_kv_t`` in include/mla.h).
-    pool uint8 [num_pages, page_size, 576]; page_table int32 [B, stride]; seq_lens int32 [B]."""
+    pool uint8 [num_pages, page_size, 576]; page_table int32 [B, stride]; seq_lens int32 [B].
+    A cache with a scale for each block of positions (``mla_scales_t``) has ``scales`` float32
+    [num_pages, page_size / block], block 1, 2, 4, .. 64, in the place of kv_scale, which is then 1."""
 
     pool: torch.Tensor
     page_table: torch.Tensor
     seq_lens: torch.Tensor
     kv_scale: float
+    scales: Optional[torch.Tensor] = None
+
+    def c_scales(self) -> Optional[mla_scales_t]:
+        """The block scales, or None for a cache with one scale (after c_struct's checks)."""
+        t = self.scales
+        if t is None:
+            return None
+        pages, size = self.pool.shape[:2]
+        if t.dtype is not _F32 or not t.is_contiguous() or t.get_device() != self.pool.get_device():
+            raise ValueError("KVCache.scales must be a contiguous float32 tensor on the pool's device")
+        block = size // t.shape[1] if t.dim() == 2 and t.shape[1] > 0 else 0
+        if t.dim() != 2 or t.shape[0] != pages or block * t.shape[1] != size or block not in _BLOCKS:
+            raise ValueError("KVCache.scales must be [num_pages, page_size / block] for blocks of 1, 2, 4, .. 64 "
+                             f"positions, got {tuple(t.shape)} for {pages} pages of {size}")
+        if float(self.kv_scale) != 1.0:
+            raise ValueError("a KVCache with block scales has kv_scale 1 (it is not read)")
+        return mla_scales_t(t.data_ptr(), block)
 
     def c_struct(self) -> mla_kv_t:
         pool, table, lens = self.pool, self.page_table, self.seq_lens
@@ -531,12 +559,42 @@ def _latent_rows(x: torch.Tensor, dev: torch.device):
     return n, x.stride(0) if n > 1 else MLA_D
 
 
+def mla_cache_append_scaled(kv: KVCache, x: torch.Tensor, cu_rows: torch.Tensor,
+                            rope: Optional[mla_rope_t] = None, positions: Optional[torch.Tensor] = None,
+                            axes: Optional[mla_rope_axes_t] = None, norm_weight: Optional[torch.Tensor] = None,
+                            eps: float = 1e-6, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write new rows x [n, 576] bf16, as the latent projection leaves them, into a cache with block
+    scales, choosing the scales: rows cu_rows[b] .. cu_rows[b + 1] - 1 (int64 [B + 1]) are the last
+    of sequence b's kv.seq_lens[b] positions. Norm, rotation and arguments otherwise as
+    mla_cache_append_rope; kv.pool and kv.scales are written. A block's scale grows to the power of
+    two that its new rows need, its earlier rows' codes with it."""
+    if stream is not None:
+        with _current(stream):
+            return mla_cache_append_scaled(kv, x, cu_rows, rope, positions, axes, norm_weight, eps, status)
+    c = kv.c_struct()
+    scales = kv.c_scales()
+    if scales is None:
+        raise ValueError("kv has no block scales (KVCache.scales)")
+    dev = kv.pool.device
+    n, stride = _latent_rows(x, dev)
+    B = cu_rows.shape[0] - 1 if cu_rows.dim() == 1 else -1
+    if B < 0 or B > kv.seq_lens.shape[0] or B > kv.page_table.shape[0]:
+        raise ValueError("cu_rows must have an entry more than there are sequences")
+    if (rope is None) != (positions is None):
+        raise ValueError("give rope and positions together, or neither")
+    _check("mla_cache_append_scaled", library().mla_cache_append_scaled(
+        c, scales, x.data_ptr(), stride, _dense(cu_rows, "cu_rows", _I64, (B + 1,), dev), B, n,
+        None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, (MLA_DV,), dev), eps, rope, axes,
+        _positions_ptr(positions, axes, n, dev), _status_ptr(status, dev), _on(dev)))
+
+
 def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optional[torch.Tensor] = None,
                      out=None, dtype: torch.dtype = torch.bfloat16,
                      status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Cached rows read back and dequantised: rows cu_rows[b] .. cu_rows[b + 1] - 1 of out
     [n, 576] (bf16 or float32) are positions starts[b], starts[b] + 1, ... of sequence b.
-    cu_rows int64 [B + 1], starts int32 [B] (None: 0); rows outside them stay as they were."""
+    cu_rows int64 [B + 1], starts int32 [B] (None: 0); rows outside them stay as they were. A cache
+    with block scales is read under them."""
     if stream is not None:
         with _current(stream):
             return mla_cache_gather(kv, cu_rows, n, starts, out, dtype, status)
@@ -553,9 +611,13 @@ def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optiona
         out = torch.empty((n, MLA_D), dtype=dtype, device=dev)
     else:
         _dense(out, "out", _F32 if f32 else _BF16, (n, MLA_D), dev)
-    _check("mla_cache_gather", library().mla_cache_gather(
-        c, B, None if starts is None else _dense(starts, "starts", _I32, (B,), dev), cu_ptr, n,
-        out.data_ptr(), f32, _status_ptr(status, dev), _on(dev)))
+    args = (B, None if starts is None else _dense(starts, "starts", _I32, (B,), dev), cu_ptr, n,
+            out.data_ptr(), f32, _status_ptr(status, dev), _on(dev))
+    scales = kv.c_scales()
+    if scales is None:
+        _check("mla_cache_gather", library().mla_cache_gather(c, *args))
+    else:
+        _check("mla_cache_gather_scaled", library().mla_cache_gather_scaled(c, scales, *args))
     return out
 
 

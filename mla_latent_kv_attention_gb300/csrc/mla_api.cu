@@ -39,6 +39,13 @@ mla_status_t check_kv(const mla_kv_t* kv) {
   return MLA_OK;
 }
 
+mla_status_t check_scales(const mla_scales_t* scales) {
+  if (!scales || !scales->scale || !aligned(scales->scale, 4)) return MLA_ERR_INVALID_ARG;
+  const int block = scales->block;
+  if (block < 1 || block > 64 || (block & (block - 1)) != 0) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
 mla::AttnParams base_params(const mla_kv_t* kv, const void* q, int B, int n_q, int H,
                             float sm_scale, void* out, float* lse) {
   mla::AttnParams p = {};
@@ -531,10 +538,53 @@ mla_status_t mla_cache_append_rope_axes(uint8_t* pool, int64_t num_pages, int32_
                          &pairs, positions, status, stream);
 }
 
-mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
-                              const int64_t* cu_rows, int64_t n, void* out, int out_is_f32,
-                              unsigned* status, void* stream) {
+mla_status_t mla_cache_append_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* x,
+                                     int64_t x_stride, const int64_t* cu_rows, int B, int64_t n,
+                                     const void* norm_weight, float eps, const mla_rope_t* rope,
+                                     const mla_rope_axes_t* axes, const int64_t* positions,
+                                     unsigned* status, void* stream) {
   g_last_launches = 0;
+  mla_status_t st = check_kv(kv);
+  if (st != MLA_OK || (st = check_scales(scales)) != MLA_OK) return st;
+  mla::AppendScaledArgs a = {};
+  if (axes && !pair_axes(axes, &a.axes)) return MLA_ERR_INVALID_ARG;
+  if (B < 0 || n < 0) return MLA_ERR_INVALID_ARG;
+  if (norm_weight && (!(eps >= 0.f) || !(eps < INFINITY))) return MLA_ERR_INVALID_ARG;
+  if ((rope == nullptr) != (positions == nullptr) && n > 0) return MLA_ERR_INVALID_ARG;
+  if (x_stride < MLA_D || x_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (n == 0 || B == 0) return MLA_OK;
+  if (!x || !cu_rows || (axes && !rope)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(cu_rows, 8) || !aligned(norm_weight, 16) || !aligned(positions, 8) ||
+      !aligned(status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (n > (int64_t)1 << 30 || B > 1 << 28) return MLA_ERR_UNSUPPORTED;  // one grid
+  a.kv = *kv;
+  a.scale = scales->scale;
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_stride = x_stride;
+  a.cu_rows = cu_rows;
+  a.B = B;
+  a.n = n;
+  a.weight = static_cast<const uint16_t*>(norm_weight);
+  a.eps = eps;
+  a.positions = positions;
+  a.status = status;
+  mla_rope_t none = {};
+  none.interleaved = 1;
+  if (mla::launch_cache_append_scaled(a, rope ? *rope : none, scales->block, static_cast<cudaStream_t>(stream)) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  ++g_last_launches;
+  return MLA_OK;
+}
+
+namespace {
+
+mla_status_t run_gather(const mla_kv_t* kv, const mla_scales_t* scales, int B, const int32_t* starts,
+                        const int64_t* cu_rows, int64_t n, void* out, int out_is_f32, unsigned* status,
+                        void* stream) {
   const mla_status_t st = check_kv(kv);
   if (st != MLA_OK) return st;
   if (B < 0 || n < 0) return MLA_ERR_INVALID_ARG;
@@ -543,13 +593,31 @@ mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
   if (!aligned(starts, 4) || !aligned(cu_rows, 8) || !aligned(out, 16) || !aligned(status, 4))
     return MLA_ERR_INVALID_ARG;
   if (n > (int64_t)1 << 36) return MLA_ERR_UNSUPPORTED;  // one grid
-  if (mla::launch_cache_gather(*kv, B, starts, cu_rows, n, out, out_is_f32 != 0, status,
+  if (mla::launch_cache_gather(*kv, scales, B, starts, cu_rows, n, out, out_is_f32 != 0, status,
                                static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;
   }
   ++g_last_launches;
   return MLA_OK;
+}
+
+}  // namespace
+
+mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
+                              const int64_t* cu_rows, int64_t n, void* out, int out_is_f32,
+                              unsigned* status, void* stream) {
+  g_last_launches = 0;
+  return run_gather(kv, nullptr, B, starts, cu_rows, n, out, out_is_f32, status, stream);
+}
+
+mla_status_t mla_cache_gather_scaled(const mla_kv_t* kv, const mla_scales_t* scales, int B,
+                                     const int32_t* starts, const int64_t* cu_rows, int64_t n,
+                                     void* out, int out_is_f32, unsigned* status, void* stream) {
+  g_last_launches = 0;
+  const mla_status_t st = check_scales(scales);
+  if (st != MLA_OK) return st;
+  return run_gather(kv, scales, B, starts, cu_rows, n, out, out_is_f32, status, stream);
 }
 
 mla_status_t mla_accept_drafts(const float* target, const int32_t* tokens, const int32_t* parents,

@@ -167,12 +167,14 @@ constexpr int kGatherRows = 32;
 constexpr int kGatherThreads = 288;
 constexpr int64_t kRowSkip = -1, kRowBad = -2;
 
-template <typename Out>
+// SC: a scale for each block of 2^shift positions, read by the thread that found the row.
+template <typename Out, bool SC>
 __global__ void __launch_bounds__(kGatherThreads)
-    cache_gather_kernel(const __grid_constant__ mla_kv_t kv, int B, const int32_t* __restrict__ starts,
-                        const int64_t* __restrict__ cu_rows, int64_t n, Out* __restrict__ out,
-                        unsigned* status) {
+    cache_gather_kernel(const __grid_constant__ mla_kv_t kv, const float* __restrict__ scale, int shift, int B,
+                        const int32_t* __restrict__ starts, const int64_t* __restrict__ cu_rows, int64_t n,
+                        Out* __restrict__ out, unsigned* status) {
   __shared__ int64_t s_row[kGatherRows];  // pool row, or kRowSkip / kRowBad
+  __shared__ float s_scale[SC ? kGatherRows : 1];
   const int64_t row0 = (int64_t)blockIdx.x * kGatherRows;
   if (threadIdx.x < kGatherRows) {
     const int64_t row = row0 + threadIdx.x;
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(kGatherThreads)
       if (from == kRowBad && status) atomicCAS(status, 0u, (unsigned)MLA_ERR_BOUNDS);
     }
     s_row[threadIdx.x] = from;
+    if (SC) s_scale[threadIdx.x] = from >= 0 ? scale[from >> shift] : 0.f;
   }
   __syncthreads();
   constexpr int kCodes = 16 / sizeof(Out);          // a thread's piece of a row
@@ -221,14 +224,15 @@ __global__ void __launch_bounds__(kGatherThreads)
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
     if (s_row[kAtOnce * k + r] == kRowSkip) continue;
+    const float times = SC ? s_scale[kAtOnce * k + r] : kv.kv_scale;
     float2 v[kCodes / 2];
 #pragma unroll
     for (int e = 0; e < kCodes / 2; ++e) {
       const uint32_t two = (e & 1) ? code[k][e / 2] >> 16 : code[k][e / 2] & 0xFFFFu;
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
       v[e] = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      v[e].x *= kv.kv_scale;
-      v[e].y *= kv.kv_scale;
+      v[e].x *= times;
+      v[e].y *= times;
     }
     Out* dst = out + (row0 + kAtOnce * k + r) * kD + kCodes * piece;
     if constexpr (kCodes == 4) {
@@ -259,16 +263,22 @@ cudaError_t launch_cache_append_rope(const AppendRopeArgs& a, const mla_rope_t& 
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_gather(const mla_kv_t& kv, int B, const int32_t* starts,
-                                const int64_t* cu_rows, int64_t n, void* out, int out_f32,
-                                unsigned* status, cudaStream_t s) {
+cudaError_t launch_cache_gather(const mla_kv_t& kv, const mla_scales_t* scales, int B,
+                                const int32_t* starts, const int64_t* cu_rows, int64_t n, void* out,
+                                int out_f32, unsigned* status, cudaStream_t s) {
   const unsigned grid = (unsigned)((n + kGatherRows - 1) / kGatherRows);
-  if (out_f32)
-    cache_gather_kernel<float><<<grid, kGatherThreads, 0, s>>>(kv, B, starts, cu_rows, n,
-                                                               static_cast<float*>(out), status);
-  else
-    cache_gather_kernel<uint16_t><<<grid, kGatherThreads, 0, s>>>(kv, B, starts, cu_rows, n,
-                                                                  static_cast<uint16_t*>(out), status);
+  const float* scale = scales ? scales->scale : nullptr;
+  const int shift = scales ? block_shift(scales->block) : 0;
+  auto go = [&](auto kernel, auto* to) {
+    kernel<<<grid, kGatherThreads, 0, s>>>(kv, scale, shift, B, starts, cu_rows, n, to, status);
+  };
+  if (out_f32) {
+    float* to = static_cast<float*>(out);
+    scale ? go(cache_gather_kernel<float, true>, to) : go(cache_gather_kernel<float, false>, to);
+  } else {
+    uint16_t* to = static_cast<uint16_t*>(out);
+    scale ? go(cache_gather_kernel<uint16_t, true>, to) : go(cache_gather_kernel<uint16_t, false>, to);
+  }
   return cudaGetLastError();
 }
 

@@ -1,0 +1,276 @@
+// mla_cache_scaled.cu -- writing new latent rows to a cache with a scale for each block of positions.
+//
+// Rows are normalised and rotated as in cache_append_rope_kernel; the scale that a block needs is
+// s = 2^ceil(log2(max |y| / 448)) over its new rows, at least the one it has while it holds earlier
+// positions. A power of two costs e4m3, a floating format, nothing in precision, needs no division,
+// and a block whose scale grows has its earlier codes moved by whole exponents, exactly (subnormals
+// round): rows written one a step end up as if written once.
+//
+// A unit of work is a block of one sequence that new positions fall into. Sequence b's units begin
+// at cu_rows[b] / G + 2 b: m rows touch at most m / G + 2 blocks of G, so no unit needs to know how
+// many blocks the sequences before it touch, at the price of a few units that find nothing (G = 1:
+// a unit a row, none wasted). Four rows a warp (fewer where G is smaller), held in registers from the
+// loads to the codes; the warps of a unit exchange their largest entries through shared memory.
+// Bound: HBM for many rows (1,152 bytes read and 576 written a row), the chain of dependent loads
+// (cu_rows, length, page and row) for few.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "mla_internal.cuh"
+#include "mla_rope.cuh"
+
+namespace mla {
+namespace {
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | e4m3x2(c, d) << 16;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// four codes times a factor, rounded again
+__device__ __forceinline__ uint32_t rescaled(uint32_t four, float by) {
+  const float2 a = from_e4m3x2(four & 0xFFFFu), b = from_e4m3x2(four >> 16);
+  return e4m3x4(a.x * by, a.y * by, b.x * by, b.y * by);
+}
+
+// The smallest power of two in [2^-60, 2^60] that brings `top` (finite, not negative) to 448 =
+// 1.75 * 2^8 or less (2^60 where none does).
+__device__ __forceinline__ float scale_for(float top) {
+  const int bits = __float_as_int(top);
+  const int e = (bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0);
+  return __int_as_float((127 + max(-60, min(60, e))) << 23);
+}
+
+template <int G>
+struct ScaledCfg {
+  static constexpr int kRows = G < 4 ? G : 4;             // rows a warp
+  static constexpr int kUnitWarps = G / kRows;            // warps a unit
+  static constexpr int kWarps = kUnitWarps > 8 ? kUnitWarps : 8;  // warps a CTA
+  static constexpr int kUnits = kWarps / kUnitWarps;      // units a CTA
+};
+
+template <int G>
+__host__ __device__ __forceinline__ int64_t first_unit_of(int64_t row, int64_t b) {
+  return G == 1 ? row : row / G + 2 * b;
+}
+
+template <int G>
+__global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
+    cache_append_scaled_kernel(const __grid_constant__ AppendScaledArgs a,
+                               const __grid_constant__ mla_rope_t rope) {
+  using C = ScaledCfg<G>;
+  __shared__ uint64_t s_turns[MLA_ROPE / 2];
+  __shared__ unsigned s_top[C::kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = warp % C::kUnitWarps;  // this warp's place in its unit
+  const int64_t unit = (int64_t)blockIdx.x * C::kUnits + warp / C::kUnitWarps;
+  // the frequencies from the parameters, where lanes' different addresses are read one after another
+  if (warp == 0) s_turns[lane] = rope.turns[lane];
+  // (sequences whose rows all lie behind x's have no unit that could say so)
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.status && a.cu_rows[a.B] > a.n)
+    atomicCAS(a.status, 0u, (unsigned)MLA_ERR_BOUNDS);
+
+  // the last sequence whose units begin at or before this one: 32 candidates a round
+  int64_t lo = 0, len = a.B;
+  bool found = true;
+  while (true) {
+    const int64_t step = (len + 31) / 32;
+    const int64_t b = lo + lane * step;
+    const bool at = b < lo + len && first_unit_of<G>(a.cu_rows[b], b) <= unit;
+    const int hits = __popc(__ballot_sync(0xffffffffu, at));
+    if (hits == 0) {  // (rows before the first sequence)
+      found = false;
+      break;
+    }
+    lo += (hits - 1) * step;
+    len = min(step, len - (hits - 1) * step);
+    if (step == 1) break;
+  }
+  const int64_t b = lo;
+  const int64_t row0 = a.cu_rows[b], row1 = a.cu_rows[b + 1];
+  const int L = a.kv.seq_lens[b];
+  const int64_t m = row1 - row0;
+  // (the unit's place among its sequence's, and its block's first position)
+  const int64_t nth = unit - first_unit_of<G>(row0, b);
+  const int64_t p0 = L - m;
+  bool write = found && m > 0;
+  if (write && (p0 < 0 || row0 < 0 || row1 > a.n || L > a.kv.page_table_stride * a.kv.page_size)) {
+    if (lane == 0 && a.status) atomicCAS(a.status, 0u, (unsigned)MLA_ERR_BOUNDS);
+    write = false;
+  }
+  const int64_t start = write ? (p0 / G + nth) * G : 0;
+  write = write && start < L;
+  const int begin = write ? (int)start : 0;
+  const int first = write ? max((int)p0 - begin, 0) : G;  // places below hold earlier positions
+  const int end = write ? min(L - begin, G) : 0;          // and from here on none yet
+  // every row of this warp's at once
+  uint4 v0[C::kRows], v1[C::kRows];
+  uint32_t pair[C::kRows];  // this lane's RoPE pair, the first entry in the low half
+  int64_t position[C::kRows];
+#pragma unroll
+  for (int k = 0; k < C::kRows; ++k) {
+    const int place = part * C::kRows + k;
+    v0[k] = v1[k] = make_uint4(0, 0, 0, 0);
+    pair[k] = 0;
+    position[k] = 0;
+    if (place >= first && place < end) {
+      const int64_t i = row0 + (begin + place - p0);
+      const uint16_t* row = a.x + i * a.x_stride;
+      const uint4* src = reinterpret_cast<const uint4*>(row) + 2 * lane;
+      v0[k] = src[0], v1[k] = src[1];
+      if (rope.interleaved)
+        pair[k] = *reinterpret_cast<const uint32_t*>(row + kDV + 2 * lane);
+      else
+        pair[k] = row[kDV + lane] | (uint32_t)row[kDV + MLA_ROPE / 2 + lane] << 16;
+      if (a.positions) position[k] = a.positions[a.axes.of(lane) * a.n + i];
+    }
+  }
+  int64_t pool_row = 0;
+  float old = 0.f;
+  if (write) {
+    const int64_t page = a.kv.page_table[b * a.kv.page_table_stride + (unsigned)begin / (unsigned)a.kv.page_size];
+    write = page >= 0 && page < a.kv.num_pages;
+    if (write) {
+      pool_row = page * a.kv.page_size + (unsigned)begin % (unsigned)a.kv.page_size;
+      if (first > 0) old = a.scale[pool_row / G];
+    } else if (lane == 0 && part == 0 && a.status) {
+      atomicCAS(a.status, 0u, (unsigned)MLA_ERR_BOUNDS);
+    }
+  }
+  uint32_t g[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (a.weight) {
+    const uint4* wp = reinterpret_cast<const uint4*>(a.weight) + 2 * lane;
+    const uint4 g0 = __ldg(wp), g1 = __ldg(wp + 1);
+    g[0] = g0.x, g[1] = g0.y, g[2] = g0.z, g[3] = g0.w;
+    g[4] = g1.x, g[5] = g1.y, g[6] = g1.z, g[7] = g1.w;
+  }
+  __syncthreads();  // (the frequencies)
+  float norm[C::kRows];
+  float2 pe[C::kRows];
+  // entry e of the row's 16 latent entries, normalised (twice the same value: once for the
+  // largest, once for its code)
+  auto latent = [&](int k, int e) {
+    const uint32_t w[8] = {v0[k].x, v0[k].y, v0[k].z, v0[k].w, v1[k].x, v1[k].y, v1[k].z, v1[k].w};
+    const uint32_t two = w[e >> 1], gain = g[e >> 1];
+    float c = __uint_as_float(e & 1 ? two & 0xFFFF0000u : two << 16);
+    if (a.weight) c = c * norm[k] * __uint_as_float(e & 1 ? gain & 0xFFFF0000u : gain << 16);
+    return c;
+  };
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < C::kRows; ++k) {
+    norm[k] = 1.f;
+    if (a.weight) {
+      const uint32_t w[8] = {v0[k].x, v0[k].y, v0[k].z, v0[k].w, v1[k].x, v1[k].y, v1[k].z, v1[k].w};
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float c0 = __uint_as_float(w[e] << 16), c1 = __uint_as_float(w[e] & 0xFFFF0000u);
+        ss = fmaf(c0, c0, ss);
+        ss = fmaf(c1, c1, ss);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      norm[k] = rsqrtf(ss * (1.0f / kDV) + a.eps);
+    }
+    pe[k] = make_float2(__uint_as_float(pair[k] << 16), __uint_as_float(pair[k] & 0xFFFF0000u));
+    if (a.positions)
+      pe[k] = rope_turn(pe[k].x, pe[k].y, rope_cos_sin(s_turns[lane], position[k], rope.amplitude));
+    // (fmaxf passes over NaN)
+    top = fmaxf(top, fmaxf(fabsf(pe[k].x), fabsf(pe[k].y)));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(latent(k, e)));
+  }
+  if (top == INFINITY) {  // rare: the largest of the finite entries
+    auto finite = [](float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.f; };
+    top = 0.f;
+#pragma unroll
+    for (int k = 0; k < C::kRows; ++k) {
+      top = fmaxf(top, fmaxf(finite(pe[k].x), finite(pe[k].y)));
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, finite(latent(k, e)));
+    }
+  }
+  // (bits of floats that are not negative order as they do)
+  unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  if constexpr (C::kUnitWarps > 1) {
+    if (lane == 0) s_top[warp] = most;
+    __syncthreads();
+    most = s_top[warp - part];
+#pragma unroll
+    for (int w = 1; w < C::kUnitWarps; ++w) most = max(most, s_top[warp - part + w]);
+  }
+  // (every warp of the unit has its `old` by now: it was read before the barrier, and the scale
+  // is written after it)
+  if (!write) return;
+  float scale = scale_for(__uint_as_float(most));
+  const bool was = is_scale(old);
+  if (first > 0 && was) scale = fmaxf(scale, old);
+  if (part == 0 && lane == 0) a.scale[pool_row / G] = scale;
+  const float inv = 1.0f / scale;
+  uint8_t* dst0 = const_cast<uint8_t*>(a.kv.pool) + pool_row * kD;
+#pragma unroll
+  for (int k = 0; k < C::kRows; ++k) {
+    const int place = part * C::kRows + k;
+    uint8_t* dst = dst0 + place * kD;
+    if (place < first) {
+      if (scale != old) {  // earlier positions move to the block's new scale
+        const float by = was ? old / scale : __int_as_float(0x7FC00000);
+        uint4 c = reinterpret_cast<const uint4*>(dst)[lane];
+        const uint32_t t = *reinterpret_cast<const uint16_t*>(dst + kDV + 2 * lane);
+        c = make_uint4(rescaled(c.x, by), rescaled(c.y, by), rescaled(c.z, by), rescaled(c.w, by));
+        const float2 tail = from_e4m3x2(t);
+        reinterpret_cast<uint4*>(dst)[lane] = c;
+        *reinterpret_cast<uint16_t*>(dst + kDV + 2 * lane) = (uint16_t)e4m3x2(tail.x * by, tail.y * by);
+      }
+    } else if (place < end) {
+      uint32_t code[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        code[e] = e4m3x4(latent(k, 4 * e) * inv, latent(k, 4 * e + 1) * inv, latent(k, 4 * e + 2) * inv,
+                         latent(k, 4 * e + 3) * inv);
+      reinterpret_cast<uint4*>(dst)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
+      uint32_t pc = e4m3x2(pe[k].x * inv, pe[k].y * inv);
+      if (!rope.interleaved) {
+        // dims 2 l, 2 l + 1 of the row: first entries of two pairs (lanes below 16) or second ones
+        const uint32_t q0 = __shfl_sync(0xffffffffu, pc, (2 * lane) & 31);
+        const uint32_t q1 = __shfl_sync(0xffffffffu, pc, (2 * lane + 1) & 31);
+        pc = lane < 16 ? (q0 & 0xFFu) | (q1 & 0xFFu) << 8 : (q0 >> 8) | (q1 & 0xFF00u);
+      }
+      *reinterpret_cast<uint16_t*>(dst + kDV + 2 * lane) = (uint16_t)pc;
+    }
+  }
+}
+
+template <int G>
+cudaError_t launch_block(const AppendScaledArgs& a, const mla_rope_t& rope, cudaStream_t s) {
+  using C = ScaledCfg<G>;
+  const int64_t units = first_unit_of<G>(a.n, a.B);
+  const int64_t grid = (units + C::kUnits - 1) / C::kUnits;
+  cache_append_scaled_kernel<G><<<(unsigned)grid, 32 * C::kWarps, 0, s>>>(a, rope);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append_scaled(const AppendScaledArgs& a, const mla_rope_t& rope, int block,
+                                       cudaStream_t s) {
+  switch (block) {
+    case 1: return launch_block<1>(a, rope, s);
+    case 2: return launch_block<2>(a, rope, s);
+    case 4: return launch_block<4>(a, rope, s);
+    case 8: return launch_block<8>(a, rope, s);
+    case 16: return launch_block<16>(a, rope, s);
+    case 32: return launch_block<32>(a, rope, s);
+    case 64: return launch_block<64>(a, rope, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace mla

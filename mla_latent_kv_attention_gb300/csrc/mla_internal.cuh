@@ -281,9 +281,34 @@ struct AppendRopeArgs {
 };
 cudaError_t launch_cache_append_rope(const AppendRopeArgs& a, const mla_rope_t& rope, const PairAxes* axes,
                                      int num_sms, cudaStream_t s);
-cudaError_t launch_cache_gather(const mla_kv_t& kv, int B, const int32_t* starts,
-                                const int64_t* cu_rows, int64_t n, void* out, int out_f32,
-                                unsigned* status, cudaStream_t s);
+// scales: null, or the blocks' scales in the place of kv.kv_scale
+cudaError_t launch_cache_gather(const mla_kv_t& kv, const mla_scales_t* scales, int B,
+                                const int32_t* starts, const int64_t* cu_rows, int64_t n, void* out,
+                                int out_f32, unsigned* status, cudaStream_t s);
+// Block scales: a block's positions are row >> shift of the pool. What counts as a scale:
+constexpr float kMinScale = 0x1p-60f, kMaxScale = 0x1p60f;
+__host__ __device__ __forceinline__ bool is_scale(float s) { return s >= kMinScale && s <= kMaxScale; }
+inline int block_shift(int block) {
+  int shift = 0;
+  while ((1 << shift) < block) ++shift;
+  return shift;
+}
+struct AppendScaledArgs {
+  mla_kv_t kv;
+  float* scale;
+  const uint16_t* x;       // [n] rows of 576 bf16, x_stride elements apart
+  int64_t x_stride;
+  const int64_t* cu_rows;  // [B + 1]
+  int B;
+  int64_t n;
+  const uint16_t* weight;  // [512] bf16, or null: the latent is not normalised
+  float eps;
+  PairAxes axes;             // (all zero: one axis)
+  const int64_t* positions;  // [axes][n], or null: no rotation
+  unsigned* status;          // or null
+};
+cudaError_t launch_cache_append_scaled(const AppendScaledArgs& a, const mla_rope_t& rope, int block,
+                                       cudaStream_t s);
 struct AcceptArgs {
   const float* target;     // [B][n][V]
   const int32_t* tokens;   // [B][n]
