@@ -474,6 +474,39 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
                              size_t workspace_bytes, void* stream);
 
 /*
+ * Attention over a cache with a scale for each block of positions (mla_scales_t): keys and values are
+ * e4m3(code) * the scale of their block, kv->kv_scale is not read, and all else is as in the calls
+ * named. A row that sees a position whose scale is none is NaN, its lse too; a position that a
+ * mask hides, or past its sequence, may have any. Weights times scale below 2^-28 of a row's largest
+ * such product are not kept in the output (as weights are in the calls without scales).
+ * mla_verify_scaled: out is float32 [B][n_q][H][512] where out_is_f32 != 0, else bfloat16;
+ * visible_shift as in mla_verify_f32_shard.
+ */
+mla_status_t mla_decode_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int B,
+                               int H, float sm_scale, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+mla_status_t mla_verify_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int B,
+                               int n_q, int H, float sm_scale, int visible_shift, void* out,
+                               int out_is_f32, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream);
+mla_status_t mla_verify_tree_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int B,
+                                    int n, int H, float sm_scale, const uint64_t* tree_mask, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+mla_status_t mla_prefill_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int T,
+                                int H, float sm_scale, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * mla_prefill_mha (bf16 = 0) or mla_prefill_mha_bf16 (bf16 != 0) over such a cache. The cached values
+ * enter the up-projection as bfloat16: code * scale, exact where the scale is a power of two (as
+ * mla_cache_append_scaled writes them), else rounded once more, with an error like the bf16 form's.
+ * A position whose scale is none counts as a row of NaN codes does there.
+ */
+mla_status_t mla_prefill_mha_scaled(const mla_kv_t* kv, const mla_scales_t* scales, int L, const void* q,
+                                    int T, int H, const void* w_ukv, float sm_scale, int bf16, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Accept drafted tokens against the target's probabilities with given random numbers, and
  * draw the token after them: the emitted tokens are distributed as the target's own.
  * A sequence's n nodes are the positions of its verify call: node 0 is the last token already

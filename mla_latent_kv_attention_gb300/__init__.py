@@ -43,7 +43,8 @@ EXPORTS = ("mla_workspace_size", "mla_decode", "mla_verify", "mla_prefill", "mla
            "mla_prefill_mha_bf16", "mla_rope_init", "mla_rope", "mla_cache_append_rope",
            "mla_cache_gather", "mla_verify_tree", "mla_accept_drafts", "mla_rope_axes_init",
            "mla_rope_axes", "mla_cache_append_rope_axes", "mla_cache_append_scaled",
-           "mla_cache_gather_scaled")
+           "mla_cache_gather_scaled", "mla_decode_scaled", "mla_verify_scaled",
+           "mla_verify_tree_scaled", "mla_prefill_scaled", "mla_prefill_mha_scaled")
 
 
 _BLOCKS = (1, 2, 4, 8, 16, 32, 64)
@@ -137,9 +138,16 @@ def _load() -> ctypes.CDLL:
     SCALES = ctypes.POINTER(mla_scales_t)
     lib.mla_cache_append_scaled.argtypes = [KV, SCALES, P, i64, P, i32, i64, P, f32, ROPE, AXES, P, P, P]
     lib.mla_cache_gather_scaled.argtypes = [KV, SCALES, i32, P, P, i64, P, i32, P, P]
+    lib.mla_decode_scaled.argtypes = [KV, SCALES, P, i32, i32, f32, P, P, P, sz, P]
+    lib.mla_verify_scaled.argtypes = [KV, SCALES, P, i32, i32, i32, f32, i32, P, i32, P, P, sz, P]
+    lib.mla_verify_tree_scaled.argtypes = [KV, SCALES, P, i32, i32, i32, f32, P, P, P, P, sz, P]
+    lib.mla_prefill_scaled.argtypes = [KV, SCALES, P, i32, i32, f32, P, P, P, sz, P]
+    lib.mla_prefill_mha_scaled.argtypes = [KV, SCALES, i32, P, i32, i32, P, f32, i32, P, P, P, sz, P]
     for name in ("mla_rope_init", "mla_rope", "mla_cache_append_rope", "mla_cache_gather",
                  "mla_verify_tree", "mla_accept_drafts", "mla_rope_axes_init", "mla_rope_axes",
-                 "mla_cache_append_rope_axes", "mla_cache_append_scaled", "mla_cache_gather_scaled"):
+                 "mla_cache_append_rope_axes", "mla_cache_append_scaled", "mla_cache_gather_scaled",
+                 "mla_decode_scaled", "mla_verify_scaled", "mla_verify_tree_scaled", "mla_prefill_scaled",
+                 "mla_prefill_mha_scaled"):
         getattr(lib, name).restype = i32
     for name in ("mla_decode", "mla_verify", "mla_prefill", "mla_merge_lse", "mla_read_status",
                  "mla_last_launch_count"):
@@ -163,7 +171,8 @@ class KVCache:
     """Device-resident paged latent cache (see ``mla_kv_t`` in include/mla.h).
     pool uint8 [num_pages, page_size, 576]; page_table int32 [B, stride]; seq_lens int32 [B].
     A cache with a scale for each block of positions (``mla_scales_t``) has ``scales`` float32
-    [num_pages, page_size / block], block 1, 2, 4, .. 64, in the place of kv_scale, which is then 1."""
+    [num_pages, page_size / block], block 1, 2, 4, .. 64, in the place of kv_scale, which is then 1;
+    every call that takes a KVCache reads it under them."""
 
     pool: torch.Tensor
     page_table: torch.Tensor
@@ -258,10 +267,12 @@ def mla_decode(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None
     out = torch.empty(B, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(B, H, dtype=torch.float32, device=q.device) if lse is None else lse
     ws = workspace(MLA_OP_DECODE, B, H, 1, q.device) if ws is None else ws
-    c = kv.c_struct()
-    _check("mla_decode", library().mla_decode(ctypes.byref(c), q.data_ptr(), B, H, sm_scale,
-                                         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
-                                         _stream(stream)))
+    c, scales = kv.c_struct(), kv.c_scales()
+    args = (q.data_ptr(), B, H, sm_scale, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream))
+    if scales is None:
+        _check("mla_decode", library().mla_decode(c, *args))
+    else:
+        _check("mla_decode_scaled", library().mla_decode_scaled(c, scales, *args))
     return out, lse
 
 
@@ -276,10 +287,15 @@ def mla_verify(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None
     out = torch.empty(B, n_q, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(B, n_q, H, dtype=torch.float32, device=q.device) if lse is None else lse
     ws = workspace(MLA_OP_VERIFY, B, H, n_q, q.device) if ws is None else ws
-    c = kv.c_struct()
-    _check("mla_verify", library().mla_verify(ctypes.byref(c), q.data_ptr(), B, n_q, H, sm_scale,
-                                         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
-                                         _stream(stream)))
+    c, scales = kv.c_struct(), kv.c_scales()
+    if scales is None:
+        _check("mla_verify", library().mla_verify(ctypes.byref(c), q.data_ptr(), B, n_q, H, sm_scale,
+                                             out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
+                                             _stream(stream)))
+    else:
+        _check("mla_verify_scaled", library().mla_verify_scaled(
+            c, scales, q.data_ptr(), B, n_q, H, sm_scale, 0, out.data_ptr(), 0, _ptr(lse), ws.data_ptr(),
+            ws.numel(), _stream(stream)))
     return out, lse
 
 
@@ -307,11 +323,14 @@ def mla_prefill_mha(kv: KVCache, q: torch.Tensor, w_ukv: torch.Tensor, sm_scale:
         if n == 0:
             raise ValueError("no workspace size for these arguments")
         ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
-    c = kv.c_struct()
+    c, scales = kv.c_struct(), kv.c_scales()
     name = "mla_prefill_mha_bf16" if bf16 else "mla_prefill_mha"
-    _check(name, getattr(library(), name)(
-        ctypes.byref(c), L, q.data_ptr(), T, H, w_ukv.data_ptr(), sm_scale, out.data_ptr(),
-        _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream)))
+    tail = (out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream))
+    if scales is None:
+        _check(name, getattr(library(), name)(c, L, q.data_ptr(), T, H, w_ukv.data_ptr(), sm_scale, *tail))
+    else:
+        _check("mla_prefill_mha_scaled", library().mla_prefill_mha_scaled(
+            c, scales, L, q.data_ptr(), T, H, w_ukv.data_ptr(), sm_scale, int(bf16), *tail))
     return out, lse
 
 
@@ -330,8 +349,12 @@ def mla_verify_f32(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=
         raise ValueError("out must be a contiguous float32 tensor [B, n_q, H, 512]")
     lse = torch.empty(B, n_q, H, dtype=torch.float32, device=q.device) if lse is None else lse
     ws = workspace(MLA_OP_VERIFY, B, H, n_q, q.device) if ws is None else ws
-    c = kv.c_struct()
-    if visible_shift == 0:
+    c, scales = kv.c_struct(), kv.c_scales()
+    if scales is not None:
+        _check("mla_verify_scaled", library().mla_verify_scaled(
+            c, scales, q.data_ptr(), B, n_q, H, sm_scale, int(visible_shift), out.data_ptr(), 1, _ptr(lse),
+            ws.data_ptr(), ws.numel(), _stream(stream)))
+    elif visible_shift == 0:
         _check("mla_verify_f32", library().mla_verify_f32(
             ctypes.byref(c), q.data_ptr(), B, n_q, H, sm_scale, out.data_ptr(), _ptr(lse),
             ws.data_ptr(), ws.numel(), _stream(stream)))
@@ -353,10 +376,12 @@ def mla_prefill(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=Non
     out = torch.empty(T, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(T, H, dtype=torch.float32, device=q.device) if lse is None else lse
     ws = workspace(MLA_OP_PREFILL, 1, H, T, q.device) if ws is None else ws
-    c = kv.c_struct()
-    _check("mla_prefill", library().mla_prefill(ctypes.byref(c), q.data_ptr(), T, H, sm_scale,
-                                           out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
-                                           _stream(stream)))
+    c, scales = kv.c_struct(), kv.c_scales()
+    args = (q.data_ptr(), T, H, sm_scale, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream))
+    if scales is None:
+        _check("mla_prefill", library().mla_prefill(c, *args))
+    else:
+        _check("mla_prefill_scaled", library().mla_prefill_scaled(c, scales, *args))
     return out, lse
 
 
@@ -645,10 +670,13 @@ def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_sc
         raise ValueError("ws must be a contiguous uint8 tensor on q's device")
     if kv.seq_lens.shape[0] < B or kv.page_table.shape[0] < B or kv.pool.device != dev:
         raise ValueError("kv must describe q's sequences, on q's device")
-    _check("mla_verify_tree", library().mla_verify_tree(
-        kv.c_struct(), q.data_ptr(), B, n, H, sm_scale,
-        _dense(tree_mask, "tree_mask", _I64, (B, n), dev), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-        ws.numel(), _on(dev)))
+    c, scales = kv.c_struct(), kv.c_scales()
+    args = (q.data_ptr(), B, n, H, sm_scale, _dense(tree_mask, "tree_mask", _I64, (B, n), dev), out.data_ptr(),
+            lse.data_ptr(), ws.data_ptr(), ws.numel(), _on(dev))
+    if scales is None:
+        _check("mla_verify_tree", library().mla_verify_tree(c, *args))
+    else:
+        _check("mla_verify_tree_scaled", library().mla_verify_tree_scaled(c, scales, *args))
     return out, lse
 
 

@@ -93,9 +93,17 @@ bool pair_axes(const mla_rope_axes_t* axes, mla::PairAxes* out) {
 // this thread.
 thread_local int g_test_stall = 0;
 
+// Block scales in the place of the cache's one (scales NULL: as base_params left it).
+void use_scales(mla::AttnParams* p, const mla_scales_t* scales) {
+  if (!scales) return;
+  p->kv_scale = 1.f;
+  p->scales = scales->scale;
+  p->scale_shift = mla::block_shift(scales->block);
+}
+
 mla_status_t run_split(const mla_kv_t* kv, const void* q, int B, int n_q, int H, float sm_scale,
                        void* out, float* lse, void* ws, size_t ws_bytes, void* stream,
-                       bool out_is_f32 = false, int mask_shift = 0) {
+                       bool out_is_f32 = false, int mask_shift = 0, const mla_scales_t* scales = nullptr) {
   g_last_launches = 0;
   mla_status_t st = check_kv(kv);
   if (st != MLA_OK) return st;
@@ -112,6 +120,7 @@ mla_status_t run_split(const mla_kv_t* kv, const void* q, int B, int n_q, int H,
   if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
   if (B == 0) return MLA_OK;
   mla::AttnParams p = base_params(kv, q, B, n_q, H, sm_scale, out, lse);
+  use_scales(&p, scales);
   p.test_stall = g_test_stall;
   g_test_stall = 0;
   p.mask_shift = mask_shift;
@@ -194,9 +203,11 @@ mla_status_t mla_verify_f32_shard(const mla_kv_t* kv, const void* q, int B, int 
                    shift);
 }
 
-mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, int H, float sm_scale,
-                             const uint64_t* tree_mask, void* out, float* lse, void* workspace,
-                             size_t workspace_bytes, void* stream) {
+namespace {
+
+mla_status_t run_tree(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int B, int n, int H,
+                      float sm_scale, const uint64_t* tree_mask, void* out, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream) {
   g_last_launches = 0;
   mla_status_t st = check_kv(kv);
   if (st != MLA_OK) return st;
@@ -218,6 +229,7 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE;
   if (B == 0) return MLA_OK;
   mla::AttnParams p = base_params(kv, q, B, n, H, sm_scale, out, lse);
+  use_scales(&p, scales);
   p.B = B * g.passes;
   p.R = p.part_rows = g.nodes * H;
   p.group_nodes = g.nodes;
@@ -255,6 +267,45 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
   return MLA_OK;
 }
 
+}  // namespace
+
+mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, int H, float sm_scale,
+                             const uint64_t* tree_mask, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return run_tree(kv, nullptr, q, B, n, H, sm_scale, tree_mask, out, lse, workspace, workspace_bytes, stream);
+}
+
+mla_status_t mla_decode_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int B,
+                               int H, float sm_scale, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  g_last_launches = 0;
+  const mla_status_t st = check_scales(scales);
+  if (st != MLA_OK) return st;
+  return run_split(kv, q, B, 1, H, sm_scale, out, lse, workspace, workspace_bytes, stream, false, 0, scales);
+}
+
+mla_status_t mla_verify_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int B,
+                               int n_q, int H, float sm_scale, int visible_shift, void* out,
+                               int out_is_f32, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  g_last_launches = 0;
+  const mla_status_t st = check_scales(scales);
+  if (st != MLA_OK) return st;
+  if (visible_shift < 0) return MLA_ERR_INVALID_ARG;
+  const int shift = (n_q >= 1 && visible_shift > n_q - 1) ? n_q - 1 : visible_shift;
+  return run_split(kv, q, B, n_q, H, sm_scale, out, lse, workspace, workspace_bytes, stream, out_is_f32 != 0,
+                   shift, scales);
+}
+
+mla_status_t mla_verify_tree_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int B,
+                                    int n, int H, float sm_scale, const uint64_t* tree_mask, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_launches = 0;
+  const mla_status_t st = check_scales(scales);
+  if (st != MLA_OK) return st;
+  return run_tree(kv, scales, q, B, n, H, sm_scale, tree_mask, out, lse, workspace, workspace_bytes, stream);
+}
+
 size_t mla_prefill_mha_workspace_size(int L, int H, int device) {
   if (L < 0 || H < 1 || H > MLA_MAX_HEADS) return 0;
   const int sms = sm_count(device);
@@ -266,7 +317,8 @@ namespace {
 
 mla_status_t run_mha(const mla_kv_t* kv, int L, const void* q, int T, int H, const void* w_ukv,
                      float sm_scale, void* out, float* lse, void* workspace,
-                     size_t workspace_bytes, void* stream, int precise) {
+                     size_t workspace_bytes, void* stream, int precise,
+                     const mla_scales_t* scales = nullptr) {
   g_last_launches = 0;
   mla_status_t st = check_kv(kv);
   if (st != MLA_OK) return st;
@@ -291,7 +343,9 @@ mla_status_t run_mha(const mla_kv_t* kv, int L, const void* q, int T, int H, con
   a.num_pages = kv->num_pages;
   a.page_size = kv->page_size;
   a.page_table = kv->page_table;
-  a.kv_scale = kv->kv_scale;
+  a.kv_scale = scales ? 1.f : kv->kv_scale;
+  a.scales = scales ? scales->scale : nullptr;
+  a.scale_shift = scales ? mla::block_shift(scales->block) : 0;
   a.L = L;
   a.T = T;
   a.H = H;
@@ -336,8 +390,20 @@ mla_status_t mla_prefill_mha_bf16(const mla_kv_t* kv, int L, const void* q, int 
   return run_mha(kv, L, q, T, H, w_ukv, sm_scale, out, lse, workspace, workspace_bytes, stream, 0);
 }
 
-mla_status_t mla_prefill(const mla_kv_t* kv, const void* q, int T, int H, float sm_scale,
-                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+mla_status_t mla_prefill_mha_scaled(const mla_kv_t* kv, const mla_scales_t* scales, int L, const void* q,
+                                    int T, int H, const void* w_ukv, float sm_scale, int bf16, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_launches = 0;
+  const mla_status_t st = check_scales(scales);
+  if (st != MLA_OK) return st;
+  return run_mha(kv, L, q, T, H, w_ukv, sm_scale, out, lse, workspace, workspace_bytes, stream, bf16 == 0,
+                 scales);
+}
+
+namespace {
+
+mla_status_t run_prefill(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int T, int H,
+                         float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
                          void* stream) {
   g_last_launches = 0;
   mla_status_t st = check_kv(kv);
@@ -355,6 +421,7 @@ mla_status_t mla_prefill(const mla_kv_t* kv, const void* q, int T, int H, float 
   if (sms <= 0) return MLA_ERR_CUDA;
   if (workspace_bytes < mla::ws_prefill_bytes(sms)) return MLA_ERR_WORKSPACE;
   mla::AttnParams p = base_params(kv, q, 1, T, H, sm_scale, out, lse);
+  use_scales(&p, scales);
   char* base = static_cast<char*>(workspace);
   p.hdr = reinterpret_cast<mla::WsHeader*>(base);
   p.status = reinterpret_cast<unsigned*>(base + mla::ws_prefill_status(sms));
@@ -375,6 +442,23 @@ mla_status_t mla_prefill(const mla_kv_t* kv, const void* q, int T, int H, float 
   }
   prof_mark(g_prof_stop, s);
   return MLA_OK;
+}
+
+}  // namespace
+
+mla_status_t mla_prefill(const mla_kv_t* kv, const void* q, int T, int H, float sm_scale,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  return run_prefill(kv, nullptr, q, T, H, sm_scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+mla_status_t mla_prefill_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int T,
+                                int H, float sm_scale, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  g_last_launches = 0;
+  const mla_status_t st = check_scales(scales);
+  if (st != MLA_OK) return st;
+  return run_prefill(kv, scales, q, T, H, sm_scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 mla_status_t mla_merge_lse(const float* part_out, const float* part_lse, int S, int64_t R,

@@ -47,6 +47,14 @@
 // code smaller, which the tile loops and a call's start fetch through caches they overflow (81 KB;
 // verify's instantiation has 243). 32 x 32 nodes of 12 heads over 4K-16K keys: 270 us, 1.01
 // PFLOP/s, 0.53 of the measured bf16 rate.
+//
+// Block scales (SC): key n's codes count times s_n, its block's scale. A softmax thread owns a key, so
+// s_n is one number a thread and tile: with x_n the key's score in log2 units, its weight in the values
+// MMA is 2^(x_n + log2 s_n - m) (the MMA then adds s_n v_n in units of the codes), its share of the row
+// sum that weight over s_n, and m the running maximum of x_n + log2 s_n. That costs the tile loop one
+// multiply-add a score and nothing in memory traffic but the scales; a rounded log2 acts on numerator
+// and sum alike. The three e5m2 terms then keep their precision relative to the largest weight
+// times scale, which is what the output's absolute error is about.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -619,7 +627,67 @@ struct Issuer {
   }
 };
 
-template <int RP, int PF, bool TR>
+// A key's scale as the softmax uses it. A scale that is none gives NaN scores to the rows that see the
+// key (those that do not see it are masked after the scores, and their weight 0 meets finite numbers).
+struct KeyScale {
+  float scale, log2, inv;
+  __device__ __forceinline__ KeyScale() {}
+  __device__ __forceinline__ explicit KeyScale(float s) : scale(s), log2(0.f), inv(1.f) {
+    if (is_scale(s)) {
+      log2 = log2f(s);
+      inv = __frcp_rn(s);
+    } else {
+      scale = __int_as_float(0x7FC00000);
+    }
+  }
+};
+
+// One thread's walk over the scales of its keys, 128 positions a tile. Its keys are places of one
+// 64-key half of every tile, which lies in one page; the page's place in the table is counted along.
+struct BlockScales {
+  float next;       // the coming tile's scale (1 past the unit's keys)
+  int page;         // the pool page of the tile after it, or -1
+  int kk, lp, off;  // that tile's first key of this half: position, logical page, offset in it
+  int place;        // the key's place in the half
+  __device__ __forceinline__ void find(const AttnParams& p, int b, int key_hi) {
+    page = -1;
+    if (kk < key_hi) page = p.page_table[(int64_t)b * p.pt_stride + lp];
+  }
+  __device__ __forceinline__ void load(const AttnParams& p, int key_hi) {
+    next = 1.f;
+    if (page >= 0 && page < p.num_pages && kk + place < key_hi)
+      next = p.scales[((int64_t)page * p.page_size + off + place) >> p.scale_shift];
+  }
+  __device__ __forceinline__ void advance(const AttnParams& p) {
+    kk += kTileKeys;
+    off += kTileKeys;
+    while (off >= p.page_size) {
+      off -= p.page_size;
+      ++lp;
+    }
+  }
+  // half0: first position of this thread's half of the unit's first tile
+  __device__ __forceinline__ void begin(const AttnParams& p, int b, int half0, int at, int key_hi) {
+    kk = half0;
+    place = at;
+    lp = kk / p.page_size;
+    off = kk % p.page_size;
+    find(p, b, key_hi);
+    load(p, key_hi);
+    advance(p);
+    find(p, b, key_hi);
+  }
+  // this tile's scale; the next one's load goes out
+  __device__ __forceinline__ KeyScale take(const AttnParams& p, int b, int key_hi) {
+    const float s = next;
+    load(p, key_hi);
+    advance(p);
+    find(p, b, key_hi);
+    return KeyScale(s);
+  }
+};
+
+template <int RP, int PF, bool TR, bool SC>
 __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ DecodeArgs args,
                      const __grid_constant__ CUtensorMap map_main,
@@ -1140,6 +1208,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       }
       return true;
     };
+    // Block scales: the scale of this thread's key of the next tile and the pool page of the one
+    // after it are loaded while a tile is worked on.
+    BlockScales bs;
     uint64_t* wg_bar = &ms->wg_bar[wg];
     // Bounded warpgroup barrier: every warp arrives, then waits for the phase.
     auto wg_sync = [&]() -> bool {
@@ -1187,6 +1258,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       const int lim_cap = un.key_hi - 1;
       // (tree: the last key of the prefix, which every node sees; the nodes' own keys follow)
       const int lim0 = min(lim_cap, L - p.n_q + (PF == 3 ? -1 : un.j0 + p.mask_shift));
+      if constexpr (SC) bs.begin(p, un.b, un.key_lo + (i & ~63), i & 63, un.key_hi);
       // this unit's row scales (staged with its query terms)
       ok &= warp_wait(&ms->q_full[k % C::kQB], (k / C::kQB) & 1);
       // mo: the row's running max less kPScale (p = 2^(x - mo)); kNoMax before its first key
@@ -1204,6 +1276,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         const int s = tile % kStages;
         const int k0 = un.key_lo + t * kTileKeys;
         const int kabs = k0 + i;
+        KeyScale ks;
+        if constexpr (SC) ks = bs.take(p, un.b, un.key_hi);
         ok &= warp_wait(&ms->s_full[sb], (tile / C::kSBuf) & 1);
         tc_fence_after();
         float x[RH];
@@ -1218,7 +1292,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           }
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < RH; ++e) x[e] = fmaf(b2[e], 1.0f / kQTerm2, a[e]) * rs[e];
+          for (int e = 0; e < RH; ++e) {
+            x[e] = fmaf(b2[e], 1.0f / kQTerm2, a[e]);
+            x[e] = SC ? fmaf(x[e] * ks.scale, rs[e], ks.log2) : x[e] * rs[e];
+          }
         }
         tc_fence_before();
         warp_arrive(&ms->s_empty[sb]);
@@ -1346,8 +1423,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         for (int r = 0; r < RH; r += 2) {
           const float p0 = ex2(x[r] - mo[r]);  // masked (x = -inf) and keyless rows give 0
           const float p1 = ex2(x[r + 1] - mo[r + 1]);
-          l[r] += p0;
-          l[r + 1] += p1;
+          l[r] = SC ? fmaf(p0, ks.inv, l[r]) : l[r] + p0;
+          l[r + 1] = SC ? fmaf(p1, ks.inv, l[r + 1]) : l[r + 1] + p1;
           const uint32_t h = f32x2_to_f16x2(p0, p1);
           const uint32_t c1 = f16x2_to_e5m2x2(h);
           const uint32_t r1 = hsub2(h, e5m2x2_to_f16x2(c1));
@@ -1707,11 +1784,11 @@ bool encode_pool_maps(const AttnParams& p, CUtensorMap* main_map, CUtensorMap* t
   return r1 == CUDA_SUCCESS && r2 == CUDA_SUCCESS;
 }
 
-template <int RP, int PF, bool TR>
+template <int RP, int PF, bool TR, bool SC>
 cudaError_t launch_rp_tr(const DecodeArgs& a, const CUtensorMap& mm, const CUtensorMap& mt,
                          int grid, cudaStream_t s) {
   constexpr int smem = smem_bytes<RP>();
-  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<RP, PF, TR>,
+  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<RP, PF, TR, SC>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1724,17 +1801,18 @@ cudaError_t launch_rp_tr(const DecodeArgs& a, const CUtensorMap& mm, const CUten
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tc_kernel<RP, PF, TR>, a, mm, mt);
+  return cudaLaunchKernelEx(&cfg, attn_tc_kernel<RP, PF, TR, SC>, a, mm, mt);
 }
 
 template <int RP, int PF>
 cudaError_t launch_rp(const DecodeArgs& a, const CUtensorMap& mm, const CUtensorMap& mt,
                       int grid, cudaStream_t s) {
+  if (a.p.scales) return launch_rp_tr<RP, PF, false, true>(a, mm, mt, grid, s);
   if constexpr (PF >= 2) {  // (never traced)
-    return launch_rp_tr<RP, PF, false>(a, mm, mt, grid, s);
+    return launch_rp_tr<RP, PF, false, false>(a, mm, mt, grid, s);
   } else {
-    return a.p.trace ? launch_rp_tr<RP, PF, true>(a, mm, mt, grid, s)
-                     : launch_rp_tr<RP, PF, false>(a, mm, mt, grid, s);
+    return a.p.trace ? launch_rp_tr<RP, PF, true, false>(a, mm, mt, grid, s)
+                     : launch_rp_tr<RP, PF, false, false>(a, mm, mt, grid, s);
   }
 }
 

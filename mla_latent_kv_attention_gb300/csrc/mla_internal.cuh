@@ -127,7 +127,9 @@ struct AttnParams {
   const int32_t* page_table;
   int64_t pt_stride;
   const int32_t* seq_lens;
-  float kv_scale;
+  float kv_scale;     // (1 where the blocks have scales)
+  const float* scales;  // one a block of 1 << scale_shift positions, or null
+  int scale_shift;
   float sm_scale;
   const uint16_t* q;  // [B][n_q][H][576]
   int B, n_q, H, R;   // R = n_q * H rows per sequence
@@ -226,7 +228,9 @@ struct MhaArgs {
   int64_t num_pages;
   int page_size;
   const int32_t* page_table;
-  float kv_scale;
+  float kv_scale;       // (1 where the blocks have scales)
+  const float* scales;  // one a block of 1 << scale_shift positions, or null
+  int scale_shift;
   int L, T, H;
   float sm_scale;
   const void* q;      // [T][H][192] bf16

@@ -603,7 +603,9 @@ __global__ void __launch_bounds__(256) mha_chunk_merge_kernel(const MhaParams p,
 // Cached rows -> latent [L][512] bf16 (the e4m3 values; exact) and RoPE rows [L][64] bf16
 // (e4m3 value x rope_scale: kv_scale, one rounding, for the bf16 form; 1, exact, for the
 // precise one). One thread per 8 codes of a row.
-__global__ void mha_dequant_kernel(const uint8_t* __restrict__ pool, int64_t num_pages,
+// SC: both times the scale of the row's block (exact for a power of two).
+template <bool SC>
+__global__ void mha_dequant_kernel(const float* __restrict__ scales, int scale_shift, const uint8_t* __restrict__ pool, int64_t num_pages,
                                    int page_size, const int32_t* __restrict__ page_table, int L,
                                    float rope_scale, __nv_bfloat16* __restrict__ latent,
                                    __nv_bfloat16* __restrict__ rope, unsigned* status) {
@@ -614,9 +616,14 @@ __global__ void mha_dequant_kernel(const uint8_t* __restrict__ pool, int64_t num
     const int c8 = (int)(it % (kD / 8));
     const int32_t page = page_table[n / page_size];
     uint2 raw = make_uint2(0u, 0u);
+    float scale = 1.f;
     if (page < 0 || page >= num_pages) {
       atomicCAS(status, 0u, (unsigned)MLA_ERR_BOUNDS);
     } else {
+      if constexpr (SC) {
+        scale = scales[((int64_t)page * page_size + n % page_size) >> scale_shift];
+        if (!is_scale(scale)) scale = __int_as_float(0x7FC00000);  // none: NaN for those who see it
+      }
       raw = *reinterpret_cast<const uint2*>(pool + ((int64_t)page * page_size + n % page_size) * kD +
                                             c8 * 8);
     }
@@ -627,8 +634,8 @@ __global__ void mha_dequant_kernel(const uint8_t* __restrict__ pool, int64_t num
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
           (__nv_fp8x2_storage_t)((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
       const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
+      f[2 * i] = SC ? x.x * scale : x.x;
+      f[2 * i + 1] = SC ? x.y * scale : x.y;
     }
     uint32_t o[4];
     if (c8 < kDV / 8) {
@@ -755,7 +762,8 @@ cudaError_t launch_mha_prefill(const MhaArgs& a, int num_sms, cudaStream_t s, in
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)a.L * (kD / 8);
   const int grid1 = (int)std::min<int64_t>((items + 255) / 256, (int64_t)num_sms * 8);
-  mha_dequant_kernel<<<grid1, 256, 0, s>>>(a.pool, a.num_pages, a.page_size, a.page_table, a.L,
+  auto* dequant = a.scales ? mha_dequant_kernel<true> : mha_dequant_kernel<false>;
+  dequant<<<grid1, 256, 0, s>>>(a.scales, a.scale_shift, a.pool, a.num_pages, a.page_size, a.page_table, a.L,
                                            a.precise ? 1.f : a.kv_scale,
                                            reinterpret_cast<__nv_bfloat16*>(a.latent),
                                            reinterpret_cast<__nv_bfloat16*>(a.rope), dq_status);

@@ -108,7 +108,7 @@ def shard_views(page_table: torch.Tensor, shard: Shard):
 
 def rank_views(kv: KVCache, shard: Shard):
     """The rank's attention calls as [(KVCache view, visible_shift)], on kv's device."""
-    return [(KVCache(kv.pool, pt, lens, kv.kv_scale), shift)
+    return [(KVCache(kv.pool, pt, lens, kv.kv_scale, kv.scales), shift)
             for pt, lens, shift in shard_views(kv.page_table, shard)]
 
 
