@@ -627,62 +627,65 @@ struct Issuer {
   }
 };
 
+#ifndef WI_RULE
+#define WI_RULE(RP, PF, SC) ((PF) == 3 || (SC))
+#endif
+constexpr bool whole_warps(int rp, int pf, bool sc) { return WI_RULE(rp, pf, sc); }
+
 // A key's scale as the softmax uses it. A scale that is none gives NaN scores to the rows that see the
 // key (those that do not see it are masked after the scores, and their weight 0 meets finite numbers).
+// The approximate log2 (2^-22) enters weight and row sum alike, the reciprocal (2^-23) the sum; both
+// are exact for powers of two.
 struct KeyScale {
   float scale, log2, inv;
   __device__ __forceinline__ KeyScale() {}
-  __device__ __forceinline__ explicit KeyScale(float s) : scale(s), log2(0.f), inv(1.f) {
-    if (is_scale(s)) {
-      log2 = log2f(s);
-      inv = __frcp_rn(s);
-    } else {
-      scale = __int_as_float(0x7FC00000);
-    }
+  __device__ __forceinline__ explicit KeyScale(float s) {
+    const bool good = is_scale(s);
+    scale = good ? s : __int_as_float(0x7FC00000);
+    const float t = good ? s : 1.f;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(log2) : "f"(t));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(t));
   }
 };
 
 // One thread's walk over the scales of its keys, 128 positions a tile. Its keys are places of one
 // 64-key half of every tile, which lies in one page; the page's place in the table is counted along.
+// (Pool rows fit 32 bits: encode_pool_maps refuses more.)
 struct BlockScales {
-  float next;       // the coming tile's scale (1 past the unit's keys)
-  int page;         // the pool page of the tile after it, or -1
-  int kk, lp, off;  // that tile's first key of this half: position, logical page, offset in it
-  int place;        // the key's place in the half
-  __device__ __forceinline__ void find(const AttnParams& p, int b, int key_hi) {
-    page = -1;
-    if (kk < key_hi) page = p.page_table[(int64_t)b * p.pt_stride + lp];
-  }
-  __device__ __forceinline__ void load(const AttnParams& p, int key_hi) {
+  const int32_t* table;  // the sequence's page-table entry of the half
+  float next;            // the coming tile's scale (1 past the unit's keys)
+  int page;              // the pool page of the tile after it, or -1
+  int kk, off;           // this thread's key in that tile: position, offset in its page
+  __device__ __forceinline__ void find(int key_hi) { page = kk < key_hi ? __ldg(table) : -1; }
+  __device__ __forceinline__ void load(const AttnParams& p) {
     next = 1.f;
-    if (page >= 0 && page < p.num_pages && kk + place < key_hi)
-      next = p.scales[((int64_t)page * p.page_size + off + place) >> p.scale_shift];
+    if ((unsigned)page < (unsigned)p.num_pages)
+      next = __ldg(p.scales + ((unsigned)(page * p.page_size + off) >> p.scale_shift));
   }
   __device__ __forceinline__ void advance(const AttnParams& p) {
     kk += kTileKeys;
     off += kTileKeys;
     while (off >= p.page_size) {
       off -= p.page_size;
-      ++lp;
+      ++table;
     }
   }
-  // half0: first position of this thread's half of the unit's first tile
-  __device__ __forceinline__ void begin(const AttnParams& p, int b, int half0, int at, int key_hi) {
-    kk = half0;
-    place = at;
-    lp = kk / p.page_size;
+  // key: this thread's in the unit's first tile
+  __device__ __forceinline__ void begin(const AttnParams& p, int b, int key, int key_hi) {
+    kk = key;
+    table = p.page_table + (int64_t)b * p.pt_stride + kk / p.page_size;
     off = kk % p.page_size;
-    find(p, b, key_hi);
-    load(p, key_hi);
+    find(key_hi);
+    load(p);
     advance(p);
-    find(p, b, key_hi);
+    find(key_hi);
   }
   // this tile's scale; the next one's load goes out
-  __device__ __forceinline__ KeyScale take(const AttnParams& p, int b, int key_hi) {
+  __device__ __forceinline__ KeyScale take(const AttnParams& p, int key_hi) {
     const float s = next;
-    load(p, key_hi);
+    load(p);
     advance(p);
-    find(p, b, key_hi);
+    find(key_hi);
     return KeyScale(s);
   }
 };
@@ -693,6 +696,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                      const __grid_constant__ CUtensorMap map_main,
                      const __grid_constant__ CUtensorMap map_tail) {
   using C = Cfg<RP>;
+  constexpr bool WI = whole_warps(RP, PF, SC);
+  constexpr int PT = WI ? 3 : PF;
   const AttnParams& p = args.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -700,7 +705,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   Misc* ms = reinterpret_cast<Misc*>(smem + C::kOffMisc);
   uint8_t* pbuf = smem + C::kOffP;
   uint8_t* qbuf = smem + C::kOffQ;
-  const int warp = PF == 3 ? __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0) : (int)threadIdx.x >> 5;
+  const int warp = WI ? __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0) : (int)threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // profiling hook: this CTA's stamps, or null
   // (TR: a separate instantiation for traced calls, so the usual one carries no stamp code)
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s)
-      for (int c = 0; c < num_parts(PF); ++c) {
+      for (int c = 0; c < num_parts(PT); ++c) {
         mbar_init(&ms->kv_full[s][c], 1);
         mbar_init(&ms->kv_free[s][c], 1);
       }
@@ -871,7 +876,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   // held it have released it.
   const int64_t rows64 = p.num_pages * (int64_t)p.page_size;
   const int total_rows = rows64 > 0x7fffff00 ? 0x7fffff00 : (int)rows64;
-  auto issue_tile = [&](const Issuer<PF == 3>& by, const UnitInfo& un, int k0, uint32_t fill,
+  auto issue_tile = [&](const Issuer<WI>& by, const UnitInfo& un, int k0, uint32_t fill,
                         uint64_t policy) -> bool {
     const int s = fill % kStages;
     const uint32_t n = fill / kStages;
@@ -893,11 +898,11 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     }
 #pragma unroll
     for (int c = 0; c < 5; ++c) {  // chunks 0..3, then the tail
-      const int part = c < 4 ? part_of_chunk(c, PF) : tail_part(PF);
+      const int part = c < 4 ? part_of_chunk(c, PT) : tail_part(PT);
       uint64_t* full = &ms->kv_full[s][part];
-      if (c < 4 && part_begins(c, PF)) {  // a part begins
+      if (c < 4 && part_begins(c, PT)) {  // a part begins
         if (!by.same(wait_or_abort(&ms->kv_free[s][part], (n & 1) ^ 1, ms, p))) return false;
-        if (by.leader) mbar_arrive_expect_tx(full, part_bytes(part, PF));
+        if (by.leader) mbar_arrive_expect_tx(full, part_bytes(part, PT));
       }
       if (c < 4) {
 #pragma unroll
@@ -922,12 +927,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   // stands between the two, and 10 KB less code, which the tile loops compete with for the
   // instruction caches, is worth more: 32 x 32 nodes 288 -> 281 us.)
   uint32_t early = 0;
-  if (PF != 3 && threadIdx.x == 0 && !p.test_stall) {
+  if (!WI && threadIdx.x == 0 && !p.test_stall) {
     const Cursor c0 = first_unit<PF>(args, ms);
     if (has_unit<PF>(args, ms, c0)) {
       const UnitInfo u0 = unit_info<PF>(args, ms, c0);
       for (int k0 = u0.key_lo; k0 < u0.key_hi && early < (uint32_t)kStages; k0 += kTileKeys) {
-        if (!issue_tile(Issuer<PF == 3>(), u0, k0, early, read_once)) break;
+        if (!issue_tile(Issuer<WI>(), u0, k0, early, read_once)) break;
         ++early;
       }
     }
@@ -964,7 +969,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    const Issuer<PF == 3> by;
+    const Issuer<WI> by;
     if (by.runs(lane)) {
       uint32_t fill = 0;  // tiles issued so far (the first `early` ones in the prologue)
       // L2 prefetch cursor: runs kPrefetchTiles tiles ahead of the TMA loads so that they
@@ -1013,7 +1018,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       }
       // Drain: wait (bounded) until the consumers released every part still holding a load.
       for (uint32_t f = (fill > kStages ? fill - kStages : 0); f < fill; ++f)
-        for (int c = 0; c < num_parts(PF); ++c)
+        for (int c = 0; c < num_parts(PT); ++c)
           mbar_wait(&ms->kv_free[f % kStages][c], (f / kStages) & 1, kWaitLimitNs);
     }
   } else if (warp == 1) {
@@ -1022,7 +1027,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // read and its unit's query terms are staged. Values (PV) have their own issuing warp: a
     // single thread spends tens of cycles per tcgen05.mma, so one issuer would serialise the
     // two.
-    const Issuer<PF == 3> by;
+    const Issuer<WI> by;
     if (by.runs(lane)) {
       constexpr uint32_t idesc_qk = instr_desc(0, 0, 0, 0, 128, C::NQK);
       const uint64_t a_main0 = smem_desc(smem_addr(smem + C::kOffStages), 16, 1024, Swizzle::k128B);
@@ -1049,8 +1054,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           // each latent chunk as soon as it has landed, then the RoPE tail
 #pragma unroll
           for (int c = 0; c < 4 && ok; ++c) {
-            if (part_begins(c, PF)) {  // a part has landed
-              if (!(ok = by.same(wait_or_abort(&ms->kv_full[s][part_of_chunk(c, PF)], ph, ms, p)))) break;
+            if (part_begins(c, PT)) {  // a part has landed
+              if (!(ok = by.same(wait_or_abort(&ms->kv_full[s][part_of_chunk(c, PT)], ph, ms, p)))) break;
               tc_fence_after();
             }
 #pragma unroll
@@ -1074,7 +1079,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // PV of every tile the moment its probabilities are in shared memory; completion hands
     // the KV stage back to the producer, part by part, and lets the softmax reuse P and
     // rescale O.
-    const Issuer<PF == 3> by;
+    const Issuer<WI> by;
     if (by.runs(lane)) {
       // A = V^T as e4m3 codes, B = P^T as e5m2 terms (kind::f8f6f4 takes each operand's
       // format from its own descriptor field), both MN-major
@@ -1116,7 +1121,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                          t > 0 || ks > 0 || term > 0);
               }
             }
-            if (part_ends(c, PF)) by.commit(&ms->kv_free[s][part_of_chunk(c, PF)]);
+            if (part_ends(c, PT)) by.commit(&ms->kv_free[s][part_of_chunk(c, PT)]);
           }
         }
       }
@@ -1175,7 +1180,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // Two or three warpgroups, each owning an equal share of the query rows; thread i of a
     // warpgroup owns key i of the tile (its TMEM lane).
     constexpr int RH = C::kRH;
-    constexpr float kHeadroom = kPScale + (PF == 3 ? kTreeGap : kRescaleGap);
+    constexpr float kHeadroom = kPScale + (WI ? kTreeGap : kRescaleGap);
     const int wg = (warp - kSoftmaxWarp0) >> 2;
     const int rb = wg * RH;  // rows [rb, rb + RH)
     const int wq = warp & 3;  // TMEM lane quadrant
@@ -1203,7 +1208,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     int pv_seen = -1;
     auto wait_pv_upto = [&](int target) -> bool {
       for (int g = pv_seen + 1; g <= target; ++g) {
-        if (!warp_wait(&ms->kv_free[g % kStages][tail_part(PF)], (g / kStages) & 1)) return false;
+        if (!warp_wait(&ms->kv_free[g % kStages][tail_part(PT)], (g / kStages) & 1)) return false;
         pv_seen = g;
       }
       return true;
@@ -1258,7 +1263,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       const int lim_cap = un.key_hi - 1;
       // (tree: the last key of the prefix, which every node sees; the nodes' own keys follow)
       const int lim0 = min(lim_cap, L - p.n_q + (PF == 3 ? -1 : un.j0 + p.mask_shift));
-      if constexpr (SC) bs.begin(p, un.b, un.key_lo + (i & ~63), i & 63, un.key_hi);
+      if constexpr (SC) bs.begin(p, un.b, un.key_lo + i, un.key_hi);
       // this unit's row scales (staged with its query terms)
       ok &= warp_wait(&ms->q_full[k % C::kQB], (k / C::kQB) & 1);
       // mo: the row's running max less kPScale (p = 2^(x - mo)); kNoMax before its first key
@@ -1269,7 +1274,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         mo[r] = kNoMax;
         l[r] = 0.f;
       }
-      if (PF == 3 && lane < RH) ms->tree_max[moves & 1][rb + lane] = kNoMax;
+      if (WI && lane < RH) ms->tree_max[moves & 1][rb + lane] = kNoMax;
       warp_arrive(&ms->q_empty[k % C::kQB]);
       for (int t = 0; t < ntiles; ++t, ++tile) {
         const int sb = tile % C::kSBuf;
@@ -1277,7 +1282,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         const int k0 = un.key_lo + t * kTileKeys;
         const int kabs = k0 + i;
         KeyScale ks;
-        if constexpr (SC) ks = bs.take(p, un.b, un.key_hi);
+        if constexpr (SC) ks = bs.take(p, un.key_hi);
         ok &= warp_wait(&ms->s_full[sb], (tile / C::kSBuf) & 1);
         tc_fence_after();
         float x[RH];
@@ -1340,7 +1345,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < RH; ++r) over |= (x[r] > mo[r] + kHeadroom);
         bool grow;
-        if constexpr (PF == 3) {
+        if constexpr (WI) {
           grow = wg_any(over || !ok);
           if (grow && wg_any(!ok)) {  // the warpgroup's once-a-tile vote on its waits
             ok = false;
@@ -1358,7 +1363,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           grow = (gf.x | gf.y | gf.z | gf.w) != 0;
         }
         bool need_rescale = false;
-        if (PF == 3 && grow) {
+        if (WI && grow) {
           // as below, but a lane takes a row (less code to fetch, and fewer steps): the maxima in
           // shared memory, read from the side that the time before wrote, written to the other
           // (each warp of the warpgroup the same values)
@@ -1451,7 +1456,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           tc_fence_after();
         }
         if (t > 0) {
-          if (PF == 3 && need_rescale) {
+          if (WI && need_rescale) {
             // (tree: one small loop over the pieces of O; its code is fetched cold when a short
             // call first needs it)
             __syncwarp();
@@ -1547,13 +1552,13 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         tc_fence_before();
         warp_arrive(&ms->p_full[tile & 1]);
       }
-      if (PF != 3 && !__all_sync(0xffffffffu, ok)) {  // (tree: the vote below)
+      if (!WI && !__all_sync(0xffffffffu, ok)) {  // (tree: the vote below)
         ok = false;
         break;
       }
       if (trace && threadIdx.x == 32 * kSoftmaxWarp0) trace[kTrLastP] = globaltimer_ns();
       // ---- epilogue: row sums, then O / l
-      if constexpr (PF == 3) {
+      if constexpr (WI) {
         // all rows at once: each exchange halves the rows that a lane still adds up
         float s[RH];
 #pragma unroll
@@ -1589,7 +1594,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         inv[r] = lt == 0.f ? 0.f : kv_scale / lt;  // (a row that saw a NaN: its sum is NaN, so is it)
       }
       ok &= wait_pv_upto((int)tile - 1);
-      if (PF == 3 ? wg_any(!ok) : !__all_sync(0xffffffffu, ok)) {
+      if (WI ? wg_any(!ok) : !__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
