@@ -185,13 +185,14 @@ class KVCache:
         t = self.scales
         if t is None:
             return None
-        pages, size = self.pool.shape[:2]
-        if t.dtype is not _F32 or not t.is_contiguous() or t.get_device() != self.pool.get_device():
+        pool = self.pool
+        if t.dtype is not _F32 or not t.is_contiguous() or t.get_device() != pool.get_device():
             raise ValueError("KVCache.scales must be a contiguous float32 tensor on the pool's device")
-        block = size // t.shape[1] if t.dim() == 2 and t.shape[1] > 0 else 0
-        if t.dim() != 2 or t.shape[0] != pages or block * t.shape[1] != size or block not in _BLOCKS:
+        shape, (pages, size, *_) = t.shape, pool.shape
+        block = size // shape[1] if len(shape) == 2 and shape[1] > 0 else 0
+        if block not in _BLOCKS or shape[0] != pages or block * shape[1] != size:
             raise ValueError("KVCache.scales must be [num_pages, page_size / block] for blocks of 1, 2, 4, .. 64 "
-                             f"positions, got {tuple(t.shape)} for {pages} pages of {size}")
+                             f"positions, got {tuple(shape)} for {pages} pages of {size}")
         if float(self.kv_scale) != 1.0:
             raise ValueError("a KVCache with block scales has kv_scale 1 (it is not read)")
         return mla_scales_t(t.data_ptr(), block)
@@ -225,8 +226,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle (as torch.cuda.current_stream() has it)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -264,10 +265,10 @@ def mla_decode(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None
             return mla_decode(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 3)
     B, H = q.shape[0], q.shape[1]
+    c, scales = kv.c_struct(), kv.c_scales()
+    ws = workspace(MLA_OP_DECODE, B, H, 1, q.device) if ws is None else ws
     out = torch.empty(B, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(B, H, dtype=torch.float32, device=q.device) if lse is None else lse
-    ws = workspace(MLA_OP_DECODE, B, H, 1, q.device) if ws is None else ws
-    c, scales = kv.c_struct(), kv.c_scales()
     args = (q.data_ptr(), B, H, sm_scale, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream))
     if scales is None:
         _check("mla_decode", library().mla_decode(c, *args))
@@ -284,10 +285,10 @@ def mla_verify(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None
             return mla_verify(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 4)
     B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
+    c, scales = kv.c_struct(), kv.c_scales()
+    ws = workspace(MLA_OP_VERIFY, B, H, n_q, q.device) if ws is None else ws
     out = torch.empty(B, n_q, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(B, n_q, H, dtype=torch.float32, device=q.device) if lse is None else lse
-    ws = workspace(MLA_OP_VERIFY, B, H, n_q, q.device) if ws is None else ws
-    c, scales = kv.c_struct(), kv.c_scales()
     if scales is None:
         _check("mla_verify", library().mla_verify(ctypes.byref(c), q.data_ptr(), B, n_q, H, sm_scale,
                                              out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
@@ -373,10 +374,10 @@ def mla_prefill(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=Non
             return mla_prefill(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 3)
     T, H = q.shape[0], q.shape[1]
+    c, scales = kv.c_struct(), kv.c_scales()
+    ws = workspace(MLA_OP_PREFILL, 1, H, T, q.device) if ws is None else ws
     out = torch.empty(T, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(T, H, dtype=torch.float32, device=q.device) if lse is None else lse
-    ws = workspace(MLA_OP_PREFILL, 1, H, T, q.device) if ws is None else ws
-    c, scales = kv.c_struct(), kv.c_scales()
     args = (q.data_ptr(), T, H, sm_scale, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream))
     if scales is None:
         _check("mla_prefill", library().mla_prefill(c, *args))
@@ -632,13 +633,13 @@ def mla_cache_gather(kv: KVCache, cu_rows: torch.Tensor, n: int, starts: Optiona
     if not f32 and out is None and dtype is not _BF16:
         raise ValueError("dtype must be bfloat16 or float32")
     cu_ptr = _dense(cu_rows, "cu_rows", _I64, (B + 1,), dev)
+    starts_ptr = None if starts is None else _dense(starts, "starts", _I32, (B,), dev)
+    scales, word, current = kv.c_scales(), _status_ptr(status, dev), _on(dev)
     if out is None:
         out = torch.empty((n, MLA_D), dtype=dtype, device=dev)
     else:
         _dense(out, "out", _F32 if f32 else _BF16, (n, MLA_D), dev)
-    args = (B, None if starts is None else _dense(starts, "starts", _I32, (B,), dev), cu_ptr, n,
-            out.data_ptr(), f32, _status_ptr(status, dev), _on(dev))
-    scales = kv.c_scales()
+    args = (B, starts_ptr, cu_ptr, n, out.data_ptr(), f32, word, current)
     if scales is None:
         _check("mla_cache_gather", library().mla_cache_gather(c, *args))
     else:
@@ -656,6 +657,14 @@ def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_sc
     _q_check(q, 4)
     B, n, H, _ = q.shape
     dev = q.device
+    c, scales = kv.c_struct(), kv.c_scales()
+    if kv.seq_lens.shape[0] < B or kv.page_table.shape[0] < B or kv.pool.device != dev:
+        raise ValueError("kv must describe q's sequences, on q's device")
+    mask, current = _dense(tree_mask, "tree_mask", _I64, (B, n), dev), _on(dev)
+    if ws is None:
+        ws = workspace(MLA_OP_VERIFY_TREE, B, H, n, dev)
+    elif ws.dtype is not _U8 or not ws.is_contiguous() or ws.device != dev:
+        raise ValueError("ws must be a contiguous uint8 tensor on q's device")
     if out is None:
         out = torch.empty((B, n, H, MLA_DV), dtype=_BF16, device=dev)
     else:
@@ -664,15 +673,7 @@ def mla_verify_tree(kv: KVCache, q: torch.Tensor, tree_mask: torch.Tensor, sm_sc
         lse = torch.empty((B, n, H), dtype=_F32, device=dev)
     else:
         _dense(lse, "lse", _F32, (B, n, H), dev)
-    if ws is None:
-        ws = workspace(MLA_OP_VERIFY_TREE, B, H, n, dev)
-    elif ws.dtype is not _U8 or not ws.is_contiguous() or ws.device != dev:
-        raise ValueError("ws must be a contiguous uint8 tensor on q's device")
-    if kv.seq_lens.shape[0] < B or kv.page_table.shape[0] < B or kv.pool.device != dev:
-        raise ValueError("kv must describe q's sequences, on q's device")
-    c, scales = kv.c_struct(), kv.c_scales()
-    args = (q.data_ptr(), B, n, H, sm_scale, _dense(tree_mask, "tree_mask", _I64, (B, n), dev), out.data_ptr(),
-            lse.data_ptr(), ws.data_ptr(), ws.numel(), _on(dev))
+    args = (q.data_ptr(), B, n, H, sm_scale, mask, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), current)
     if scales is None:
         _check("mla_verify_tree", library().mla_verify_tree(c, *args))
     else:
