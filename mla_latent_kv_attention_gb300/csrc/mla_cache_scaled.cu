@@ -9,10 +9,16 @@
 // A unit of work is a block of one sequence that new positions fall into. Sequence b's units begin
 // at cu_rows[b] / G + 2 b: m rows touch at most m / G + 2 blocks of G, so no unit needs to know how
 // many blocks the sequences before it touch, at the price of a few units that find nothing (G = 1:
-// a unit a row, none wasted). Four rows a warp (fewer where G is smaller), held in registers from the
-// loads to the codes; the warps of a unit exchange their largest entries through shared memory.
-// Bound: HBM for many rows (1,152 bytes read and 576 written a row), the chain of dependent loads
-// (cu_rows, length, page and row) for few.
+// a unit a row, none wasted). Rows stay in registers, normalised, from the loads to the codes; the
+// warps of a unit exchange their largest entries through shared memory.
+//
+// Rows a warp: two, four for blocks of 64 (whose unit would be a CTA of 1,024 threads otherwise). In
+// us for 8,192 rows from HBM with one / two / four: G = 4 8.2 / 7.4 / 8.2, 16 8.9 / 7.4 / 8.1, 32 10.5 /
+// 7.7 / 8.1, 64 - / 8.4 / 8.3; 32 sequences of one row, G = 16: 3.2 / 3.4 / 3.9.
+// Bound: the launch and a chain of dependent steps (cu_rows, rows and page, the largest entry over the
+// unit, codes), one round of CTAs each: 8,192 rows (14.2 MB) 5.8 us in L2, 7.4 us from HBM; 32
+// sequences of one row 3.4 us in blocks of 16, of which about 0.7 us are the earlier positions' scale
+// and codes, 2.6 us with a scale a position.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -49,7 +55,7 @@ __device__ __forceinline__ float scale_for(float top) {
 
 template <int G>
 struct ScaledCfg {
-  static constexpr int kRows = G < 4 ? G : 4;             // rows a warp
+  static constexpr int kRows = G == 64 ? 4 : (G < 2 ? 1 : 2);  // rows a warp
   static constexpr int kUnitWarps = G / kRows;            // warps a unit
   static constexpr int kWarps = kUnitWarps > 8 ? kUnitWarps : 8;  // warps a CTA
   static constexpr int kUnits = kWarps / kUnitWarps;      // units a CTA
@@ -76,25 +82,35 @@ __global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.status && a.cu_rows[a.B] > a.n)
     atomicCAS(a.status, 0u, (unsigned)MLA_ERR_BOUNDS);
 
-  // the last sequence whose units begin at or before this one: 32 candidates a round
-  int64_t lo = 0, len = a.B;
-  bool found = true;
+  // the last sequence whose units begin at or before this one: 32 candidates a round, of which the
+  // last round's come with what the unit needs of them
+  int64_t lo = 0, len = a.B, row0, row1;
+  int L;
+  bool found;
   while (true) {
     const int64_t step = (len + 31) / 32;
-    const int64_t b = lo + lane * step;
-    const bool at = b < lo + len && first_unit_of<G>(a.cu_rows[b], b) <= unit;
-    const int hits = __popc(__ballot_sync(0xffffffffu, at));
-    if (hits == 0) {  // (rows before the first sequence)
-      found = false;
+    const int64_t at = min(lo + lane * step, lo + len - 1);
+    row0 = a.cu_rows[at];
+    row1 = 0;
+    L = 0;
+    if (step == 1) {
+      row1 = a.cu_rows[at + 1];
+      L = a.kv.seq_lens[at];
+    }
+    const bool begun = lane * step < len && first_unit_of<G>(row0, at) <= unit;
+    const int hits = __popc(__ballot_sync(0xffffffffu, begun));
+    const int last = max(hits - 1, 0);
+    found = hits > 0;  // (not found: rows before the first sequence)
+    lo += last * step;
+    len = min(step, len - last * step);
+    if (step == 1) {
+      row0 = __shfl_sync(0xffffffffu, row0, last);
+      row1 = __shfl_sync(0xffffffffu, row1, last);
+      L = __shfl_sync(0xffffffffu, L, last);
       break;
     }
-    lo += (hits - 1) * step;
-    len = min(step, len - (hits - 1) * step);
-    if (step == 1) break;
   }
   const int64_t b = lo;
-  const int64_t row0 = a.cu_rows[b], row1 = a.cu_rows[b + 1];
-  const int L = a.kv.seq_lens[b];
   const int64_t m = row1 - row0;
   // (the unit's place among its sequence's, and its block's first position)
   const int64_t nth = unit - first_unit_of<G>(row0, b);
@@ -151,33 +167,29 @@ __global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
     g[4] = g1.x, g[5] = g1.y, g[6] = g1.z, g[7] = g1.w;
   }
   __syncthreads();  // (the frequencies)
-  float norm[C::kRows];
+  float y[C::kRows][16];
   float2 pe[C::kRows];
-  // entry e of the row's 16 latent entries, normalised (twice the same value: once for the
-  // largest, once for its code)
-  auto latent = [&](int k, int e) {
-    const uint32_t w[8] = {v0[k].x, v0[k].y, v0[k].z, v0[k].w, v1[k].x, v1[k].y, v1[k].z, v1[k].w};
-    const uint32_t two = w[e >> 1], gain = g[e >> 1];
-    float c = __uint_as_float(e & 1 ? two & 0xFFFF0000u : two << 16);
-    if (a.weight) c = c * norm[k] * __uint_as_float(e & 1 ? gain & 0xFFFF0000u : gain << 16);
-    return c;
-  };
   float top = 0.f;
 #pragma unroll
   for (int k = 0; k < C::kRows; ++k) {
-    norm[k] = 1.f;
+    const uint32_t w[8] = {v0[k].x, v0[k].y, v0[k].z, v0[k].w, v1[k].x, v1[k].y, v1[k].z, v1[k].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[k][2 * e] = __uint_as_float(w[e] << 16);
+      y[k][2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
     if (a.weight) {
-      const uint32_t w[8] = {v0[k].x, v0[k].y, v0[k].z, v0[k].w, v1[k].x, v1[k].y, v1[k].z, v1[k].w};
       float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float c0 = __uint_as_float(w[e] << 16), c1 = __uint_as_float(w[e] & 0xFFFF0000u);
-        ss = fmaf(c0, c0, ss);
-        ss = fmaf(c1, c1, ss);
-      }
+      for (int e = 0; e < 16; ++e) ss = fmaf(y[k][e], y[k][e], ss);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      norm[k] = rsqrtf(ss * (1.0f / kDV) + a.eps);
+      const float norm = rsqrtf(ss * (1.0f / kDV) + a.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[k][2 * e] = y[k][2 * e] * norm * __uint_as_float(g[e] << 16);
+        y[k][2 * e + 1] = y[k][2 * e + 1] * norm * __uint_as_float(g[e] & 0xFFFF0000u);
+      }
     }
     pe[k] = make_float2(__uint_as_float(pair[k] << 16), __uint_as_float(pair[k] & 0xFFFF0000u));
     if (a.positions)
@@ -185,7 +197,7 @@ __global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
     // (fmaxf passes over NaN)
     top = fmaxf(top, fmaxf(fabsf(pe[k].x), fabsf(pe[k].y)));
 #pragma unroll
-    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(latent(k, e)));
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(y[k][e]));
   }
   if (top == INFINITY) {  // rare: the largest of the finite entries
     auto finite = [](float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.f; };
@@ -194,7 +206,7 @@ __global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
     for (int k = 0; k < C::kRows; ++k) {
       top = fmaxf(top, fmaxf(finite(pe[k].x), finite(pe[k].y)));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, finite(latent(k, e)));
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, finite(y[k][e]));
     }
   }
   // (bits of floats that are not negative order as they do)
@@ -233,8 +245,7 @@ __global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
       uint32_t code[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        code[e] = e4m3x4(latent(k, 4 * e) * inv, latent(k, 4 * e + 1) * inv, latent(k, 4 * e + 2) * inv,
-                         latent(k, 4 * e + 3) * inv);
+        code[e] = e4m3x4(y[k][4 * e] * inv, y[k][4 * e + 1] * inv, y[k][4 * e + 2] * inv, y[k][4 * e + 3] * inv);
       reinterpret_cast<uint4*>(dst)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
       uint32_t pc = e4m3x2(pe[k].x * inv, pe[k].y * inv);
       if (!rope.interleaved) {
