@@ -402,10 +402,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = wk.j0; j < wk.j1; ++j, ++g) {
         if ((g & 1) != wg) continue;
         // the k-th tile of this parity is phase k of this parity's barriers
-        if (!(ok = wait_or_abort(&ms->s_full[wg], mine & 1, ms))) break;
+        ok = wait_or_abort(&ms->s_full[wg], mine & 1, ms);
         // this warpgroup's previous values MMA (it wrote O and read P from the buffer about
         // to be overwritten) finished before these scores were computed; confirm its phase
-        if (mine > 0 && !(ok = wait_or_abort(&ms->pv_done[wg], (mine - 1) & 1, ms))) break;
+        if (mine > 0) ok &= wait_or_abort(&ms->pv_done[wg], (mine - 1) & 1, ms);
+        // (a wait that gave up takes the whole warp along: what follows loads tensor memory, which
+        // a warp does as one)
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const int k0 = j * kBN;
         const bool edge = k0 + kBN - 1 > last_key;  // the causal edge crosses this tile
@@ -426,9 +432,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         mt *= p.scale_log2;
-        if (mt > m_run + kRescale) {  // first tile, or a large jump: rescale this O
+        // First tile, or a large jump of some row: rescale this O. Rows jump one by one, but the warp
+        // loads and stores tensor memory as one: rows that stay take the factor 1.
+        const bool jump = mt > m_run + kRescale;
+        if (__any_sync(0xffffffffu, jump)) {
+          const float f = jump ? ex2(m_run - mt) : 1.f;
           if (have) {
-            const float f = ex2(m_run - mt);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               float w[16];
@@ -440,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             l *= f;
           }
-          m_run = mt;
+          if (jump) m_run = mt;
         }
         // pass 2: probabilities, packed two 16-bit values per column over the first kBN / 2
         // score columns (column 16q + i holds keys 32q + 2i, 32q + 2i + 1; chunk q's packed
@@ -488,11 +497,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- epilogue: both warpgroups' (m, l, O) merge; warpgroup wg writes dims 64 wg.. ----
-      if (have && !(ok = wait_or_abort(&ms->pv_done[wg], (mine - 1) & 1, ms))) break;
+      if (have) ok = wait_or_abort(&ms->pv_done[wg], (mine - 1) & 1, ms);
       tc_fence_before();
       ms->red_max[0][wg][row] = have ? m_run : -INFINITY;
       ms->red_sum[wg][row] = have ? l : 0.f;
-      if (!(ok = pair_sync())) break;
+      ok &= pair_sync();
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       const float m0 = ms->red_max[0][0][row], m1 = ms->red_max[0][1][row];
       const float mm = fmaxf(m0, m1);
@@ -545,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else if (wg == 0 && x.write && t < p.T && p.lse)
         p.lse[(int64_t)t * p.H + x.h] = 0.6931471805599453f * (mm + log2f(lt));
       tc_fence_before();
-      if (!(ok = pair_sync())) break;  // both have read the shared (m, l) and both O's
+      ok = __all_sync(0xffffffffu, pair_sync());  // both have read the shared (m, l) and both O's
     }
   }
 

@@ -123,7 +123,9 @@ __global__ void __launch_bounds__(128, 2)
   __syncwarp();
 
   // ---- epilogue: thread t of warp w holds row m0 + 32 w + t of the tile
-  const bool ok = mbar_wait(&ms->done, 0, kPWaitNs) && !*reinterpret_cast<volatile int*>(&ms->abort);
+  // (one outcome a warp, which loads tensor memory as one)
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(&ms->done, 0, kPWaitNs) &&
+                                              !*reinterpret_cast<volatile int*>(&ms->abort));
   tc_fence_after();
   const int row = m0 + warp * 32 + lane;
   if (ok) {
