@@ -402,16 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = wk.j0; j < wk.j1; ++j, ++g) {
         if ((g & 1) != wg) continue;
         // the k-th tile of this parity is phase k of this parity's barriers
-        ok = wait_or_abort(&ms->s_full[wg], mine & 1, ms);
+        // (A lane whose wait gave up waits no more but runs on with its warp, to the vote after the
+        // tiles: what follows loads tensor memory, which a warp does as one.)
+        if (ok) ok = wait_or_abort(&ms->s_full[wg], mine & 1, ms);
         // this warpgroup's previous values MMA (it wrote O and read P from the buffer about
         // to be overwritten) finished before these scores were computed; confirm its phase
-        if (mine > 0) ok &= wait_or_abort(&ms->pv_done[wg], (mine - 1) & 1, ms);
-        // (a wait that gave up takes the whole warp along: what follows loads tensor memory, which
-        // a warp does as one)
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        if (ok && mine > 0) ok = wait_or_abort(&ms->pv_done[wg], (mine - 1) & 1, ms);
         tc_fence_after();
         const int k0 = j * kBN;
         const bool edge = k0 + kBN - 1 > last_key;  // the causal edge crosses this tile
@@ -495,13 +491,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&ms->p_full[wg]);
         ++mine;
       }
-      if (!ok) break;
       // ---- epilogue: both warpgroups' (m, l, O) merge; warpgroup wg writes dims 64 wg.. ----
-      if (have) ok = wait_or_abort(&ms->pv_done[wg], (mine - 1) & 1, ms);
+      if (ok && have) ok = wait_or_abort(&ms->pv_done[wg], (mine - 1) & 1, ms);
       tc_fence_before();
       ms->red_max[0][wg][row] = have ? m_run : -INFINITY;
       ms->red_sum[wg][row] = have ? l : 0.f;
-      ok &= pair_sync();
+      if (ok) ok = pair_sync();
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
