@@ -74,34 +74,26 @@ constexpr int kTileKeys = 128;
 constexpr int kStages = 2;
 constexpr int kChunkBytes = 16384;                     // 128 keys x 128 bytes, SW128
 constexpr int kStageBytes = 4 * kChunkBytes + 2 * 4096;  // 73,728 bytes loaded per tile
-// A stage is filled and freed in two halves: latent chunks 0-1, then chunks 2-3 with the
-// RoPE tail. The values MMA frees the first half as soon as its own MMAs complete, so the
-// next tile's first half loads while the second is still being read. (Every
-// tcgen05.commit costs the issuing thread time: measured, five parts ran slower than one,
-// two fastest.)
-// Tree verify (pf = 3, the kernel's PF): the second half once more in two, chunk 2, then chunk 3
-// with the tail (its MMAs are issued fast enough for the commit: 32 x 32 nodes over 4K-16K 291.7
-// -> 287.7 us; four parts or 3 + 1 chunks ran slower).
-constexpr int kMaxParts = 3;
-__host__ __device__ constexpr int num_parts(int pf) { return pf == 3 ? 3 : 2; }
-__host__ __device__ constexpr int part_of_chunk(int c, int pf) {
-  return c < 2 ? 0 : (pf == 3 ? c - 1 : 1);
+// A stage is filled and freed in three parts: latent chunks 0-1, chunk 2, chunk 3 with the RoPE
+// tail. The values MMA frees a part as soon as its own MMAs complete, so the next tile's keys begin
+// to land while the rest of the stage is still being read. (Every tcgen05.commit costs the issuing
+// warp time: draft trees, 32 x 32 nodes over 4K-16K, 291.7 us in two parts, 287.7 in three; four
+// parts or 3 + 1 chunks ran slower.)
+constexpr int kParts = 3;
+__host__ __device__ constexpr int part_of_chunk(int c) { return c < 2 ? 0 : c - 1; }
+constexpr int kTailPart = kParts - 1;
+__host__ __device__ constexpr bool part_begins(int c) {
+  return c == 0 || part_of_chunk(c) != part_of_chunk(c - 1);
 }
-__host__ __device__ constexpr int tail_part(int pf) { return num_parts(pf) - 1; }
-__host__ __device__ constexpr bool part_begins(int c, int pf) {
-  return c == 0 || part_of_chunk(c, pf) != part_of_chunk(c - 1, pf);
+__host__ __device__ constexpr bool part_ends(int c) {
+  return c == 3 || part_of_chunk(c) != part_of_chunk(c + 1);
 }
-__host__ __device__ constexpr bool part_ends(int c, int pf) {
-  return c == 3 || part_of_chunk(c, pf) != part_of_chunk(c + 1, pf);
-}
-__host__ __device__ constexpr int part_bytes(int part, int pf) {
-  int bytes = part == tail_part(pf) ? 2 * 4096 : 0;
-  for (int c = 0; c < 4; ++c) bytes += part_of_chunk(c, pf) == part ? kChunkBytes : 0;
+__host__ __device__ constexpr int part_bytes(int part) {
+  int bytes = part == kTailPart ? 2 * 4096 : 0;
+  for (int c = 0; c < 4; ++c) bytes += part_of_chunk(c) == part ? kChunkBytes : 0;
   return bytes;
 }
-static_assert(part_bytes(0, 0) + part_bytes(1, 0) == kStageBytes &&
-                  part_bytes(0, 3) + part_bytes(1, 3) + part_bytes(2, 3) == kStageBytes,
-              "the parts make up the stage");
+static_assert(part_bytes(0) + part_bytes(1) + part_bytes(2) == kStageBytes, "the parts make up the stage");
 constexpr int kMaxThreads = 512;  // producer, 2 MMA issuers, query stager, 2-3 softmax warpgroups
 constexpr int kSoftmaxWarp0 = 4;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;        // 1 s
@@ -178,14 +170,13 @@ struct Misc {
   alignas(16) float row_scale[2][48];  // by unit parity
   alignas(16) float red[2][48 * 4];  // per-tile warp maxima, [row][warp]
   alignas(16) float lred[4][48];
-  alignas(16) float tree_max[2][48];  // tree: running maxima, by parity of the times they moved
+  alignas(16) float row_max[2][48];  // running maxima, by parity of the times they moved
   alignas(16) float alpha[48];       // this tile's rescale factors (each warp of a
                                      // warpgroup writes the same values for its rows)
-  alignas(16) int grow[2][12];       // per tile parity and warp: some row's max moves
   alignas(16) int row_j[48];         // new-position index j of each row (very negative for padding)
   alignas(16) int row_off[48];       // j * H + h: the row's index among its sequence's rows
-  alignas(8) uint64_t kv_full[kStages][kMaxParts];  // part landed (TMA transaction bytes)
-  uint64_t kv_free[kStages][kMaxParts];             // part no longer read by any MMA
+  alignas(8) uint64_t kv_full[kStages][kParts];  // part landed (TMA transaction bytes)
+  uint64_t kv_free[kStages][kParts];             // part no longer read by any MMA
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2];   // P of tile g is written: p_full[g % 2] (the softmax may run a tile
                         // ahead of the value MMAs when P lives in the stage)
@@ -208,7 +199,7 @@ struct Misc {
 };
 static_assert(offsetof(Misc, row_scale) % 16 == 0 && offsetof(Misc, red) % 16 == 0 &&
                   offsetof(Misc, lred) % 16 == 0 && offsetof(Misc, alpha) % 16 == 0 &&
-                  offsetof(Misc, grow) % 16 == 0,
+                  offsetof(Misc, row_j) % 16 == 0,
               "vector-accessed arrays must be 16-byte aligned");
 static_assert(offsetof(Misc, kv_full) % 8 == 0, "mbarriers must be 8-byte aligned");
 
@@ -583,54 +574,38 @@ __device__ __forceinline__ void stage_rows(const AttnParams& p, int R, const int
   }
 }
 
-// How the producer and the two issuing warps run. One thread each: lane 0 alone walks the tiles.
-// Tree: the whole warp does, and an elected lane issues. The control flow and the operands are
-// then the same for every lane as far as the compiler can tell (votes and broadcasts say so), so
-// it keeps them (of a descriptor only the low half moves) in the uniform registers that the MMA
-// and the TMA read, instead of moving up to eight registers there for each one. All three lie on
-// the chain of a key stage (values done, load, scores): 32 x 32 nodes over 4K-16K 315 -> 291 us
-// for the MMAs, 281 -> 270 us for the loads.
-template <bool WARP>
+// How the producer and the two issuing warps run: whole, an elected lane issuing. The control flow
+// and the operands are then the same for every lane as far as the compiler can tell (votes and
+// broadcasts say so), so it keeps them (of a descriptor only the low half moves) in the uniform
+// registers that the MMA and the TMA read, instead of moving up to eight registers there for each
+// one. All three lie on the chain of a key stage (values done, load, scores). In us, one thread
+// each (and a stage in two parts) / this: draft trees, 32 x 32 nodes over 4K-16K, 315 / 291 for the
+// MMAs, 281 / 270 for the loads; prefill 8,192 on 32K 8,787 / 6,777; verify 8 x 4 on 32K 69.2 / 57.1;
+// decode 32 x 4K-16K 48.9 / 46.5, 142,000 30.8 / 28.7, 512 x 100-300 60.1 / 57.6.
 struct Issuer {
   uint32_t leader;
-  __device__ __forceinline__ Issuer() : leader(WARP ? elect_one() : 1u) {}
-  __device__ __forceinline__ bool runs(int lane) const { return WARP || lane == 0; }
-  __device__ __forceinline__ bool same(bool v) const {
-    return WARP ? (bool)__all_sync(0xffffffffu, v) : v;
-  }
-  __device__ __forceinline__ uint32_t same(uint32_t v) const {
-    return WARP ? __shfl_sync(0xffffffffu, v, 0) : v;
-  }
+  __device__ __forceinline__ Issuer() : leader(elect_one()) {}
+  __device__ __forceinline__ bool same(bool v) const { return (bool)__all_sync(0xffffffffu, v); }
+  __device__ __forceinline__ uint32_t same(uint32_t v) const { return __shfl_sync(0xffffffffu, v, 0); }
   // a tile's place within a descriptor's base, and the descriptor `off` (16-byte units) past it
   __device__ __forceinline__ uint32_t place(uint64_t base, uint32_t tile_off) const {
-    return WARP ? same((uint32_t)base + tile_off) : tile_off;
+    return same((uint32_t)base + tile_off);
   }
   static __device__ __forceinline__ uint64_t at(uint64_t base, uint32_t place, uint32_t off) {
-    return WARP ? ((base >> 32 << 32) | (place + off)) : base + place + off;
+    return (base >> 32 << 32) | (place + off);
   }
   __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                       uint32_t accumulate) const {
-    if constexpr (WARP)
-      mma_f8f6f4_by(leader, d, a, b, idesc, accumulate);
-    else
-      mma_f8f6f4(d, a, b, idesc, accumulate);
+    mma_f8f6f4_by(leader, d, a, b, idesc, accumulate);
   }
   __device__ __forceinline__ void load(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
                                        uint64_t policy) const {
-    if constexpr (WARP)
-      tma_load_2d_hint_by(leader, dst, map, x, y, bar, policy);
-    else
-      tma_load_2d_hint(dst, map, x, y, bar, policy);
+    tma_load_2d_hint_by(leader, dst, map, x, y, bar, policy);
   }
   __device__ __forceinline__ void commit(uint64_t* bar) const {
-    if (!WARP || leader) mma_commit(bar);
+    if (leader) mma_commit(bar);
   }
 };
-
-#ifndef WI_RULE
-#define WI_RULE(RP, PF, SC) ((PF) == 3 || (SC))
-#endif
-constexpr bool whole_warps(int rp, int pf, bool sc) { return WI_RULE(rp, pf, sc); }
 
 // A key's scale as the softmax uses it. A scale that is none gives NaN scores to the rows that see the
 // key (those that do not see it are masked after the scores, and their weight 0 meets finite numbers).
@@ -696,8 +671,6 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                      const __grid_constant__ CUtensorMap map_main,
                      const __grid_constant__ CUtensorMap map_tail) {
   using C = Cfg<RP>;
-  constexpr bool WI = whole_warps(RP, PF, SC);
-  constexpr int PT = WI ? 3 : PF;
   const AttnParams& p = args.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -705,7 +678,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   Misc* ms = reinterpret_cast<Misc*>(smem + C::kOffMisc);
   uint8_t* pbuf = smem + C::kOffP;
   uint8_t* qbuf = smem + C::kOffQ;
-  const int warp = WI ? __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0) : (int)threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   // profiling hook: this CTA's stamps, or null
   // (TR: a separate instantiation for traced calls, so the usual one carries no stamp code)
@@ -716,7 +689,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s)
-      for (int c = 0; c < num_parts(PT); ++c) {
+      for (int c = 0; c < kParts; ++c) {
         mbar_init(&ms->kv_full[s][c], 1);
         mbar_init(&ms->kv_free[s][c], 1);
       }
@@ -876,7 +849,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   // held it have released it.
   const int64_t rows64 = p.num_pages * (int64_t)p.page_size;
   const int total_rows = rows64 > 0x7fffff00 ? 0x7fffff00 : (int)rows64;
-  auto issue_tile = [&](const Issuer<WI>& by, const UnitInfo& un, int k0, uint32_t fill,
+  auto issue_tile = [&](const Issuer& by, const UnitInfo& un, int k0, uint32_t fill,
                         uint64_t policy) -> bool {
     const int s = fill % kStages;
     const uint32_t n = fill / kStages;
@@ -898,11 +871,11 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     }
 #pragma unroll
     for (int c = 0; c < 5; ++c) {  // chunks 0..3, then the tail
-      const int part = c < 4 ? part_of_chunk(c, PT) : tail_part(PT);
+      const int part = c < 4 ? part_of_chunk(c) : kTailPart;
       uint64_t* full = &ms->kv_full[s][part];
-      if (c < 4 && part_begins(c, PT)) {  // a part begins
+      if (c < 4 && part_begins(c)) {  // a part begins
         if (!by.same(wait_or_abort(&ms->kv_free[s][part], (n & 1) ^ 1, ms, p))) return false;
-        if (by.leader) mbar_arrive_expect_tx(full, part_bytes(part, PT));
+        if (by.leader) mbar_arrive_expect_tx(full, part_bytes(part));
       }
       if (c < 4) {
 #pragma unroll
@@ -922,21 +895,6 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   // for the groups of one sequence.
   const uint64_t read_once = (is_prefill(PF) || (PF == 3 && p.team * p.passes > 1)) ? l2_policy_evict_normal()
                                                                           : l2_policy_evict_first();
-  // The first unit's first tiles go out from here, straight after the plan: on the way to
-  // the producer's loop a cold kernel spends microseconds fetching instructions. (Tree: nothing
-  // stands between the two, and 10 KB less code, which the tile loops compete with for the
-  // instruction caches, is worth more: 32 x 32 nodes 288 -> 281 us.)
-  uint32_t early = 0;
-  if (!WI && threadIdx.x == 0 && !p.test_stall) {
-    const Cursor c0 = first_unit<PF>(args, ms);
-    if (has_unit<PF>(args, ms, c0)) {
-      const UnitInfo u0 = unit_info<PF>(args, ms, c0);
-      for (int k0 = u0.key_lo; k0 < u0.key_hi && early < (uint32_t)kStages; k0 += kTileKeys) {
-        if (!issue_tile(Issuer<WI>(), u0, k0, early, read_once)) break;
-        ++early;
-      }
-    }
-  }
   if (trace && threadIdx.x == 0) trace[kTrPlanned] = globaltimer_ns();
 
   // The first unit's queries are on every CTA's critical path: warps 2.. stage them into
@@ -969,160 +927,154 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    const Issuer<WI> by;
-    if (by.runs(lane)) {
-      uint32_t fill = 0;  // tiles issued so far (the first `early` ones in the prologue)
-      // L2 prefetch cursor: runs kPrefetchTiles tiles ahead of the TMA loads so that they
-      // find their pages in L2 (deeper than the two shared-memory stages allow). The first
-      // kStages tiles are the TMA loads' own: the cursor starts past them (no page-table
-      // reads there: each is a round trip the second tile's load would wait behind).
-      Cursor pf_c = first_unit<PF>(args, ms);
-      UnitInfo pu = has_unit<PF>(args, ms, pf_c) ? unit_info<PF>(args, ms, pf_c) : UnitInfo{};
-      int pf_k = pu.key_lo;
-      uint32_t pf_tiles = 0;
-      auto prefetch_upto = [&](uint32_t target, bool issue) {
-        while (pf_tiles < target && has_unit<PF>(args, ms, pf_c)) {
-          if (pf_k >= pu.key_hi) {  // unit done (or empty)
-            pf_c = next_unit<PF>(args, pf_c);
-            if (has_unit<PF>(args, ms, pf_c)) pu = unit_info<PF>(args, ms, pf_c);
-            pf_k = pu.key_lo;
-            continue;
-          }
-          for (int h = 0; h < 2 && issue; ++h) {
-            const int kk = pf_k + 64 * h;
-            if (kk < pu.key_hi) {
-              const int phys = p.page_table[(int64_t)pu.b * p.pt_stride + kk / p.page_size];
-              if (phys >= 0 && phys < p.num_pages) {
-                const int rows = min(64, pu.key_hi - kk);
-                if (by.leader) bulk_prefetch_l2(p.pool + ((int64_t)phys * p.page_size + kk % p.page_size) * kD,
-                                 (uint32_t)rows * kD);
-              }
+    const Issuer by;
+    uint32_t fill = 0;  // tiles issued so far
+    // L2 prefetch cursor: runs kPrefetchTiles tiles ahead of the TMA loads so that they
+    // find their pages in L2 (deeper than the two shared-memory stages allow). The first
+    // kStages tiles are the TMA loads' own: the cursor starts past them (no page-table
+    // reads there: each is a round trip the second tile's load would wait behind).
+    Cursor pf_c = first_unit<PF>(args, ms);
+    UnitInfo pu = has_unit<PF>(args, ms, pf_c) ? unit_info<PF>(args, ms, pf_c) : UnitInfo{};
+    int pf_k = pu.key_lo;
+    uint32_t pf_tiles = 0;
+    auto prefetch_upto = [&](uint32_t target, bool issue) {
+      while (pf_tiles < target && has_unit<PF>(args, ms, pf_c)) {
+        if (pf_k >= pu.key_hi) {  // unit done (or empty)
+          pf_c = next_unit<PF>(args, pf_c);
+          if (has_unit<PF>(args, ms, pf_c)) pu = unit_info<PF>(args, ms, pf_c);
+          pf_k = pu.key_lo;
+          continue;
+        }
+        for (int h = 0; h < 2 && issue; ++h) {
+          const int kk = pf_k + 64 * h;
+          if (kk < pu.key_hi) {
+            const int phys = p.page_table[(int64_t)pu.b * p.pt_stride + kk / p.page_size];
+            if (phys >= 0 && phys < p.num_pages) {
+              const int rows = min(64, pu.key_hi - kk);
+              if (by.leader) bulk_prefetch_l2(p.pool + ((int64_t)phys * p.page_size + kk % p.page_size) * kD,
+                               (uint32_t)rows * kD);
             }
           }
-          ++pf_tiles;
-          pf_k += kTileKeys;
         }
-      };
-      prefetch_upto(kStages, false);
-      for (Cursor cu = first_unit<PF>(args, ms);
-           by.same(has_unit<PF>(args, ms, cu) && !aborted(ms) && !p.test_stall);
-           cu = next_unit<PF>(args, cu)) {
-        const UnitInfo un = unit_info<PF>(args, ms, cu);
-        const int key_hi = (int)by.same((uint32_t)un.key_hi);
-        for (int k0 = (int)by.same((uint32_t)un.key_lo); k0 < key_hi; k0 += kTileKeys) {
-          const bool ok = fill < early || issue_tile(by, un, k0, fill, read_once);
-          if (!ok) break;
-          ++fill;
-          prefetch_upto(fill + kPrefetchTiles, true);
-        }
+        ++pf_tiles;
+        pf_k += kTileKeys;
       }
-      // Drain: wait (bounded) until the consumers released every part still holding a load.
-      for (uint32_t f = (fill > kStages ? fill - kStages : 0); f < fill; ++f)
-        for (int c = 0; c < num_parts(PT); ++c)
-          mbar_wait(&ms->kv_free[f % kStages][c], (f / kStages) & 1, kWaitLimitNs);
+    };
+    prefetch_upto(kStages, false);
+    for (Cursor cu = first_unit<PF>(args, ms);
+         by.same(has_unit<PF>(args, ms, cu) && !aborted(ms) && !p.test_stall);
+         cu = next_unit<PF>(args, cu)) {
+      const UnitInfo un = unit_info<PF>(args, ms, cu);
+      const int key_hi = (int)by.same((uint32_t)un.key_hi);
+      for (int k0 = (int)by.same((uint32_t)un.key_lo); k0 < key_hi; k0 += kTileKeys) {
+        const bool ok = issue_tile(by, un, k0, fill, read_once);
+        if (!ok) break;
+        ++fill;
+        prefetch_upto(fill + kPrefetchTiles, true);
+      }
     }
+    // Drain: wait (bounded) until the consumers released every part still holding a load.
+    for (uint32_t f = (fill > kStages ? fill - kStages : 0); f < fill; ++f)
+      for (int c = 0; c < kParts; ++c)
+        mbar_wait(&ms->kv_free[f % kStages][c], (f / kStages) & 1, kWaitLimitNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ scores issuer
     // QK of every tile, chunk by chunk as its KV stage fills, once its S^T buffer has been
     // read and its unit's query terms are staged. Values (PV) have their own issuing warp: a
     // single thread spends tens of cycles per tcgen05.mma, so one issuer would serialise the
     // two.
-    const Issuer<WI> by;
-    if (by.runs(lane)) {
-      constexpr uint32_t idesc_qk = instr_desc(0, 0, 0, 0, 128, C::NQK);
-      const uint64_t a_main0 = smem_desc(smem_addr(smem + C::kOffStages), 16, 1024, Swizzle::k128B);
-      const uint64_t a_tail0 = smem_desc(smem_addr(smem + C::kOffStages + C::kTail), 16, 512, Swizzle::k64B);
-      const uint64_t b_main0 = smem_desc(smem_addr(qbuf), 16, 1024, Swizzle::k128B);
-      const uint64_t b_tail0 = smem_desc(smem_addr(qbuf + 4 * (C::NQK * 128)), 16, 512, Swizzle::k64B);
-      uint32_t g = 0, units_done = 0;
-      bool ok = true;
-      for (Cursor cu = first_unit<PF>(args, ms); by.same(has_unit<PF>(args, ms, cu) && ok);
-           cu = next_unit<PF>(args, cu)) {
-        const int n = (int)by.same((uint32_t)tiles_in(unit_info<PF>(args, ms, cu)));
-        if (n == 0) continue;
-        const int qslot = units_done % C::kQB;
-        if (!(ok = by.same(wait_or_abort(&ms->q_full[qslot], (units_done / C::kQB) & 1, ms, p)))) break;
-        const uint32_t qoff = (uint32_t)(qslot * C::kQBytes) >> 4;
-        for (int t = 0; t < n; ++t, ++g) {
-          const int s = g % kStages, sb = g % C::kSBuf;
-          const uint32_t ph = (g / kStages) & 1;
-          if (!(ok = by.same(wait_or_abort(&ms->s_empty[sb], ((g / C::kSBuf) & 1) ^ 1, ms, p)))) break;
-          const uint32_t soff = (uint32_t)(s * C::kStageStride) >> 4;
-          const uint32_t d = by.same(tmem + C::kSCol + sb * C::NQK);
-          const uint32_t am = by.place(a_main0, soff), at = by.place(a_tail0, soff);
-          const uint32_t bm = by.place(b_main0, qoff), bt = by.place(b_tail0, qoff);
-          // each latent chunk as soon as it has landed, then the RoPE tail
+    const Issuer by;
+    constexpr uint32_t idesc_qk = instr_desc(0, 0, 0, 0, 128, C::NQK);
+    const uint64_t a_main0 = smem_desc(smem_addr(smem + C::kOffStages), 16, 1024, Swizzle::k128B);
+    const uint64_t a_tail0 = smem_desc(smem_addr(smem + C::kOffStages + C::kTail), 16, 512, Swizzle::k64B);
+    const uint64_t b_main0 = smem_desc(smem_addr(qbuf), 16, 1024, Swizzle::k128B);
+    const uint64_t b_tail0 = smem_desc(smem_addr(qbuf + 4 * (C::NQK * 128)), 16, 512, Swizzle::k64B);
+    uint32_t g = 0, units_done = 0;
+    bool ok = true;
+    for (Cursor cu = first_unit<PF>(args, ms); by.same(has_unit<PF>(args, ms, cu) && ok);
+         cu = next_unit<PF>(args, cu)) {
+      const int n = (int)by.same((uint32_t)tiles_in(unit_info<PF>(args, ms, cu)));
+      if (n == 0) continue;
+      const int qslot = units_done % C::kQB;
+      if (!(ok = by.same(wait_or_abort(&ms->q_full[qslot], (units_done / C::kQB) & 1, ms, p)))) break;
+      const uint32_t qoff = (uint32_t)(qslot * C::kQBytes) >> 4;
+      for (int t = 0; t < n; ++t, ++g) {
+        const int s = g % kStages, sb = g % C::kSBuf;
+        const uint32_t ph = (g / kStages) & 1;
+        if (!(ok = by.same(wait_or_abort(&ms->s_empty[sb], ((g / C::kSBuf) & 1) ^ 1, ms, p)))) break;
+        const uint32_t soff = (uint32_t)(s * C::kStageStride) >> 4;
+        const uint32_t d = by.same(tmem + C::kSCol + sb * C::NQK);
+        const uint32_t am = by.place(a_main0, soff), at = by.place(a_tail0, soff);
+        const uint32_t bm = by.place(b_main0, qoff), bt = by.place(b_tail0, qoff);
+        // each latent chunk as soon as it has landed, then the RoPE tail
 #pragma unroll
-          for (int c = 0; c < 4 && ok; ++c) {
-            if (part_begins(c, PT)) {  // a part has landed
-              if (!(ok = by.same(wait_or_abort(&ms->kv_full[s][part_of_chunk(c, PT)], ph, ms, p)))) break;
-              tc_fence_after();
-            }
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              by.mma(d, by.at(a_main0, am, (c * kChunkBytes + kk * 32) >> 4),
-                     by.at(b_main0, bm, (c * (C::NQK * 128) + kk * 32) >> 4), idesc_qk, (c | kk) != 0);
+        for (int c = 0; c < 4 && ok; ++c) {
+          if (part_begins(c)) {  // a part has landed
+            if (!(ok = by.same(wait_or_abort(&ms->kv_full[s][part_of_chunk(c)], ph, ms, p)))) break;
+            tc_fence_after();
           }
-          if (!ok) break;  // the tail belongs to the last part, landed by now
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-            by.mma(d, by.at(a_tail0, at, (kk * 32) >> 4), by.at(b_tail0, bt, (kk * 32) >> 4), idesc_qk, 1);
-          by.commit(&ms->s_full[sb]);
+          for (int kk = 0; kk < 4; ++kk)
+            by.mma(d, by.at(a_main0, am, (c * kChunkBytes + kk * 32) >> 4),
+                   by.at(b_main0, bm, (c * (C::NQK * 128) + kk * 32) >> 4), idesc_qk, (c | kk) != 0);
         }
-        if (!ok) break;
-        by.commit(&ms->q_empty[qslot]);  // that query buffer is free once these complete
-        ++units_done;
+        if (!ok) break;  // the tail belongs to the last part, landed by now
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+          by.mma(d, by.at(a_tail0, at, (kk * 32) >> 4), by.at(b_tail0, bt, (kk * 32) >> 4), idesc_qk, 1);
+        by.commit(&ms->s_full[sb]);
       }
+      if (!ok) break;
+      by.commit(&ms->q_empty[qslot]);  // that query buffer is free once these complete
+      ++units_done;
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------------ values issuer
     // PV of every tile the moment its probabilities are in shared memory; completion hands
     // the KV stage back to the producer, part by part, and lets the softmax reuse P and
     // rescale O.
-    const Issuer<WI> by;
-    if (by.runs(lane)) {
-      // A = V^T as e4m3 codes, B = P^T as e5m2 terms (kind::f8f6f4 takes each operand's
-      // format from its own descriptor field), both MN-major
-      constexpr uint32_t idesc_stacked = instr_desc(kFmtE4M3, kFmtE5M2, 1, 1, 128, 3 * RP);
-      constexpr uint32_t idesc_term = instr_desc(kFmtE4M3, kFmtE5M2, 1, 1, 128, RP);
-      const uint64_t a0 = smem_desc(smem_addr(smem + C::kOffStages), kChunkBytes, 1024, Swizzle::k128B);
-      // P^T of stage 0's tile (at 48 rows; each stage has its own) or the shared buffer
-      const uint64_t b0 = smem_desc(smem_addr(C::kPInStage ? smem + C::kOffStages + 4 * kChunkBytes : pbuf),
-                                    128, 2048, Swizzle::kNone);
-      uint32_t g = 0;
-      bool ok = true;
-      for (Cursor cu = first_unit<PF>(args, ms); by.same(has_unit<PF>(args, ms, cu) && ok);
-           cu = next_unit<PF>(args, cu)) {
-        const int n = (int)by.same((uint32_t)tiles_in(unit_info<PF>(args, ms, cu)));
-        for (int t = 0; t < n; ++t, ++g) {
-          if (!(ok = by.same(wait_or_abort(&ms->p_full[g & 1], (g >> 1) & 1, ms, p)))) break;
-          tc_fence_after();
-          const int s = g % kStages;
-          const uint32_t soff = (uint32_t)(s * C::kStageStride) >> 4;
-          const uint32_t poff = C::kPInStage ? soff : 0u;
-          const uint32_t o = by.same(tmem), av = by.place(a0, soff), bp = by.place(b0, poff);
-          // chunk by chunk, each freed for the next tile's load once its own MMAs complete
-          // (back-to-back MMAs into one accumulator cost no more than alternating ones)
-          // chunk by chunk (back-to-back MMAs into one accumulator cost no more than
-          // alternating ones); each half of the stage is handed back once its MMAs complete.
-          // The second half's release also stands for the whole tile's values being done
-          // (P, which lives in the tail at 48 rows, and O for the softmax's rescale).
+    const Issuer by;
+    // A = V^T as e4m3 codes, B = P^T as e5m2 terms (kind::f8f6f4 takes each operand's
+    // format from its own descriptor field), both MN-major
+    constexpr uint32_t idesc_stacked = instr_desc(kFmtE4M3, kFmtE5M2, 1, 1, 128, 3 * RP);
+    constexpr uint32_t idesc_term = instr_desc(kFmtE4M3, kFmtE5M2, 1, 1, 128, RP);
+    const uint64_t a0 = smem_desc(smem_addr(smem + C::kOffStages), kChunkBytes, 1024, Swizzle::k128B);
+    // P^T of stage 0's tile (at 48 rows; each stage has its own) or the shared buffer
+    const uint64_t b0 = smem_desc(smem_addr(C::kPInStage ? smem + C::kOffStages + 4 * kChunkBytes : pbuf),
+                                  128, 2048, Swizzle::kNone);
+    uint32_t g = 0;
+    bool ok = true;
+    for (Cursor cu = first_unit<PF>(args, ms); by.same(has_unit<PF>(args, ms, cu) && ok);
+         cu = next_unit<PF>(args, cu)) {
+      const int n = (int)by.same((uint32_t)tiles_in(unit_info<PF>(args, ms, cu)));
+      for (int t = 0; t < n; ++t, ++g) {
+        if (!(ok = by.same(wait_or_abort(&ms->p_full[g & 1], (g >> 1) & 1, ms, p)))) break;
+        tc_fence_after();
+        const int s = g % kStages;
+        const uint32_t soff = (uint32_t)(s * C::kStageStride) >> 4;
+        const uint32_t poff = C::kPInStage ? soff : 0u;
+        const uint32_t o = by.same(tmem), av = by.place(a0, soff), bp = by.place(b0, poff);
+        // chunk by chunk, each freed for the next tile's load once its own MMAs complete
+        // (back-to-back MMAs into one accumulator cost no more than alternating ones)
+        // chunk by chunk (back-to-back MMAs into one accumulator cost no more than
+        // alternating ones); each half of the stage is handed back once its MMAs complete.
+        // The second half's release also stands for the whole tile's values being done
+        // (P, which lives in the tail at 48 rows, and O for the softmax's rescale).
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 4; ++c) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint64_t a = by.at(a0, av, (c * kChunkBytes + ks * 4096) >> 4);
-              if (C::oterms(c) == 3) {  // stacked: one MMA over all three terms' rows
-                by.mma(o + C::ocol(c), a, by.at(b0, bp, (ks * 512) >> 4), idesc_stacked, t > 0 || ks > 0);
-              } else {  // summed: one MMA per term into the same accumulator
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t a = by.at(a0, av, (c * kChunkBytes + ks * 4096) >> 4);
+            if (C::oterms(c) == 3) {  // stacked: one MMA over all three terms' rows
+              by.mma(o + C::ocol(c), a, by.at(b0, bp, (ks * 512) >> 4), idesc_stacked, t > 0 || ks > 0);
+            } else {  // summed: one MMA per term into the same accumulator
 #pragma unroll
-                for (int term = 0; term < 3; ++term)
-                  by.mma(o + C::ocol(c), a, by.at(b0, bp, (C::pterm(term) + ks * 512) >> 4), idesc_term,
-                         t > 0 || ks > 0 || term > 0);
-              }
+              for (int term = 0; term < 3; ++term)
+                by.mma(o + C::ocol(c), a, by.at(b0, bp, (C::pterm(term) + ks * 512) >> 4), idesc_term,
+                       t > 0 || ks > 0 || term > 0);
             }
-            if (part_ends(c, PT)) by.commit(&ms->kv_free[s][part_of_chunk(c, PT)]);
           }
+          if (part_ends(c)) by.commit(&ms->kv_free[s][part_of_chunk(c)]);
         }
       }
     }
@@ -1180,7 +1132,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // Two or three warpgroups, each owning an equal share of the query rows; thread i of a
     // warpgroup owns key i of the tile (its TMEM lane).
     constexpr int RH = C::kRH;
-    constexpr float kHeadroom = kPScale + (WI ? kTreeGap : kRescaleGap);
+    constexpr float kHeadroom = kPScale + (PF == 3 || SC ? kTreeGap : kRescaleGap);
     const int wg = (warp - kSoftmaxWarp0) >> 2;
     const int rb = wg * RH;  // rows [rb, rb + RH)
     const int wq = warp & 3;  // TMEM lane quadrant
@@ -1188,7 +1140,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const uint32_t lane_addr = (uint32_t)(wq * 32) << 16;
     const float kv_scale = p.kv_scale;
     uint32_t tile = 0, wg_phase = 0, k = 0;  // k: units with work, in order
-    uint32_t moves = 0;  // tree: times a running maximum of the warpgroup has moved
+    uint32_t moves = 0;  // times a running maximum of the warpgroup has moved
     // PV completions are confirmed in tile order, each before the PV two tiles later can
     // complete (that one needs this warpgroup's next P), so a phase parity names one tile
     // A wait that gives up does not make its lane leave on its own: `ok` collects the
@@ -1208,7 +1160,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     int pv_seen = -1;
     auto wait_pv_upto = [&](int target) -> bool {
       for (int g = pv_seen + 1; g <= target; ++g) {
-        if (!warp_wait(&ms->kv_free[g % kStages][tail_part(PT)], (g / kStages) & 1)) return false;
+        if (!warp_wait(&ms->kv_free[g % kStages][kTailPart], (g / kStages) & 1)) return false;
         pv_seen = g;
       }
       return true;
@@ -1224,8 +1176,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       ++wg_phase;
       return good;
     };
-    // Tree: whether v holds for any thread of the warpgroup, by one hardware barrier instead of a
-    // vote through shared memory and an mbarrier (measured: 4% of a call). It has no limit of its
+    // Whether v holds for any thread of the warpgroup, by one hardware barrier instead of a vote
+    // through shared memory and an mbarrier (draft trees: 4% of a call). It has no limit of its
     // own, and needs none: the warps of a warpgroup run the same units and tiles, every wait
     // between two of these barriers has a limit, and a warp whose wait gave up carries on to the
     // next barrier, from which all four leave together.
@@ -1274,7 +1226,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         mo[r] = kNoMax;
         l[r] = 0.f;
       }
-      if (WI && lane < RH) ms->tree_max[moves & 1][rb + lane] = kNoMax;
+      if (lane < RH) ms->row_max[moves & 1][rb + lane] = kNoMax;
       warp_arrive(&ms->q_empty[k % C::kQB]);
       for (int t = 0; t < ntiles; ++t, ++tile) {
         const int sb = tile % C::kSBuf;
@@ -1338,35 +1290,21 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           }
         }
         // The running max of a row moves only when some score exceeds it by more than the
-        // 2^8 headroom (kRescaleGap in log2 units); only then is the exact tile max needed.
-        // The warps of the warpgroup first agree whether that happens anywhere, and the
-        // common case skips the exchange of per-row maxima.
+        // headroom (in log2 units); only then is the exact tile max needed. The warps of the
+        // warpgroup first agree whether that happens anywhere, and the common case skips the
+        // exchange of per-row maxima.
         bool over = false;
 #pragma unroll
         for (int r = 0; r < RH; ++r) over |= (x[r] > mo[r] + kHeadroom);
-        bool grow;
-        if constexpr (WI) {
-          grow = wg_any(over || !ok);
-          if (grow && wg_any(!ok)) {  // the warpgroup's once-a-tile vote on its waits
-            ok = false;
-            break;
-          }
-        } else {
-          over = __any_sync(0xffffffffu, over);
-          if (__any_sync(0xffffffffu, !ok)) {  // the warp's once-a-tile vote on its waits
-            ok = false;
-            break;
-          }
-          if (lane == 0) ms->grow[tile & 1][wg * 4 + wq] = over ? 1 : 0;
-          ok &= wg_sync();
-          const int4 gf = *reinterpret_cast<const int4*>(&ms->grow[tile & 1][wg * 4]);
-          grow = (gf.x | gf.y | gf.z | gf.w) != 0;
-        }
         bool need_rescale = false;
-        if (WI && grow) {
-          // as below, but a lane takes a row (less code to fetch, and fewer steps): the maxima in
-          // shared memory, read from the side that the time before wrote, written to the other
-          // (each warp of the warpgroup the same values)
+        if (wg_any(over || !ok)) {
+          if (wg_any(!ok)) {  // the warpgroup's once-a-tile vote on its waits
+            ok = false;
+            break;
+          }
+          // The tile's maximum of each row: a warp's in hardware, then the four warps' through shared
+          // memory, a lane a row. The running maxima are read from the side that the time before wrote
+          // and written to the other (each warp of the warpgroup the same values).
           float* red = &ms->red[tile & 1][0];
           float v = 0.f;
 #pragma unroll
@@ -1380,13 +1318,13 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           if (lane < RH) {
             const float4 t4 = *reinterpret_cast<const float4*>(&red[(rb + lane) * 4]);
             const float tm = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
-            float now = ms->tree_max[moves & 1][rb + lane], al = 1.f;
-            if (tm > now + kHeadroom) {
-              al = ex2(now + kPScale - tm);
+            float now = ms->row_max[moves & 1][rb + lane], al = 1.f;
+            if (tm > now + kHeadroom) {  // lazy: the headroom absorbs small increases
+              al = ex2(now + kPScale - tm);  // 0 before the first key (nothing accumulated yet)
               moved = now != kNoMax;
               now = tm - kPScale;
             }
-            ms->tree_max[(moves & 1) ^ 1][rb + lane] = now;
+            ms->row_max[(moves & 1) ^ 1][rb + lane] = now;
             ms->alpha[rb + lane] = al;
           }
           need_rescale = __any_sync(0xffffffffu, moved);
@@ -1394,30 +1332,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           ++moves;
 #pragma unroll
           for (int r = 0; r < RH; ++r) {
-            mo[r] = ms->tree_max[moves & 1][rb + r];
+            mo[r] = ms->row_max[moves & 1][rb + r];
             l[r] *= ms->alpha[rb + r];
-          }
-        } else if (grow) {
-          // tile max per row: warp max in hardware, then the four warps through shared memory
-          float* red = &ms->red[tile & 1][0];
-#pragma unroll
-          for (int r = 0; r < RH; ++r) {
-            const float v = warp_max(x[r]);
-            if (lane == 0) red[(rb + r) * 4 + wq] = v;
-          }
-          ok &= wg_sync();
-#pragma unroll
-          for (int r = 0; r < RH; ++r) {
-            const float4 t4 = *reinterpret_cast<const float4*>(&red[(rb + r) * 4]);
-            const float tm = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
-            float al = 1.f;
-            if (tm > mo[r] + kHeadroom) {  // lazy: the headroom absorbs small increases
-              al = ex2(mo[r] + kPScale - tm);  // 0 before the first key (nothing accumulated yet)
-              need_rescale |= (mo[r] != kNoMax);
-              l[r] *= al;
-              mo[r] = tm - kPScale;
-            }
-            if (lane == 0) ms->alpha[rb + r] = al;
           }
         }
         // p = 2^(x - m + 11) <= 2^15 rounded to fp16, then three e5m2 terms, each the
@@ -1455,48 +1371,24 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           ok &= wait_pv_upto(upto);
           tc_fence_after();
         }
-        if (t > 0) {
-          if (WI && need_rescale) {
-            // (tree: one small loop over the pieces of O; its code is fetched cold when a short
-            // call first needs it)
-            __syncwarp();
-            const float* al = &ms->alpha[rb];
+        if (t > 0 && need_rescale) {
+          // (one small loop over the pieces of O; its code is fetched cold when a short call first
+          // needs it)
+          __syncwarp();
+          const float* al = &ms->alpha[rb];
 #pragma unroll 1
-            for (int part = 0; part < C::kOParts; ++part) {
-              const uint32_t a = tmem + lane_addr + C::kOCol + part * RP + rb;
-              float v[RH];
+          for (int part = 0; part < C::kOParts; ++part) {
+            const uint32_t a = tmem + lane_addr + C::kOCol + part * RP + rb;
+            float v[RH];
 #pragma unroll
-              for (int cc = 0; cc < RH; cc += 8) tmem_ld8(a + cc, *reinterpret_cast<float(*)[8]>(&v[cc]));
-              tmem_wait_ld();
+            for (int cc = 0; cc < RH; cc += 8) tmem_ld8(a + cc, *reinterpret_cast<float(*)[8]>(&v[cc]));
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < RH; ++e) v[e] *= al[e];
+            for (int e = 0; e < RH; ++e) v[e] *= al[e];
 #pragma unroll
-              for (int cc = 0; cc < RH; cc += 8) tmem_st8(a + cc, *reinterpret_cast<float(*)[8]>(&v[cc]));
-            }
-            tmem_wait_st();
-          } else if (need_rescale) {
-            __syncwarp();
-            const float* al = &ms->alpha[rb];
-            // (rare: rolled up at 16 rows, so that the code of the tile loop stays small; at
-            // more rows the rolled loop needs more registers than there are)
-#pragma unroll(C::kUnrollChunks)
-            for (int c = 0; c < 4; ++c) {
-#pragma unroll
-              for (int term = 0; term < C::oterms(c); ++term) {
-#pragma unroll
-                for (int cc = 0; cc < RH; cc += 8) {
-                  const uint32_t a = tmem + lane_addr + C::ocol(c) + term * RP + rb + cc;
-                  float v[8];
-                  tmem_ld8(a, v);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) v[e] *= al[cc + e];
-                  tmem_st8(a, v);
-                }
-              }
-            }
-            tmem_wait_st();
+            for (int cc = 0; cc < RH; cc += 8) tmem_st8(a + cc, *reinterpret_cast<float(*)[8]>(&v[cc]));
           }
+          tmem_wait_st();
         }
         // keys past this unit's range: zero their V bytes so 0 * garbage cannot be NaN
         if (wg == 0 && kabs >= un.key_hi) {
@@ -1552,13 +1444,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         tc_fence_before();
         warp_arrive(&ms->p_full[tile & 1]);
       }
-      if (!WI && !__all_sync(0xffffffffu, ok)) {  // (tree: the vote below)
-        ok = false;
-        break;
-      }
       if (trace && threadIdx.x == 32 * kSoftmaxWarp0) trace[kTrLastP] = globaltimer_ns();
       // ---- epilogue: row sums, then O / l
-      if constexpr (WI) {
+      if constexpr (PF == 3 || SC) {
         // all rows at once: each exchange halves the rows that a lane still adds up
         float s[RH];
 #pragma unroll
@@ -1594,88 +1482,54 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         inv[r] = lt == 0.f ? 0.f : kv_scale / lt;  // (a row that saw a NaN: its sum is NaN, so is it)
       }
       ok &= wait_pv_upto((int)tile - 1);
-      if (WI ? wg_any(!ok) : !__all_sync(0xffffffffu, ok)) {
+      if (wg_any(!ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
       if (trace && threadIdx.x == 32 * kSoftmaxWarp0) trace[kTrLastPV] = globaltimer_ns();
-      if constexpr (PF == 3) {
-        // One small loop (the rows' reciprocals in shared memory, not in registers that only
-        // unrolled code can index): a short call fetches the epilogue's code cold. Row r of the
-        // unit is row r of its group in q, out and lse.
-        __syncwarp();
+      // One small loop (the rows' reciprocals in shared memory, not in registers that only unrolled
+      // code can index): a short call fetches the epilogue's code cold.
+      __syncwarp();
 #pragma unroll
-        for (int r = 0; r < RH; ++r)
-          if (lane == 0) ms->alpha[rb + r] = inv[r];  // (every warp of the warpgroup the same)
-        __syncwarp();
+      for (int r = 0; r < RH; ++r)
+        if (lane == 0) ms->alpha[rb + r] = inv[r];  // (every warp of the warpgroup the same)
+      __syncwarp();
 #pragma unroll 1
-        for (int u = 0; u < 4 * (RH / 8); ++u) {
-          const int c = u / (RH / 8), row = rb + u % (RH / 8) * 8;
-          if (row >= R) continue;
-          const uint32_t a = tmem + lane_addr + C::ocol(c) + row;
-          float o[8];
-          tmem_ld8(a, o);
-          if (C::oterms(c) == 3) {
-            float o1[8], o2[8];
-            tmem_ld8(a + RP, o1);
-            tmem_ld8(a + 2 * RP, o2);
-            tmem_wait_ld();
+      for (int u = 0; u < 4 * (RH / 8); ++u) {
+        const int c = u / (RH / 8), row = rb + u % (RH / 8) * 8;
+        if (row >= R) continue;
+        const uint32_t a = tmem + lane_addr + C::ocol(c) + row;
+        // The rows' output offsets go to registers before any of these stores: as far as the
+        // compiler knows a store may alias the table, so a lookup between two stores would wait for
+        // the first one to drain (about 60 ns a store when every SM writes).
+        int roff[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] += o1[e] + o2[e];
-          } else {
-            tmem_wait_ld();
-          }
-          const int dv = c * 128 + i;
-          const float* scale = &ms->alpha[row];
-          if (final_out) {
-            uint16_t* dst = p.out + ((int64_t)un.qrow0 + row) * kDV + dv;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (row + e < R) dst[e * kDV] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e] * scale[e]));
-          } else {
-            float* dst = p.part_out + ((int64_t)un.slot * p.part_rows + row) * kDV + dv;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (row + e < R) dst[e * kDV] = o[e] * scale[e];
-          }
-        }
-      } else {
-      // (once a unit: rolled up over the dv chunks at 16 rows, fewer instructions to fetch)
-#pragma unroll(C::kUnrollChunks)
-      for (int c = 0; c < 4; ++c) {
-        const int NT = C::oterms(c);
-#pragma unroll
-        for (int cc = 0; cc < RH; cc += 8) {
-          if (rb + cc >= R) break;
-          // The rows' output offsets go to registers before any of these stores: as far as
-          // the compiler knows a store may alias the table, so a lookup between two stores
-          // would wait for the first one to drain (about 60 ns a store when every SM writes).
-          int roffs[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) roffs[e] = ms->row_off[rb + cc + e];
-          float o[3][8];
-#pragma unroll
-          for (int term = 0; term < 3; ++term)
-            if (term < NT) tmem_ld8(tmem + lane_addr + C::ocol(c) + term * RP + rb + cc, o[term]);
+        for (int e = 0; e < 8; ++e) roff[e] = PF == 3 ? row + e : ms->row_off[row + e];
+        float o[8];
+        tmem_ld8(a, o);
+        if (C::oterms(c) == 3) {
+          float o1[8], o2[8];
+          tmem_ld8(a + RP, o1);
+          tmem_ld8(a + 2 * RP, o2);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = cc + e;
-            if (rb + r >= R) break;
-            float acc = o[0][e];
-#pragma unroll
-            for (int term = 1; term < 3; ++term)
-              if (term < NT) acc += o[term][e];
-            const int dv = c * 128 + i;
-            if (final_out) {
-              store_out(p, ((int64_t)un.qrow0 + roffs[e]) * kDV + dv, acc * inv[r]);
-            } else {
-              p.part_out[((int64_t)un.slot * p.part_rows + roffs[e]) * kDV + dv] = acc * inv[r];
-            }
-          }
+          for (int e = 0; e < 8; ++e) o[e] = PF == 3 || SC ? o[e] + (o1[e] + o2[e]) : o[e] + o1[e] + o2[e];
+        } else {
+          tmem_wait_ld();
         }
-      }
+        const int dv = c * 128 + i;
+        const float* scale = &ms->alpha[row];
+        if (final_out) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (row + e < R) store_out(p, ((int64_t)un.qrow0 + roff[e]) * kDV + dv, o[e] * scale[e]);
+        } else {
+          float* dst = p.part_out + (int64_t)un.slot * p.part_rows * kDV + dv;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (row + e < R) dst[(int64_t)roff[e] * kDV] = o[e] * scale[e];
+        }
       }
       tc_fence_before();
       if (i < RH && rb + i < R) {

@@ -119,17 +119,8 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// The same with an L2 cache policy (from createpolicy) attached to the load.
-__device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* map, int x, int y,
-                                                 uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(policy)
-      : "memory");
-}
-
-// tma_load_2d_hint by the lane whose `issue` is set, in code that the whole warp runs.
+// The same with an L2 cache policy (from createpolicy) attached to the load, by the lane whose
+// `issue` is set, in code that the whole warp runs.
 __device__ __forceinline__ void tma_load_2d_hint_by(uint32_t issue, void* dst, const CUtensorMap* map,
                                                     int x, int y, uint64_t* bar, uint64_t policy) {
   asm volatile(
@@ -258,15 +249,6 @@ __host__ __device__ constexpr uint32_t instr_desc(uint32_t a_type, uint32_t b_ty
          ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_f8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // One lane of a converged warp (the same one every time).
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t e;
@@ -274,7 +256,7 @@ __device__ __forceinline__ uint32_t elect_one() {
   return e;
 }
 
-// mma_f8f6f4 by the lane whose `issue` is set, in code that the whole warp runs.
+// tcgen05.mma kind::f8f6f4 by the lane whose `issue` is set, in code that the whole warp runs.
 __device__ __forceinline__ void mma_f8f6f4_by(uint32_t issue, uint32_t d_tmem, uint64_t a_desc,
                                               uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
