@@ -5,6 +5,7 @@
     python -m mla_latent_kv_attention_gb300.run_workload cache_append --iters 5
     python -m mla_latent_kv_attention_gb300.run_workload top_k_renorm --iters 5
     python -m mla_latent_kv_attention_gb300.run_workload speculative_step --iters 5
+    python -m mla_latent_kv_attention_gb300.run_workload block_scaled_step --iters 5
 
 Prints the device status word after the last call. Intended as the command line that
 ncu wraps: every launch it makes is a library launch on the named inputs.
@@ -23,7 +24,7 @@ from mla_latent_kv_attention_gb300 import workloads as W
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("workload", choices=sorted(W.WORKLOADS) + ["cache_append", "top_k_renorm",
-                                                                 "mha_prefill", "speculative_step"])
+                                                                 "mha_prefill", "speculative_step", "block_scaled_step"])
     ap.add_argument("--iters", type=int, default=5)
     ap.add_argument("--heads", type=int, default=12, help="long_history_decode only")
     ap.add_argument("--T", type=int, default=8192, help="causal_prefill and mha_prefill only")
@@ -35,6 +36,8 @@ def main(argv=None) -> int:
         return _mha_prefill(args.T, args.iters, args.bf16)
     if args.workload == "speculative_step":
         return _speculative_step(args.iters)
+    if args.workload == "block_scaled_step":
+        return _block_scaled_step(args.iters)
     if args.workload == "top_k_renorm":
         return _top_k_renorm(args.iters)
     if args.workload == "long_history_decode":
@@ -138,6 +141,48 @@ def _speculative_step(iters: int) -> int:
     torch.cuda.synchronize()
     status = mla.mla_read_status(ws) or int(word.item())
     print(f"speculative_step: {iters} calls, status {mla.STATUS.get(status, status)}")
+    return 0 if status == 0 else 1
+
+
+def _block_scaled_step(iters: int) -> int:
+    """Steps over a cache with a scale for every 16 positions, positions with three axes: eight
+    sequences on a 32,768-position prefix write four new rows each (norm, rotation, scales), their
+    queries are rotated and verified, the last 512 positions are read back; a 2,048-position chunk of
+    a ninth sequence is written and prefilled."""
+    B, n, T, H, block = 8, 4, 2048, 12, 16
+    inp = W.make_inputs("block_scaled_step", [32768 + n] * B + [32768 + T], H=H, n_q=1, seed=0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    scales = torch.exp2(torch.randint(-8, -5, (inp.pool.shape[0], 64 // block), generator=g, device="cuda").float())
+    kv = mla.KVCache(inp.pool.cuda(), inp.page_table.cuda(), inp.seq_lens.cuda(), 1.0, scales=scales)
+    some = mla.KVCache(kv.pool, kv.page_table[:B], kv.seq_lens[:B], 1.0, scales=scales)
+    last = mla.KVCache(kv.pool, kv.page_table[B:], kv.seq_lens[B:], 1.0, scales=scales)
+    rope, axes = mla.mla_rope_init(factor=40.0, original_positions=4096), mla.mla_rope_axes_init([8, 12, 12])
+    weight = torch.ones(mla.MLA_DV, dtype=torch.bfloat16, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def tokens(rows):
+        return (torch.randn(rows, mla.MLA_D, generator=g, device="cuda").bfloat16(),
+                torch.randn(rows, H, mla.MLA_D, generator=g, device="cuda").bfloat16(),
+                torch.randint(0, 32768, (3, rows), generator=g, device="cuda"))
+
+    x, q, at = tokens(B * n)
+    px, pq, pat = tokens(T)
+    cu, pcu = torch.arange(B + 1, device="cuda") * n, torch.tensor([0, T], device="cuda")
+    back = torch.arange(B + 1, device="cuda") * 512
+    starts = torch.full((B,), 32768 + n - 512, dtype=torch.int32, device="cuda")
+    ws = mla.workspace(mla.MLA_OP_VERIFY, B, H, n)
+    pws = mla.workspace(mla.MLA_OP_PREFILL, 1, H, T)
+    for _ in range(iters):
+        mla.mla_cache_append_scaled(some, x, cu, rope, at, axes, norm_weight=weight, status=word)
+        part = q[..., mla.MLA_DV:]
+        mla.mla_rope(rope, part, at, out=part, axes=axes)
+        mla.mla_verify(some, q.view(B, n, H, mla.MLA_D), inp.sm_scale, ws=ws)
+        mla.mla_cache_gather(some, back, B * 512, starts=starts, status=word)
+        mla.mla_cache_append_scaled(last, px, pcu, rope, pat, axes, norm_weight=weight, status=word)
+        mla.mla_prefill(last, pq, inp.sm_scale, ws=pws)
+    torch.cuda.synchronize()
+    status = mla.mla_read_status(ws) or mla.mla_read_status(pws) or int(word.item())
+    print(f"block_scaled_step: {iters} calls, status {mla.STATUS.get(status, status)}")
     return 0 if status == 0 else 1
 
 
