@@ -491,8 +491,10 @@ __device__ __forceinline__ void stage_rows(const AttnParams& p, int R, const int
   using C = Cfg<RP>;
   const float kv_scale = p.kv_scale;
   constexpr int nw = NW;  // warps staging together
-  // rows of one pass of a warp (at most four; no more than NW warps leave for it)
-  constexpr int K2 = (RP + NW - 1) / NW < 4 ? (RP + NW - 1) / NW : 4;
+  // rows of one pass of a warp: two, so that the code, fetched cold at a call's start, is short and its
+  // second pass finds it (in us, four / two / one a pass: verify 8 x 4 on 32K 55.6 / 54.7 / 54.6, 32 x 2
+  // on 4K-16K 57.4 / 55.7 / 55.8, 300 x 2 on 200 61.4 / 58.6 / 62.3; prefill 2,048 189 / 184 / 195)
+  constexpr int K2 = (RP + NW - 1) / NW < 2 ? (RP + NW - 1) / NW : 2;
   // rows r0, r0 + nw, ... of this warp: all loads first, then the arithmetic
   for (int r0 = w0; r0 < RP; r0 += K2 * nw) {
     uint4 ld[K2][2], tl[K2][2];
@@ -904,24 +906,24 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
   // second unit there before the first key tile lands, the stager warp each later one while
   // the unit before it runs.
   if (PF != 3 && warp >= 2) {
-    Cursor c0 = first_unit<PF>(args, ms);
-    while (has_unit<PF>(args, ms, c0) && tiles_in(unit_info<PF>(args, ms, c0)) == 0) c0 = next_unit<PF>(args, c0);
-    if (has_unit<PF>(args, ms, c0)) {
-      const UnitInfo ui = unit_info<PF>(args, ms, c0);
-      stage_rows<RP, C::kStageWarps>(p, ui.rows, ms->row_off, p.q + (int64_t)ui.qrow0 * kD, qbuf,
-                                     ms->row_scale[0], warp - 2, lane);
-      fence_proxy_async_smem();
-      mbar_arrive(&ms->q0_done);
-      Cursor c1 = next_unit<PF>(args, c0);
-      while (has_unit<PF>(args, ms, c1) && tiles_in(unit_info<PF>(args, ms, c1)) == 0) c1 = next_unit<PF>(args, c1);
-      if (has_unit<PF>(args, ms, c1)) {
-        const UnitInfo u1 = unit_info<PF>(args, ms, c1);
-        uint8_t* img = p.qimg + (int64_t)blockIdx.x * p.qimg_stride;
-        stage_rows<RP, C::kStageWarps>(p, u1.rows, ms->row_off, p.q + (int64_t)u1.qrow0 * kD, img,
-                                       reinterpret_cast<float*>(img + C::kQBytes), warp - 2, lane);
+    uint8_t* img = p.qimg + (int64_t)blockIdx.x * p.qimg_stride;
+    Cursor cu = first_unit<PF>(args, ms);
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      while (has_unit<PF>(args, ms, cu) && tiles_in(unit_info<PF>(args, ms, cu)) == 0) cu = next_unit<PF>(args, cu);
+      if (!has_unit<PF>(args, ms, cu)) break;
+      const UnitInfo ui = unit_info<PF>(args, ms, cu);
+      stage_rows<RP, C::kStageWarps>(p, ui.rows, ms->row_off, p.q + (int64_t)ui.qrow0 * kD, k == 0 ? qbuf : img,
+                                     k == 0 ? ms->row_scale[0] : reinterpret_cast<float*>(img + C::kQBytes),
+                                     warp - 2, lane);
+      if (k == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive(&ms->q0_done);
+      } else {
         fence_proxy_async_global();
         mbar_arrive(&ms->q1_done);
       }
+      cu = next_unit<PF>(args, cu);
     }
   }
 
