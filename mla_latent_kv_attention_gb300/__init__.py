@@ -257,6 +257,16 @@ def _q_check(q: torch.Tensor, ndim: int) -> None:
                          f"with last dimension {MLA_D}")
 
 
+def _cache_of(kv: KVCache, q: torch.Tensor):
+    """kv's C structs for a call on q, which has to lie on kv's device, the current one (the library
+    launches there)."""
+    c, scales = kv.c_struct(), kv.c_scales()
+    if not kv.pool.get_device() == q.get_device() == torch._C._cuda_getDevice():
+        raise ValueError(f"the cache on {kv.pool.device}, q on {q.device}, the current device "
+                         f"cuda:{torch._C._cuda_getDevice()}: they have to be one")
+    return c, scales
+
+
 def mla_decode(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None, ws=None,
                stream=None):
     """q [B, H, 576] bf16 -> (out [B, H, 512] bf16, lse [B, H] fp32)."""
@@ -265,7 +275,7 @@ def mla_decode(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None
             return mla_decode(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 3)
     B, H = q.shape[0], q.shape[1]
-    c, scales = kv.c_struct(), kv.c_scales()
+    c, scales = _cache_of(kv, q)
     ws = workspace(MLA_OP_DECODE, B, H, 1, q.device) if ws is None else ws
     out = torch.empty(B, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(B, H, dtype=torch.float32, device=q.device) if lse is None else lse
@@ -285,7 +295,7 @@ def mla_verify(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None
             return mla_verify(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 4)
     B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
-    c, scales = kv.c_struct(), kv.c_scales()
+    c, scales = _cache_of(kv, q)
     ws = workspace(MLA_OP_VERIFY, B, H, n_q, q.device) if ws is None else ws
     out = torch.empty(B, n_q, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(B, n_q, H, dtype=torch.float32, device=q.device) if lse is None else lse
@@ -324,7 +334,7 @@ def mla_prefill_mha(kv: KVCache, q: torch.Tensor, w_ukv: torch.Tensor, sm_scale:
         if n == 0:
             raise ValueError("no workspace size for these arguments")
         ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
-    c, scales = kv.c_struct(), kv.c_scales()
+    c, scales = _cache_of(kv, q)
     name = "mla_prefill_mha_bf16" if bf16 else "mla_prefill_mha"
     tail = (out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream))
     if scales is None:
@@ -350,7 +360,7 @@ def mla_verify_f32(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=
         raise ValueError("out must be a contiguous float32 tensor [B, n_q, H, 512]")
     lse = torch.empty(B, n_q, H, dtype=torch.float32, device=q.device) if lse is None else lse
     ws = workspace(MLA_OP_VERIFY, B, H, n_q, q.device) if ws is None else ws
-    c, scales = kv.c_struct(), kv.c_scales()
+    c, scales = _cache_of(kv, q)
     if scales is not None:
         _check("mla_verify_scaled", library().mla_verify_scaled(
             c, scales, q.data_ptr(), B, n_q, H, sm_scale, int(visible_shift), out.data_ptr(), 1, _ptr(lse),
@@ -374,7 +384,7 @@ def mla_prefill(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=Non
             return mla_prefill(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 3)
     T, H = q.shape[0], q.shape[1]
-    c, scales = kv.c_struct(), kv.c_scales()
+    c, scales = _cache_of(kv, q)
     ws = workspace(MLA_OP_PREFILL, 1, H, T, q.device) if ws is None else ws
     out = torch.empty(T, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(T, H, dtype=torch.float32, device=q.device) if lse is None else lse

@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const int per = (B + C::kThreads - 1) / C::kThreads;  // sequences per thread, contiguous
     const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
     long long mine = 0;
-#pragma unroll(PF == 3 ? 1 : 4)
+#pragma unroll 1
     for (PlanIndex<PF> i(p, b_lo); i.b < b_hi; i.next(p)) {
       const int L = p.seq_lens[i.seq];
       const int64_t cap = p.pt_stride * (int64_t)p.page_size;
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       x0 = total > 0 ? range_lo(c, total, n) : 0;
       x1 = total > 0 ? range_lo(c + 1, total, n) : 0;
     }
-#pragma unroll(PF == 3 ? 1 : 4)
+#pragma unroll 1
     for (PlanIndex<PF> i(p, b_lo); i.b < b_hi; i.next(p)) {
       const int nb = blocks_of(seq_len_of(p, i.seq));
       const long long first = pre + kUnitCost;  // the sequence's first block

@@ -270,3 +270,16 @@ def test_refusals():
                      lambda: mla.mla_prefill(kv, q[0], SM)):
             with pytest.raises(ValueError):
                 call()
+
+
+def test_another_device():
+    """A cache that says it lies on another device than q and the current one is refused (no such device is
+    needed: nothing is launched)."""
+    from tests.test_kv_cache import OnDevice
+    kv = cache([100], 16, 9)
+    far = mla.KVCache(*(OnDevice(t, 1) for t in (kv.pool, kv.page_table, kv.seq_lens)), 1.0, scales=OnDevice(kv.scales, 1))
+    q = queries(9, 1, 1, 4)
+    for call in (lambda: mla.mla_decode(far, q[0], SM), lambda: mla.mla_verify(far, q, SM),
+                 lambda: mla.mla_verify_f32(far, q, SM), lambda: mla.mla_prefill(far, q[0], SM)):
+        with pytest.raises(ValueError, match="have to be one"):
+            call()
