@@ -594,8 +594,8 @@ void mla_set_profile_events(void* start, void* stop);
  * Profiling hook. With a device buffer of `bytes` (8-byte aligned), the next decode /
  * verify / prefill calls on this host thread make each CTA c of their attention kernel
  * (while c < bytes / 128) write sixteen 64-bit words at buffer + 128 c: the GPU's global
- * timer (ns) at entry, after the wait on the previous kernel, after the split plan and the
- * first tile loads issued, when the first tile's scores were read, when the last tile's
+ * timer (ns) at entry, after the wait on the previous kernel, after the split plan, when
+ * the first tile's scores were read, when the last tile's
  * probabilities were written, when the last values MMA completed, after its last epilogue
  * and at exit; then (tiles << 32 | units) it processed; then, for CTAs with two units or
  * more, the end of the first unit's epilogue and the second unit's first scores; then

@@ -38,23 +38,29 @@
 // rows per unit: 384 or 512 threads) run the softmax and write the epilogue. Every wait is
 // bounded.
 //
+// What bounds it: with 16 rows HBM (32 x 4K-16K keys: 28 us of the 45 that a call takes stream at
+// 6.7 TB/s, the rest is start, epilogue and merge), with 48 the tile's chain. At 48 rows a tile's MMAs
+// take about 2,700 cycles of the tensor pipe and the tile 3,400 to 3,600 (prefill 1.7 us, 8,192 on 32K
+// 6.64 ms, 1.19 PFLOP/s, 0.63 of the measured bf16 rate): values - load - scores of a stage, two of
+// them, sets the pace, so whatever issues on it was made shorter (Issuer), and the code smaller, which
+// the tile loops and a call's start fetch through caches they overflow.
+//
 // Tree verify (PF = 3) is the same kernel over groups of a sequence's nodes, each node seeing the
 // prefix and the nodes its 64-bit mask names: teams of CTAs walk the same keys, a group each; the
 // query images come from a kernel of their own; a key's column of the masks is looked up only
-// in tiles that reach the nodes. At 48 rows a tile's MMAs take about 2,700 cycles of the tensor
-// pipe and the tile 3,600 (1.86 us; 2.2 us in prefill): the chain values - load - scores of a
-// stage, two of them, sets the pace, so whatever issues on it was made shorter (Issuer), and the
-// code smaller, which the tile loops and a call's start fetch through caches they overflow (81 KB;
-// verify's instantiation has 243). 32 x 32 nodes of 12 heads over 4K-16K keys: 270 us, 1.01
+// in tiles that reach the nodes. 32 x 32 nodes of 12 heads over 4K-16K keys: 270 us, 1.01
 // PFLOP/s, 0.53 of the measured bf16 rate.
 //
 // Block scales (SC): key n's codes count times s_n, its block's scale. A softmax thread owns a key, so
 // s_n is one number a thread and tile: with x_n the key's score in log2 units, its weight in the values
 // MMA is 2^(x_n + log2 s_n - m) (the MMA then adds s_n v_n in units of the codes), its share of the row
 // sum that weight over s_n, and m the running maximum of x_n + log2 s_n. That costs the tile loop one
-// multiply-add a score and nothing in memory traffic but the scales; a rounded log2 acts on numerator
-// and sum alike. The three e5m2 terms then keep their precision relative to the largest weight
-// times scale, which is what the output's absolute error is about.
+// multiply-add a score and nothing in memory traffic but the scales, loaded a tile ahead (BlockScales);
+// a rounded log2 acts on numerator and sum alike. The three e5m2 terms then keep their precision
+// relative to the largest weight times scale, which is what the output's absolute error is about.
+// One scale / scales of blocks, in us, the same codes: decode 32 x 4K-16K 45.6 / 46.1, 142,000 28.0 /
+// 28.7, verify 8 x 4 on 32K 54.3 / 55.9, 8 x 16 nodes on 32K 127.6 / 134 (half of it from maxima that
+// move more often where blocks differ), prefill 8,192 on 32K 6,640 / 6,730.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -847,7 +853,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     if (trace && threadIdx.x == 0) trace[kTrPlanPrefetch] = globaltimer_ns();
   }
   // Loads of one key tile into its stage (producer thread): the two 64-key halves' pool rows
-  // from the page table, then the stage's two halves, each once the MMAs of the tile that
+  // from the page table, then the stage's parts, each once the MMAs of the tile that
   // held it have released it.
   const int64_t rows64 = p.num_pages * (int64_t)p.page_size;
   const int total_rows = rows64 > 0x7fffff00 ? 0x7fffff00 : (int)rows64;
@@ -1056,11 +1062,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         const uint32_t soff = (uint32_t)(s * C::kStageStride) >> 4;
         const uint32_t poff = C::kPInStage ? soff : 0u;
         const uint32_t o = by.same(tmem), av = by.place(a0, soff), bp = by.place(b0, poff);
-        // chunk by chunk, each freed for the next tile's load once its own MMAs complete
-        // (back-to-back MMAs into one accumulator cost no more than alternating ones)
         // chunk by chunk (back-to-back MMAs into one accumulator cost no more than
-        // alternating ones); each half of the stage is handed back once its MMAs complete.
-        // The second half's release also stands for the whole tile's values being done
+        // alternating ones); each part of the stage is handed back once its MMAs complete.
+        // The last part's release also stands for the whole tile's values being done
         // (P, which lives in the tail at 48 rows, and O for the softmax's rescale).
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

@@ -167,7 +167,8 @@ constexpr int kGatherRows = 32;
 constexpr int kGatherThreads = 288;
 constexpr int64_t kRowSkip = -1, kRowBad = -2;
 
-// SC: a scale for each block of 2^shift positions, read by the thread that found the row.
+// SC: a scale for each block of 2^shift positions, read by the thread that found the row (one more
+// dependent load, behind other CTAs' rows: 8 x 32,768 rows 69.5 us, 8 x 333 3.7 us in L2).
 template <typename Out, bool SC>
 __global__ void __launch_bounds__(kGatherThreads)
     cache_gather_kernel(const __grid_constant__ mla_kv_t kv, const float* __restrict__ scale, int shift, int B,

@@ -157,12 +157,11 @@ struct AttnParams {
 };
 
 // Per-CTA stamps of the profiling hook (mla_set_trace_buffer), in nanoseconds of the GPU's
-// global timer: entry, end of the wait on the previous kernel, end of the split plan (with
-// the first tile loads issued), the first tile's scores read by the softmax, the last tile's
-// probabilities written, the last values MMA done, end of the last epilogue, exit; the
-// tiles and units the CTA processed; end of the first unit's epilogue and the second unit's
-// first scores (CTAs with two units or more); decode/verify: end of the plan's scan, end of
-// its L2 prefetches.
+// global timer: entry, end of the wait on the previous kernel, end of the split plan, the
+// first tile's scores read by the softmax, the last tile's probabilities written, the last
+// values MMA done, end of the last epilogue, exit; the tiles and units the CTA processed; end
+// of the first unit's epilogue and the second unit's first scores (CTAs with two units or
+// more); decode/verify: end of the plan's scan, end of its L2 prefetches.
 constexpr int kTraceWords = 16;
 enum TraceSlot { kTrEntry = 0, kTrWaited, kTrPlanned, kTrFirstScores, kTrLastP, kTrLastPV,
                  kTrEpilogue, kTrExit, kTrCounts, kTrUnit1End, kTrUnit2Scores, kTrPlanScan,

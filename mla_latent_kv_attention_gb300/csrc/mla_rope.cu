@@ -26,7 +26,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // HEADS: heads a thread turns (loads of all of them in flight together).
 // AXES: positions [axes][n], each pair by its own axis' (its position is loaded where it is used:
-// the quarter's eight pairs read at most four words, the first of each from L2, in flight with x).
+// the quarter's eight pairs read at most four words, in flight with x; 8,192 tokens of 12 heads 6.5 us
+// from HBM, 4.6 us in L2, half layout, 32 tokens 1.95 us: as with one axis, to 0.1 us).
 template <bool INTERLEAVED, int HEADS, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ mla_rope_t rope, const PairAxes axes, const uint16_t* x,
