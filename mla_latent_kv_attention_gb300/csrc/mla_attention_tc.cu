@@ -497,25 +497,27 @@ __device__ __forceinline__ void stage_rows(const AttnParams& p, int R, const int
   using C = Cfg<RP>;
   const float kv_scale = p.kv_scale;
   constexpr int nw = NW;  // warps staging together
-  // rows of one pass of a warp: two, so that the code, fetched cold at a call's start, is short and its
-  // second pass finds it (in us, four / two / one a pass: verify 8 x 4 on 32K 55.6 / 54.7 / 54.6, 32 x 2
-  // on 4K-16K 57.4 / 55.7 / 55.8, 300 x 2 on 200 61.4 / 58.6 / 62.3; prefill 2,048 189 / 184 / 195)
+  // Rows of one pass of a warp: two. Fewer are shorter code, fetched cold at a call's start, more hide a
+  // lone warp's loads better (in us, one / two / three a pass: verify 8 x 4 on 32K 53.1 / 53.8 / 54.1, 300 x
+  // 2 on 200 55.9 / 53.1 / 52.3, decode 512 x 100-300 53.1 / 50.1 / 50.3, prefill 2,048 178 / 155 / 160).
   constexpr int K2 = (RP + NW - 1) / NW < 2 ? (RP + NW - 1) / NW : 2;
-  // rows r0, r0 + nw, ... of this warp: all loads first, then the arithmetic
+  // rows r0, r0 + nw, ... of this warp: all loads first, then the arithmetic. A lane takes latent dims
+  // 16 lane .. + 15 and RoPE dims 2 lane, 2 lane + 1 (a whole group of 16 RoPE dims a lane would have the
+  // warp run the conversion a second time for four lanes).
   for (int r0 = w0; r0 < RP; r0 += K2 * nw) {
-    uint4 ld[K2][2], tl[K2][2];
+    uint4 ld[K2][2];
+    uint32_t tl[K2];
 #pragma unroll
     for (int k2 = 0; k2 < K2; ++k2) {
       const int r = r0 + nw * k2;
-      ld[k2][0] = ld[k2][1] = tl[k2][0] = tl[k2][1] = make_uint4(0, 0, 0, 0);
+      ld[k2][0] = ld[k2][1] = make_uint4(0, 0, 0, 0);
+      tl[k2] = 0;
       if (r < R) {
-        const uint4* s4 = reinterpret_cast<const uint4*>(qseq + (int64_t)row_off[r] * kD);
+        const uint16_t* row = qseq + (int64_t)row_off[r] * kD;
+        const uint4* s4 = reinterpret_cast<const uint4*>(row);
         ld[k2][0] = s4[2 * lane];
         ld[k2][1] = s4[2 * lane + 1];
-        if (lane < 4) {  // dims 512 + 16*lane .. +15 (1024 bytes in: 64 uint4)
-          tl[k2][0] = s4[64 + 2 * lane];
-          tl[k2][1] = s4[64 + 2 * lane + 1];
-        }
+        tl[k2] = reinterpret_cast<const uint32_t*>(row + kDV)[lane];
       }
     }
 #pragma unroll
@@ -523,21 +525,16 @@ __device__ __forceinline__ void stage_rows(const AttnParams& p, int R, const int
       const int r = r0 + nw * k2;
       if (r >= RP) break;
       const bool real = r < R;
-      float v[16], tail[16];
+      float v[18];  // the latent entries, then the two of the RoPE part
       {
-        const uint32_t w[8] = {ld[k2][0].x, ld[k2][0].y, ld[k2][0].z, ld[k2][0].w,
-                               ld[k2][1].x, ld[k2][1].y, ld[k2][1].z, ld[k2][1].w};
-        const uint32_t wt[8] = {tl[k2][0].x, tl[k2][0].y, tl[k2][0].z, tl[k2][0].w,
-                                tl[k2][1].x, tl[k2][1].y, tl[k2][1].z, tl[k2][1].w};
+        const uint32_t w[9] = {ld[k2][0].x, ld[k2][0].y, ld[k2][0].z, ld[k2][0].w, ld[k2][1].x,
+                               ld[k2][1].y, ld[k2][1].z, ld[k2][1].w, tl[k2]};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          v[e] = __uint_as_float((w[e >> 1] >> ((e & 1) * 16)) << 16);
-          tail[e] = __uint_as_float((wt[e >> 1] >> ((e & 1) * 16)) << 16);
-        }
+        for (int e = 0; e < 18; ++e) v[e] = __uint_as_float((w[e >> 1] >> ((e & 1) * 16)) << 16);
       }
       float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fmaxf(fabsf(v[e]), fabsf(tail[e])));
+      for (int e = 0; e < 18; ++e) amax = fmaxf(amax, fabsf(v[e]));
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       // scale 2^ex so that amax * 2^ex lies in (224, 448]; from the exponent field of
       // amax (normal floats: biased exponent E means amax in [2^(E-127), 2^(E-126)))
@@ -555,29 +552,23 @@ __device__ __forceinline__ void stage_rows(const AttnParams& p, int R, const int
         if (INF) scale += amax - amax;  // 0, or NaN
         row_scale[r] = scale;
       }
-      // two terms per value, packed 16 codes per 16-byte group
-      auto emit = [&](const float* x, int w16) {
-        uint32_t t1w[4], t2w[4];
+      // two terms per value, two codes (one pair of values) a word's half
+      uint32_t t1[9], t2[9];
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float a0 = x[e] * up, a1 = x[e + 1] * up;
-          const uint16_t c1 = to_e4m3x2(a0, a1);
-          const float2 b1 = from_e4m3x2(c1);
-          const uint16_t c2 = to_e4m3x2((a0 - b1.x) * kQTerm2, (a1 - b1.y) * kQTerm2);
-          const int wi = e >> 2, sh = (e & 2) * 8;
-          if ((e & 2) == 0) {
-            t1w[wi] = c1;
-            t2w[wi] = c2;
-          } else {
-            t1w[wi] |= (uint32_t)c1 << sh;
-            t2w[wi] |= (uint32_t)c2 << sh;
-          }
-        }
-        *reinterpret_cast<uint4*>(qdst + q_offset<C::NQK>(r, w16)) = make_uint4(t1w[0], t1w[1], t1w[2], t1w[3]);
-        *reinterpret_cast<uint4*>(qdst + q_offset<C::NQK>(RP + r, w16)) = make_uint4(t2w[0], t2w[1], t2w[2], t2w[3]);
+      for (int e = 0; e < 9; ++e) {
+        const float a0 = v[2 * e] * up, a1 = v[2 * e + 1] * up;
+        t1[e] = to_e4m3x2(a0, a1);
+        const float2 b1 = from_e4m3x2((uint16_t)t1[e]);
+        t2[e] = to_e4m3x2((a0 - b1.x) * kQTerm2, (a1 - b1.y) * kQTerm2);
+      }
+      auto words = [](const uint32_t* t) {
+        return make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
       };
-      emit(v, lane);
-      if (lane < 4) emit(tail, 32 + lane);
+      *reinterpret_cast<uint4*>(qdst + q_offset<C::NQK>(r, lane)) = words(t1);
+      *reinterpret_cast<uint4*>(qdst + q_offset<C::NQK>(RP + r, lane)) = words(t2);
+      const int w16 = 32 + (lane >> 3), in16 = (lane & 7) * 2;  // the RoPE pair's group, its place there
+      *reinterpret_cast<uint16_t*>(qdst + q_offset<C::NQK>(r, w16) + in16) = (uint16_t)t1[8];
+      *reinterpret_cast<uint16_t*>(qdst + q_offset<C::NQK>(RP + r, w16) + in16) = (uint16_t)t2[8];
     }
   }
 }
