@@ -136,6 +136,7 @@ mla_status_t run_split(const mla_kv_t* kv, const void* q, int B, int n_q, int H,
   p.qimg = reinterpret_cast<uint8_t*>(base + w.qimg);
   p.qimg_stride = (int64_t)w.qimg_stride;
   p.num_ctas = sms;
+  p.teams_inv = sms > 1 ? ~0ull / (unsigned)sms + 1 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_mark(g_prof_start, s);
   int launched = 0;

@@ -778,20 +778,17 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     }
     long long pre = before + incl - mine;
     long long x0, x1;
-    if constexpr (PF == 3) {
-      // A tree's ranges belong to teams of CTAs (tree_ranges). range_lo's quotients by the
-      // reciprocal: exact, as c * total is below 2^64 / teams (and less code than 64-bit divisions,
-      // which a short call fetches cold; the same goes for the plan's loops not being unrolled).
-      const unsigned c = blockIdx.x / p.team, teams = gridDim.x / p.team;
-      const unsigned n = tree_ranges(total, teams);
+    {
+      // range_lo's quotients by the reciprocal: exact, as c * total is below 2^64 / n (and less code
+      // than 64-bit divisions, which a short call fetches cold; the same goes for the plan's loops not
+      // being unrolled). A tree's ranges belong to teams of CTAs (tree_ranges).
+      const unsigned c = PF == 3 ? blockIdx.x / p.team : blockIdx.x;
+      const unsigned teams = PF == 3 ? gridDim.x / p.team : gridDim.x;
+      const unsigned n = PF == 3 ? tree_ranges(total, teams) : teams;
       const unsigned long long inv = n == teams ? p.teams_inv : p.fewer_inv;
       x0 = (long long)__umul64hi(c * (unsigned long long)total, inv);
       x1 = inv ? (long long)__umul64hi((c + 1) * (unsigned long long)total, inv) : total;
       if (c >= n) x0 = x1 = total;  // a team without a range
-    } else {
-      const long long n = gridDim.x, c = blockIdx.x;
-      x0 = total > 0 ? range_lo(c, total, n) : 0;
-      x1 = total > 0 ? range_lo(c + 1, total, n) : 0;
     }
 #pragma unroll 1
     for (PlanIndex<PF> i(p, b_lo); i.b < b_hi; i.next(p)) {
@@ -835,7 +832,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       }
       // four lines of 32 page-table entries, by the CTA's last four threads (past the
       // query lines: at most 48 rows x 9)
-      const int64_t pg0 = max(0ll, ms->plan_x0 - ms->plan_pre0) * kKeyBlock / p.page_size;
+      const int64_t pg0 = (unsigned)(max(0ll, ms->plan_x0 - ms->plan_pre0) * kKeyBlock) / (unsigned)p.page_size;
       const int tp = (int)threadIdx.x - (C::kThreads - 4);
       const int64_t pg = pg0 + (int64_t)tp * 32;
       if (tp >= 0 && pg < p.pt_stride) prefetch_l2(p.page_table + (int64_t)(PF == 3 ? ms->plan_seq0 : b0) * p.pt_stride + pg);

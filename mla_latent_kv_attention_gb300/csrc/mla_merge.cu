@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeMinBlocks<VEC, WPR>)
   auto cta_of = [&](int64_t c) -> int64_t { return TREE ? c * p.team + at.member : c; };
   auto slot_of = [&](int i) -> int64_t {
     if (i == 0) return 2 * cta_of(c0) + first_odd;
-    return 2 * cta_of((total >= n) ? c0 + i : range_of(first + i, total, n));
+    return 2 * cta_of((total >= n) ? c0 + i : range_of_few((int)first + i, (int)total, (int)n));
   };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_tree_kernel(AttnParams
   if (count == 1) return;  // the attention kernel writes this row itself
   const int64_t first_odd = (range_lo(c0, total, n) < first - kUnitCost) ? 1 : 0;
   auto at_of = [&](int i) -> int64_t {
-    const int64_t c = (i == 0 || total >= n) ? c0 + i : range_of(first + i, total, n);
+    const int64_t c = (i == 0 || total >= n) ? c0 + i : range_of_few((int)first + i, (int)total, (int)n);
     return (2 * (c * p.team + member) + (i == 0 ? first_odd : 0)) * p.part_rows + r;
   };
   asm volatile("griddepcontrol.wait;" ::: "memory");
