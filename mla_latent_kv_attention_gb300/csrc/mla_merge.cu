@@ -54,16 +54,20 @@ __device__ void merge_row_chunk(const float* __restrict__ po, const float* __res
     if (gt == 0 && chunk == 0 && lse_out) *lse_out = -INFINITY;
     return;
   }
-  // load the pieces i0 + k * 8 (k < NB) of this warp: weights' lse values and data;
-  // indices past the end are clamped to the last piece (a valid address) and dropped later
+  // load the pieces i0 + k * WPR (k < NB) of this warp: weights' lse values and data. Lane k looks up
+  // piece k's slot (a lookup may divide), the warp takes it from there; pieces past the end weigh 0 and
+  // are not loaded.
   float v[NB][VEC];
   float w[NB];
   auto load_batch = [&](int i0) {
+    const int slot = (int)slot_of(min(i0 + lane * WPR, count - 1));
     int64_t at[NB];
 #pragma unroll
-    for (int k = 0; k < NB; ++k) at[k] = slot_of(min(i0 + k * WPR, count - 1)) * R + r;
+    for (int k = 0; k < NB; ++k) at[k] = __shfl_sync(0xffffffffu, slot, k) * R + r;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
+      w[k] = -INFINITY;
+      if (i0 + k * WPR >= count) continue;
       w[k] = __ldg(pl + at[k]);
       const float* src = po + at[k] * kDV + chunk * W + lane * VEC;
       if constexpr (VEC % 4 == 0) {
@@ -80,18 +84,13 @@ __device__ void merge_row_chunk(const float* __restrict__ po, const float* __res
         for (int e = 0; e < VEC; ++e) v[k][e] = __ldg(src + e);
       }
     }
-#pragma unroll
-    for (int k = 0; k < NB; ++k)
-      if (i0 + k * WPR >= count) w[k] = -INFINITY;
   };
   // round one: this lane's share of the lse values, and the warp's first batch
   float lv[kLse];
-  {
-    int64_t at[kLse];
 #pragma unroll
-    for (int j = 0; j < kLse; ++j) at[j] = slot_of(min(lane + 32 * j, count - 1)) * R + r;
-#pragma unroll
-    for (int j = 0; j < kLse; ++j) lv[j] = __ldg(pl + at[j]);
+  for (int j = 0; j < kLse; ++j) {
+    lv[j] = -INFINITY;
+    if (32 * j < count) lv[j] = __ldg(pl + slot_of(min(lane + 32 * j, count - 1)) * R + r);
   }
   load_batch(warp);
   // lse = max + ln sum exp(lse_i - max)
