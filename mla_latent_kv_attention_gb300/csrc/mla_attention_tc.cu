@@ -38,7 +38,7 @@
 // rows per unit: 384 or 512 threads) run the softmax and write the epilogue. Every wait is
 // bounded.
 //
-// What bounds it: with 16 rows HBM (32 x 4K-16K keys: 28 us of the 45 that a call takes stream at
+// What bounds it: with 16 rows HBM (32 x 4K-16K keys: 28 us of the 44.7 that a call takes stream at
 // 6.7 TB/s, the rest is start, epilogue and merge), with 48 the tile's chain. At 48 rows a tile's MMAs
 // take about 2,700 cycles of the tensor pipe and the tile 3,400 to 3,600 (prefill 1.7 us, 8,192 on 32K
 // 6.64 ms, 1.19 PFLOP/s, 0.63 of the measured bf16 rate): values - load - scores of a stage, two of
@@ -58,9 +58,9 @@
 // multiply-add a score and nothing in memory traffic but the scales, loaded a tile ahead (BlockScales);
 // a rounded log2 acts on numerator and sum alike. The three e5m2 terms then keep their precision
 // relative to the largest weight times scale, which is what the output's absolute error is about.
-// One scale / scales of blocks, in us, the same codes: decode 32 x 4K-16K 45.6 / 46.1, 142,000 28.0 /
-// 28.7, verify 8 x 4 on 32K 54.3 / 55.9, 8 x 16 nodes on 32K 127.6 / 134 (half of it from maxima that
-// move more often where blocks differ), prefill 8,192 on 32K 6,640 / 6,730.
+// One scale / scales of blocks, in us, the same codes: decode 32 x 4K-16K 44.7 / 45.5, 142,000 27.2 /
+// 27.9, verify 8 x 4 on 32K 52.8 / 53.9, 8 x 16 nodes on 32K 126 / 133 (half of it from maxima that
+// move more often where blocks differ), prefill 8,192 on 32K 6,640 / 6,690.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
