@@ -106,7 +106,7 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;        // 1 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPScale = 11.0f;     // P carried as 2^(x - m + 11): at most 2^15 while x <= m + 4
 constexpr float kRescaleGap = 4.0f;  // the running max (log2 units) moves only past m + 4
-// Tree verify uses what e5m2 still holds above that (2^15.75 < 57,344 < 2^16): moving the max
+// Tree verify and block scales use what e5m2 still holds above that (2^15.75 < 57,344 < 2^16): moving the max
 // rescales O in tensor memory, and half as many tiles of N(0, 1) data do (a rescale costs its
 // warpgroup about 1.5 us).
 constexpr float kTreeGap = 4.75f;
@@ -150,9 +150,6 @@ struct Cfg {
   // 12 KB between the chunks and the tail, term 0 over the first 6 KB of the tail, which
   // the scores no longer need by then. Otherwise one P buffer serves every tile.
   static constexpr bool kPInStage = (RP == 48);
-  // dv-chunk loops of the epilogue and the rescale: rolled up at 16 rows (measured: smaller
-  // code, a faster decode), unrolled at 32 and 48 (rolled, they spill)
-  static constexpr int kUnrollChunks = (RP == 16) ? 1 : 4;
   static constexpr int kPTerm = (RP / 16) * 2048;       // one term: RP/16 groups of 16 rows
   static constexpr int kTail = 4 * kChunkBytes + (kPInStage ? 2 * kPTerm : 0);
   static constexpr int kStageStride = kTail + 2 * 4096;
@@ -1483,13 +1480,15 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       tc_fence_after();
       if (trace && threadIdx.x == 32 * kSoftmaxWarp0) trace[kTrLastPV] = globaltimer_ns();
       // One small loop (the rows' reciprocals in shared memory, not in registers that only unrolled
-      // code can index): a short call fetches the epilogue's code cold.
+      // code can index): a short call fetches the epilogue's code cold. Two passes at once where a thread
+      // has 16 rows (in us, one / two: verify 8 x 4 on 32K 52.9 / 51.9, 1 x 4 on 1K 17.5 / 17.0; with 8 rows
+      // decode 512 x 100-300 50.2 / 50.8, trees 132.8 / 133.7).
       __syncwarp();
 #pragma unroll
       for (int r = 0; r < RH; ++r)
         if (lane == 0) ms->alpha[rb + r] = inv[r];  // (every warp of the warpgroup the same)
       __syncwarp();
-#pragma unroll 1
+#pragma unroll(RP == 48 && PF != 3 ? 2 : 1)
       for (int u = 0; u < 4 * (RH / 8); ++u) {
         const int c = u / (RH / 8), row = rb + u % (RH / 8) * 8;
         if (row >= R) continue;
