@@ -480,7 +480,9 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
  * mask hides, or past its sequence, may have any. Weights times scale below 2^-28 of a row's largest
  * such product are not kept in the output (as weights are in the calls without scales).
  * mla_verify_scaled: out is float32 [B][n_q][H][512] where out_is_f32 != 0, else bfloat16;
- * visible_shift as in mla_verify_f32_shard.
+ * visible_shift as in mla_verify_f32_shard. The float32 output carries the weights in twice as many
+ * terms (relative error below 1e-6, 2^-33 of the largest term); with more than 32 rows (n_q * H) a
+ * sequence it takes two passes over the cache, half of the heads each.
  */
 mla_status_t mla_decode_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int B,
                                int H, float sm_scale, void* out, float* lse, void* workspace,

@@ -114,8 +114,16 @@ constexpr float kQTerm2 = 16.0f;     // the second query term carries the residu
 constexpr float kNoMax = -1e30f;     // running max (less kPScale) of a row that has seen no key
 constexpr int kPrefetchTiles = 1;    // tiles the producer pulls into L2 ahead of its TMA loads
 
-template <int RP>
+// FINE: the probabilities as six e5m2 terms instead of three, in two sets of three side by side, both
+// summed by the same accumulators: 18 bits, for float32 outputs under block scales, whose error falls
+// from 1e-6 .. 1e-4 to 3e-7 .. 8e-7 (what a float32 computation of the formulas gives). In us, bfloat16
+// out and three terms / float32 out and six: decode 32 x 4K-16K 45.5 / 50.0, verify 32 x 2 57.1 / 63.5; more
+// than 32 rows of a sequence, which run as two halves of the heads, each reading the keys: 8 x 4 on 32K
+// 54.2 / 98.0, of 16 heads (halved either way) 93.4 / 104.
+template <int RP, bool FINE = false>
 struct Cfg {
+  static_assert(!FINE || RP <= 32, "six terms do not fit a 48-row unit's stages");
+  static constexpr int kSets = FINE ? 2 : 1;
   // softmax warpgroups: three at 48 rows (16 rows per thread), else two
   static constexpr int kNWG = (RP == 48) ? 3 : 2;
   static constexpr int kThreads = 128 + 128 * kNWG;
@@ -153,7 +161,7 @@ struct Cfg {
   static constexpr int kPTerm = (RP / 16) * 2048;       // one term: RP/16 groups of 16 rows
   static constexpr int kTail = 4 * kChunkBytes + (kPInStage ? 2 * kPTerm : 0);
   static constexpr int kStageStride = kTail + 2 * 4096;
-  static constexpr int kPBytes = kPInStage ? 0 : 3 * kPTerm;
+  static constexpr int kPBytes = kPInStage ? 0 : kSets * 3 * kPTerm;
   // offset of P term t from the P base (the stage's P area, or the shared buffer)
   static constexpr __host__ __device__ int pterm(int t) {
     return kPInStage ? ((t + 2) % 3) * kPTerm : t * kPTerm;
@@ -206,11 +214,11 @@ static_assert(offsetof(Misc, row_scale) % 16 == 0 && offsetof(Misc, red) % 16 ==
               "vector-accessed arrays must be 16-byte aligned");
 static_assert(offsetof(Misc, kv_full) % 8 == 0, "mbarriers must be 8-byte aligned");
 
-template <int RP>
+template <int RP, bool FINE = false>
 constexpr int smem_bytes() {
-  return Cfg<RP>::kOffMisc + (int)sizeof(Misc) + 1024;
+  return Cfg<RP, FINE>::kOffMisc + (int)sizeof(Misc) + 1024;
 }
-static_assert(smem_bytes<16>() <= 232448 && smem_bytes<32>() <= 232448 && smem_bytes<48>() <= 232448,
+static_assert(smem_bytes<16, true>() <= 232448 && smem_bytes<32, true>() <= 232448 && smem_bytes<48>() <= 232448,
               "dynamic shared memory per CTA");
 
 struct DecodeArgs {
@@ -426,6 +434,15 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
 }
 __device__ __forceinline__ float2 from_e4m3x2(uint16_t v) {
   __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// the same for e5m2, from float32 and back
+__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ float2 from_e5m2x2(uint32_t v) {
+  __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E5M2);
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
@@ -661,12 +678,12 @@ struct BlockScales {
   }
 };
 
-template <int RP, int PF, bool TR, bool SC>
+template <int RP, int PF, bool TR, bool SC, bool FINE>
 __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ DecodeArgs args,
                      const __grid_constant__ CUtensorMap map_main,
                      const __grid_constant__ CUtensorMap map_tail) {
-  using C = Cfg<RP>;
+  using C = Cfg<RP, FINE>;
   const AttnParams& p = args.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1056,8 +1073,11 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
             const uint64_t a = by.at(a0, av, (c * kChunkBytes + ks * 4096) >> 4);
-            if (C::oterms(c) == 3) {  // stacked: one MMA over all three terms' rows
-              by.mma(o + C::ocol(c), a, by.at(b0, bp, (ks * 512) >> 4), idesc_stacked, t > 0 || ks > 0);
+            if (C::oterms(c) == 3) {  // stacked: one MMA over all three terms' rows (of a set)
+#pragma unroll
+              for (int set = 0; set < C::kSets; ++set)
+                by.mma(o + C::ocol(c), a, by.at(b0, bp, (set * 3 * C::kPTerm + ks * 512) >> 4), idesc_stacked,
+                       t > 0 || ks > 0 || set > 0);
             } else {  // summed: one MMA per term into the same accumulator
 #pragma unroll
               for (int term = 0; term < 3; ++term)
@@ -1329,7 +1349,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         }
         // p = 2^(x - m + 11) <= 2^15 rounded to fp16, then three e5m2 terms, each the
         // nearest e5m2 value to what the terms before it left (the differences are exact
-        // in fp16); the row sum takes the float32 p
+        // in fp16); the row sum takes the float32 p. FINE: six terms of the float32 p, each within 2^-3 of
+        // what the terms before it left, so p to 2^-18 (and no closer than 2^-17, 2^-33 of the largest).
         uint32_t w1[RH / 4], w2[RH / 4], w3[RH / 4];
 #pragma unroll
         for (int r = 0; r < RH; r += 2) {
@@ -1337,6 +1358,11 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           const float p1 = ex2(x[r + 1] - mo[r + 1]);
           l[r] = SC ? fmaf(p0, ks.inv, l[r]) : l[r] + p0;
           l[r + 1] = SC ? fmaf(p1, ks.inv, l[r + 1]) : l[r + 1] + p1;
+          if constexpr (FINE) {  // (its terms go out one by one, below)
+            x[r] = p0;
+            x[r + 1] = p1;
+            continue;
+          }
           const uint32_t h = f32x2_to_f16x2(p0, p1);
           const uint32_t c1 = f16x2_to_e5m2x2(h);
           const uint32_t r1 = hsub2(h, e5m2x2_to_f16x2(c1));
@@ -1410,7 +1436,25 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         // 8 rows it writes its 8-byte half.
         uint8_t* pb = C::kPInStage ? smem + C::kOffStages + s * C::kStageStride + 4 * kChunkBytes : pbuf;
         const int off = (i >> 3) * 128 + (i & 7) * 16;
-        if constexpr (RH % 16 == 0) {
+        if constexpr (FINE) {
+          const int o = (rb >> 4) * 2048 + off + ((rb & 15) >> 3) * 8;
+#pragma unroll 1
+          for (int term = 0; term < 3 * C::kSets; ++term) {
+            uint32_t w[RH / 4];
+#pragma unroll
+            for (int r = 0; r < RH; r += 2) {
+              const uint32_t c = to_e5m2x2(x[r], x[r + 1]);
+              const float2 b = from_e5m2x2(c);
+              x[r] -= b.x;
+              x[r + 1] -= b.y;
+              w[r >> 2] = (r & 2) == 0 ? c : w[r >> 2] | c << 16;
+            }
+            if constexpr (RH == 16)
+              *reinterpret_cast<uint4*>(pb + C::pterm(term) + o) = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+              *reinterpret_cast<uint2*>(pb + C::pterm(term) + o) = make_uint2(w[0], w[1]);
+          }
+        } else if constexpr (RH % 16 == 0) {
 #pragma unroll
           for (int blk = 0; blk < RH / 16; ++blk) {
             const int o = ((rb >> 4) + blk) * 2048 + off;
@@ -1636,12 +1680,12 @@ bool encode_pool_maps(const AttnParams& p, CUtensorMap* main_map, CUtensorMap* t
   return r1 == CUDA_SUCCESS && r2 == CUDA_SUCCESS;
 }
 
-template <int RP, int PF, bool TR, bool SC>
+template <int RP, int PF, bool TR, bool SC, bool FINE = false>
 cudaError_t launch_rp_tr(const DecodeArgs& a, const CUtensorMap& mm, const CUtensorMap& mt,
                          int grid, cudaStream_t s) {
-  constexpr int smem = smem_bytes<RP>();
-  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<RP, PF, TR, SC>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = smem_bytes<RP, FINE>();
+  auto* kernel = attn_tc_kernel<RP, PF, TR, SC, FINE>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -1653,7 +1697,7 @@ cudaError_t launch_rp_tr(const DecodeArgs& a, const CUtensorMap& mm, const CUten
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tc_kernel<RP, PF, TR, SC>, a, mm, mt);
+  return cudaLaunchKernelEx(&cfg, kernel, a, mm, mt);
 }
 
 template <int RP, int PF>
@@ -1677,7 +1721,10 @@ cudaError_t launch_decode_tc(const AttnParams& p, int num_sms, cudaStream_t s, i
   if (!encode_pool_maps(p, &mm, &mt)) return cudaErrorInvalidValue;
   const int grid = p.num_ctas;  // the split plan cuts the blocks into this many ranges
   (void)num_sms;
-  const int groups = (p.R > 48) ? 2 : 1;
+  // A float32 output under block scales carries its probabilities in six terms (FINE), for which units
+  // of 48 rows have no room.
+  const bool fine = p.scales && p.out_f32;
+  const int groups = (p.R > (fine ? 32 : 48)) ? 2 : 1;
   for (int gi = 0; gi < groups; ++gi) {
     DecodeArgs a;
     a.p = p;
@@ -1692,7 +1739,10 @@ cudaError_t launch_decode_tc(const AttnParams& p, int num_sms, cudaStream_t s, i
     a.split_base = 0;
     a.status_overwrite = (gi == 0);
     cudaError_t e;
-    if (a.rows <= 16)
+    if (fine)
+      e = a.rows <= 16 ? launch_rp_tr<16, 0, false, true, true>(a, mm, mt, grid, s)
+                       : launch_rp_tr<32, 0, false, true, true>(a, mm, mt, grid, s);
+    else if (a.rows <= 16)
       e = launch_rp<16, 0>(a, mm, mt, grid, s);
     else if (a.rows <= 32)
       e = launch_rp<32, 0>(a, mm, mt, grid, s);

@@ -106,6 +106,25 @@ def test_verify(lens, block, page_size, n, H, f32):
         compare(out, lse, reference(kv, q, shift=n - 1), "shifted")
 
 
+@pytest.mark.parametrize("n,H", [(1, 1), (1, 16), (2, 12), (3, 11), (3, 16), (4, 12), (4, 16)])
+def test_float32_output(n, H):
+    """The float32 output keeps the weights to 2^-18 (six e5m2 terms), or 2^-33 of the row's largest weight
+    times scale. A row's error is a mean of the value rows with those errors for weights, so at most 2^-18 of
+    about the row's size however the keys' errors add up; the scores' own float32 rounding (up to 46 in log2
+    units here, 2^-24 each of product and sum: 2^-17.5 of a weight, of random sign) comes on top. 2e-5 is
+    2^-18 and 2^-17.5 with a factor of two; bfloat16's 2^-9 is 100 times that."""
+    lens = [5000, n, 0, 333, 128 + n]
+    kv = cache(lens, 16, n + H, low=-8, high=-6)
+    q = queries(H, len(lens), n, H)
+    out, lse = mla.mla_verify_f32(kv, q, SM)
+    ref, ref_lse = reference(kv, q)
+    got = out.double().cpu().numpy()
+    for b in range(len(lens)):
+        assert np.linalg.norm(got[b] - ref[b]) <= 2e-5 * np.linalg.norm(ref[b])
+    fin = np.isfinite(ref_lse)
+    assert np.abs(lse.cpu().numpy()[fin] - ref_lse[fin]).max() <= 1e-5 * np.abs(ref_lse[fin]).max()
+
+
 @pytest.mark.parametrize("B,n,H,lens,block,page_size", [
     (1, 1, 12, [1000], 16, 64), (3, 8, 12, [2000, 0, 9], 1, 64), (2, 64, 16, [300, 64], 64, 64), (5, 16, 4, [700] * 5, 32, 128),
     (40, 5, 3, [200] * 40, 4, 192), (1, 33, 16, [9000], 8, 64)])
