@@ -257,10 +257,13 @@ def _q_check(q: torch.Tensor, ndim: int) -> None:
                          f"with last dimension {MLA_D}")
 
 
-def _cache_of(kv: KVCache, q: torch.Tensor):
-    """kv's C structs for a call on q, which has to lie on kv's device, the current one (the library
-    launches there)."""
+def _cache_of(kv: KVCache, q: torch.Tensor, B: int = 1):
+    """kv's C structs for a call on q's B sequences, which has to lie on kv's device, the current one
+    (the library launches there)."""
     c, scales = kv.c_struct(), kv.c_scales()
+    if kv.seq_lens.shape[0] < B or kv.page_table.shape[0] < B:
+        raise ValueError(f"kv describes {kv.seq_lens.shape[0]} lengths and {kv.page_table.shape[0]} rows of pages, "
+                         f"q has {B} sequences")
     if not kv.pool.get_device() == q.get_device() == torch._C._cuda_getDevice():
         raise ValueError(f"the cache on {kv.pool.device}, q on {q.device}, the current device "
                          f"cuda:{torch._C._cuda_getDevice()}: they have to be one")
@@ -275,7 +278,7 @@ def mla_decode(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None
             return mla_decode(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 3)
     B, H = q.shape[0], q.shape[1]
-    c, scales = _cache_of(kv, q)
+    c, scales = _cache_of(kv, q, B)
     ws = workspace(MLA_OP_DECODE, B, H, 1, q.device) if ws is None else ws
     out = torch.empty(B, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(B, H, dtype=torch.float32, device=q.device) if lse is None else lse
@@ -295,7 +298,7 @@ def mla_verify(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=None
             return mla_verify(kv, q, sm_scale, out, lse, ws)
     _q_check(q, 4)
     B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
-    c, scales = _cache_of(kv, q)
+    c, scales = _cache_of(kv, q, B)
     ws = workspace(MLA_OP_VERIFY, B, H, n_q, q.device) if ws is None else ws
     out = torch.empty(B, n_q, H, MLA_DV, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(B, n_q, H, dtype=torch.float32, device=q.device) if lse is None else lse
@@ -360,7 +363,7 @@ def mla_verify_f32(kv: KVCache, q: torch.Tensor, sm_scale: float, out=None, lse=
         raise ValueError("out must be a contiguous float32 tensor [B, n_q, H, 512]")
     lse = torch.empty(B, n_q, H, dtype=torch.float32, device=q.device) if lse is None else lse
     ws = workspace(MLA_OP_VERIFY, B, H, n_q, q.device) if ws is None else ws
-    c, scales = _cache_of(kv, q)
+    c, scales = _cache_of(kv, q, B)
     if scales is not None:
         _check("mla_verify_scaled", library().mla_verify_scaled(
             c, scales, q.data_ptr(), B, n_q, H, sm_scale, int(visible_shift), out.data_ptr(), 1, _ptr(lse),

@@ -302,3 +302,13 @@ def test_another_device():
                  lambda: mla.mla_verify_f32(far, q, SM), lambda: mla.mla_prefill(far, q[0], SM)):
         with pytest.raises(ValueError, match="have to be one"):
             call()
+
+
+def test_more_sequences_than_the_cache_has():
+    kv = cache([100, 60], 16, 9)
+    q = queries(9, 3, 1, 4)
+    for call in (lambda: mla.mla_decode(kv, q[:, 0].contiguous(), SM), lambda: mla.mla_verify(kv, q, SM),
+                 lambda: mla.mla_verify_f32(kv, q, SM),
+                 lambda: mla.mla_verify_tree(kv, q, torch.ones(3, 1, dtype=torch.int64, device=DEV), SM)):
+        with pytest.raises(ValueError, match="sequences"):
+            call()
