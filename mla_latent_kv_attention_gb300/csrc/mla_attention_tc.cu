@@ -424,6 +424,9 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Mi
   return false;
 }
 
+// A warp that runs whole leaves together: the outcome of a wait that any of its lanes gave up.
+__device__ __forceinline__ bool warp_waited(bool ok) { return (bool)__all_sync(0xffffffffu, ok); }
+
 __device__ __forceinline__ bool aborted(const Misc* m) {
   return *reinterpret_cast<const volatile int*>(&m->abort) != 0;
 }
@@ -1109,16 +1112,16 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
           fence_proxy_async_global();
         }
       } else if (k == 0) {  // staged into shared memory by warps 2.. in the prologue
-        if (!wait_or_abort(&ms->q0_done, 0, ms, p)) break;
+        if (!warp_waited(wait_or_abort(&ms->q0_done, 0, ms, p))) break;
         if (lane == 0) mbar_arrive(&ms->q_full[0]);
         ++k;
         continue;
       } else if (k == 1) {  // staged into the image by warps 2.. in the prologue
-        if (!wait_or_abort(&ms->q1_done, 0, ms, p)) break;
+        if (!warp_waited(wait_or_abort(&ms->q1_done, 0, ms, p))) break;
       } else {
         // the image is free once the previous unit's copy out of it has landed
         const uint32_t pk = k - 1;
-        if (!wait_or_abort(&ms->q_full[pk % C::kQB], (pk / C::kQB) & 1, ms, p)) break;
+        if (!warp_waited(wait_or_abort(&ms->q_full[pk % C::kQB], (pk / C::kQB) & 1, ms, p))) break;
         stage_rows<RP, 1>(p, ui.rows, ms->row_off, p.q + (int64_t)ui.qrow0 * kD, img,
                           reinterpret_cast<float*>(img + C::kQBytes), 0, lane);
         fence_proxy_async_global();
@@ -1129,7 +1132,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
       // have its scores done before its softmax has begun, and q_full would run two phases ahead of
       // those warps, which a parity cannot tell from none (and unit k or the one after it replaces
       // the scales). One barrier for both: a second one took verify 69.1 us to this one's 68.8.
-      if (k >= (uint32_t)C::kQB && !wait_or_abort(&ms->q_empty[slot], ((k / C::kQB) - 1) & 1, ms, p)) break;
+      if (k >= (uint32_t)C::kQB && !warp_waited(wait_or_abort(&ms->q_empty[slot], ((k / C::kQB) - 1) & 1, ms, p)))
+        break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&ms->q_full[slot], kImgBytes);
         bulk_g2s(qbuf + slot * C::kQBytes, from, C::kQBytes, &ms->q_full[slot]);
