@@ -433,7 +433,8 @@ mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
  *                [axes->n_axes][n] where axes is given
  *   status       device word or NULL: set to MLA_ERR_BOUNDS (if it held 0) for a sequence with more
  *                new rows than positions, longer than its table, or with rows outside x (none of
- *                it is written), and for a page outside the pool (its positions are not written)
+ *                it is written), for a page outside the pool (its positions are not written), and
+ *                where cu_rows is found to decrease (rows around it may be left unwritten)
  * No two sequences may hold new positions in the same block. One launch.
  */
 mla_status_t mla_cache_append_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* x,

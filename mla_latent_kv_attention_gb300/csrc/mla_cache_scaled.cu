@@ -115,8 +115,10 @@ __global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
   // (the unit's place among its sequence's, and its block's first position)
   const int64_t nth = unit - first_unit_of<G>(row0, b);
   const int64_t p0 = L - m;
-  bool write = found && m > 0;
-  if (write && (p0 < 0 || row0 < 0 || row1 > a.n || L > a.kv.page_table_stride * a.kv.page_size)) {
+  // (nth < 0: the search was led astray by a cu_rows that decreases)
+  bool write = found && m != 0;
+  if (write && (m < 0 || nth < 0 || p0 < 0 || row0 < 0 || row1 > a.n ||
+                L > a.kv.page_table_stride * a.kv.page_size)) {
     if (lane == 0 && a.status) atomicCAS(a.status, 0u, (unsigned)MLA_ERR_BOUNDS);
     write = false;
   }

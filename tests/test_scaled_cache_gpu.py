@@ -256,6 +256,25 @@ def test_bounds():
     run(lambda kv: kv.page_table.__setitem__((0, 1), -1), [0, 3, 8, 12], refused=(0,))
 
 
+@pytest.mark.parametrize("block", [1, 2, 16])
+def test_decreasing_rows(block):
+    """cu_rows that decreases (units 0 to 6 of blocks of one are led to the first sequence, whose own begin at 7) is
+    reported, and nothing but the sequences' last positions is written."""
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(20, 576, generator=g).bfloat16().to(DEV)
+    kv = cache([2, 40, 20], block, g)
+    pool = kv.pool.clone()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    mla.mla_cache_append_scaled(kv, x, torch.tensor([7, 9, 0, 20], device=DEV), status=status)
+    assert int(status) == mla.MLA_ERR_BOUNDS
+    changed = ~(kv.pool == pool).all(-1)
+    pages = kv.page_table[:, 0].tolist()
+    allowed = torch.zeros_like(changed)
+    allowed[pages[0], :2] = True
+    allowed[pages[2], :20] = True
+    assert not bool((changed & ~allowed).any())
+
+
 def test_refusals():
     g = torch.Generator().manual_seed(10)
     kv = cache([64], 16, g)

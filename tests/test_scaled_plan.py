@@ -41,8 +41,9 @@ def blocks_of_unit(cu, lens, n, unit, G):
         return None
     nth = unit - first_unit(cu[b], b, G)
     begin = ((L - m) // G + nth) * G
-    if begin >= L:
+    if nth < 0 or begin >= L:
         return None
+    assert begin >= 0
     first, end = max(L - m - begin, 0), min(L - begin, G)
     for place in range(first, end):
         assert cu[b] <= cu[b] + begin + place - (L - m) < cu[b + 1] <= n
@@ -70,3 +71,19 @@ def test_every_block_once(G, seed):
 def test_rows_outside_x_and_lengths_too_short():
     assert blocks_of_unit([0, 4, 8], [10, 10], 6, 4, 1) is None  # sequence 1 reaches past x
     assert blocks_of_unit([0, 4], [3], 4, 0, 16) is None         # more rows than positions
+
+
+@pytest.mark.parametrize("G", BLOCKS)
+def test_decreasing_rows_stay_inside(G):
+    """cu_rows that decreases leads the search to a sequence whose units begin later: such a unit does nothing."""
+    r = random.Random(G)
+    astray = 0
+    for _ in range(300):
+        B, n = r.choice([2, 3, 5, 33, 70]), 60
+        cu, lens = [r.randint(-3, n) for _ in range(B + 1)], [r.randint(0, 100) for _ in range(B)]
+        for unit in range(first_unit(n, B, G)):
+            blocks_of_unit(cu, lens, n, unit, G)  # (its assertions)
+            b = find(cu, B, unit, G)
+            astray += b is not None and first_unit(cu[b], b, G) > unit and cu[b + 1] > cu[b]
+    assert astray or G > 8
+    assert blocks_of_unit([7, 9, 0, 20], [2, 2, 30], 20, 3, 1) is None
