@@ -505,7 +505,7 @@ def mla_rope_axes_init(sections, interleaved: bool = False) -> mla_rope_axes_t:
     pairs in turn while they have any left. Kept by the caller and handed to mla_rope and the cache
     writes with positions int64 [len(sections), n]."""
     axes = mla_rope_axes_t()
-    sections = [int(k) for k in sections]
+    sections = [max(-1, min(int(k), MLA_ROPE)) for k in sections]  # (the C entry's int32 would wrap)
     _check("mla_rope_axes_init", library().mla_rope_axes_init(
         axes, (ctypes.c_int32 * len(sections))(*sections), len(sections), int(interleaved)))
     return axes

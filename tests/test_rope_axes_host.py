@@ -27,7 +27,8 @@ def test_assignments(sections):
     assert list(mla.mla_rope_axes_init(sections, interleaved=True).axis) == in_turn(sections)
 
 
-@pytest.mark.parametrize("sections", [[], [31], [33], [16, 17], [40, -8], [8] * 5, [2 ** 31 - 1, 1], [16, 16, 0, 0, 0]])
+@pytest.mark.parametrize("sections", [[], [31], [33], [16, 17], [40, -8], [8] * 5, [2 ** 31 - 1, 1], [16, 16, 0, 0, 0],
+                                      [2 ** 32 + 16, 16], [16, 16 - 2 ** 32]])
 def test_init_refusals(sections):
     with pytest.raises(mla.MlaError) as e:
         mla.mla_rope_axes_init(sections)
