@@ -217,7 +217,8 @@ mla_status_t mla_prefill(const mla_kv_t* kv, const void* q, int T, int H, float 
  *   out    device, [T][H][128] bfloat16, 16-B aligned
  *   lse    device, [T][H] float32 (natural log), or NULL
  *   workspace  device, 256-B aligned, mla_prefill_mha_workspace_size(L, H, device) bytes:
- *          the dequantised latent, the up-projected keys and values, status words.
+ *          the dequantised latent, the up-projected keys and values, status words (and a
+ *          cache's block scales, 12 bytes a position).
  * Errors as mla_prefill; a page index outside the pool is reported by mla_read_status.
  * Launches: a dequantisation kernel, the up-projection GEMM (tcgen05), the attention kernel
  * (and a merge of key-split units when the last round of units is cut along the keys).
@@ -500,10 +501,14 @@ mla_status_t mla_prefill_scaled(const mla_kv_t* kv, const mla_scales_t* scales, 
                                 size_t workspace_bytes, void* stream);
 
 /*
- * mla_prefill_mha (bf16 = 0) or mla_prefill_mha_bf16 (bf16 != 0) over such a cache. The cached values
- * enter the up-projection as bfloat16: code * scale, exact where the scale is a power of two (as
- * mla_cache_append_scaled writes them), else rounded once more, with an error like the bf16 form's.
- * A position whose scale is none counts as a row of NaN codes does there.
+ * mla_prefill_mha (bf16 = 0) or mla_prefill_mha_bf16 (bf16 != 0) over such a cache.
+ * bf16 = 0: the up-projection sees code / 256, exactly, whatever the scales; they enter with the
+ * softmax, as above, so blocks of any size keep the values' float16 precision side by side. Up-projected
+ * entries of code / 256 past float16's 65,504 are infinite; weights times scale below 2^-25 of a row's
+ * largest are not kept in the output.
+ * bf16 != 0: the cached values enter the up-projection as bfloat16 code * scale, exact where the scale is
+ * a power of two (as mla_cache_append_scaled writes them), else rounded once more. A position whose
+ * scale is none counts there as a row of NaN codes does.
  */
 mla_status_t mla_prefill_mha_scaled(const mla_kv_t* kv, const mla_scales_t* scales, int L, const void* q,
                                     int T, int H, const void* w_ukv, float sm_scale, int bf16, void* out,

@@ -358,6 +358,7 @@ mla_status_t run_mha(const mla_kv_t* kv, int L, const void* q, int T, int H, con
   a.kvup = base + w.kvup;
   a.part_out = base + w.part_out;
   a.part_lse = base + w.part_lse;
+  a.scale_table = reinterpret_cast<float*>(base + w.scales);
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = reinterpret_cast<unsigned*>(base + w.status);

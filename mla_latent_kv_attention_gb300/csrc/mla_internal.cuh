@@ -206,9 +206,12 @@ inline __host__ __device__ int mha_up_width(bool precise) { return precise ? 384
 // up-projected keys and values [L][H][384] 16-bit (room for the precise form's hi, lo and
 // value columns; the bf16 form uses the first 256 columns' worth of each row), and the
 // partials of units split along the key axis: one slot per pair of CTAs, each
-// [2][128][128] float32 outputs and [2][128] float32 LSE.
+// [2][128][128] float32 outputs and [2][128] float32 LSE; under block scales the precise form's
+// table of them, kMhaScales numbers for each key of every tile of kMhaKeys.
+constexpr int kMhaKeys = 96;  // keys of a tile of the precise form
+constexpr int kMhaScales = 3;
 struct MhaWsLayout {
-  size_t status, latent, rope, kvup, part_out, part_lse, total;
+  size_t status, latent, rope, kvup, part_out, part_lse, scales, total;
 };
 inline MhaWsLayout mha_ws_layout(int64_t L, int H, int num_sms) {
   MhaWsLayout w;
@@ -226,6 +229,8 @@ inline MhaWsLayout mha_ws_layout(int64_t L, int H, int num_sms) {
   off = align_up(off + slots * 2 * 128 * 128 * sizeof(float), 256);
   w.part_lse = off;
   off = align_up(off + slots * 2 * 128 * sizeof(float), 256);
+  w.scales = off;
+  off = align_up(off + (size_t)((L + kMhaKeys - 1) / kMhaKeys) * kMhaScales * kMhaKeys * sizeof(float), 256);
   w.total = off;
   return w;
 }
@@ -247,6 +252,7 @@ struct MhaArgs {
   void* kvup;
   void* part_out;     // partials of split units (see MhaWsLayout)
   void* part_lse;
+  float* scale_table;  // the precise form's, under block scales (see mha_dequant_kernel)
   uint16_t* out;      // [T][H][128] bf16
   float* lse;         // [T][H] or null
   unsigned* status;   // [num attention CTAs + 1]

@@ -11,7 +11,7 @@
 //
 // Three steps:
 //   1. mha_dequant_kernel: cached rows -> latent [L][512] bf16 (e4m3 values, exact; the
-//      scale goes into the GEMM) and RoPE rows [L][64] bf16 (scaled).
+//      scale goes into the GEMM) and RoPE rows [L][64] bf16 (scaled); block scales: below.
 //   2. mha_proj_kernel (mla_mha_proj.cu, tcgen05): kvup [L][H][256] = kv_scale * latent @ W_ukv.
 //   3. mha_attn_kernel: flash attention on tcgen05. One persistent CTA per SM walks units
 //      of (128 new positions, one head), longest first. Per 128-key tile: S = Q K^T
@@ -58,9 +58,23 @@ constexpr uint64_t kWaitNs = 1000000000ull;    // every wait gives up after 1 s
 //     values, all without kv_scale (it goes into the softmax scale), so the scores carry
 //     about 16 bits; values (x kv_scale) and probabilities in fp16; 96-key tiles of five
 //     key boxes (hi 0..63, hi 64..127, lo 0..63, lo 64..127, RoPE) so that the rings fit.
+// Block scales. The bf16 form takes them in the dequantisation: its keys and values have float32's
+// range. The precise form's values have fp16's, so there (SC) keys and values are those of
+// code * 2^-8, whatever their scale, and key n counts times s_n = 2^8 * its block's scale as in the
+// attention over the latent itself: with x_n its score (log2 units) the weight in the values MMA is
+// 2^(x_n + log2 s_n - m), m the running maximum of x_n + log2 s_n, and its share of the row sum that
+// weight over s_n. (2^8 brings codes up to 448 near the size that values under one scale have.) A
+// tile's numbers come with its keys, into a ring of four tiles: one is loaded when the scores of the
+// tile two before it have been computed, by when the tile four before has its probabilities. SC is
+// the number of neighbouring keys sure to share a scale, 16 (what a thread takes from tensor memory at
+// once) or 1: numbers read for every key cost shared memory's bandwidth, 120 loads of 16 bytes a thread
+// and tile. 8,192 positions on 32K, 12 heads, in ms: one scale 2.87, SC = 16 3.17, SC = 1 3.74.
+constexpr float kCodeUnit = 0x1p-8f;
+constexpr int kScaleSlots = 4;
+constexpr int kScaleBytes = kMhaScales * kMhaKeys * (int)sizeof(float);  // a tile's
 template <bool PREC>
 struct MhaCfg {
-  static constexpr int kBN = PREC ? 96 : 128;    // keys per tile
+  static constexpr int kBN = PREC ? kMhaKeys : 128;  // keys per tile
   static constexpr int kKBox = kBN * 128;        // one 64-wide 16-bit box of kBN keys
   static constexpr int kKBytes = (PREC ? 5 : 3) * kKBox;
   static constexpr int kVBytes = 2 * kKBox;      // values: dims 0..63, 64..127
@@ -81,6 +95,7 @@ struct Misc {
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_full, q_free;
   uint64_t pair_bar;  // bounded barrier of the two softmax warpgroups (256 arrivals)
+  uint64_t scales_full[kScaleSlots];  // SC: a tile's scales have landed
   uint32_t tmem_base;
   int abort;
   unsigned status;
@@ -89,10 +104,12 @@ struct Misc {
 };
 
 template <bool PREC>
+constexpr int kOffScales = MhaCfg<PREC>::kOffMisc + ((int)sizeof(Misc) + 15) / 16 * 16;
+template <bool PREC, int SC>
 constexpr int mha_smem_bytes() {
-  return MhaCfg<PREC>::kOffMisc + (int)sizeof(Misc) + 1024;  // + alignment slack
+  return kOffScales<PREC> + (SC ? kScaleSlots * kScaleBytes : 0) + 1024;  // + alignment slack
 }
-static_assert(mha_smem_bytes<false>() <= 232448 && mha_smem_bytes<true>() <= 232448, "shared memory");
+static_assert(mha_smem_bytes<false, 0>() <= 232448 && mha_smem_bytes<true, 1>() <= 232448, "shared memory");
 
 // 2^x on the SFU (the PTX instruction; inputs are <= 0 or -inf here)
 __device__ __forceinline__ float ex2(float x) {
@@ -111,6 +128,7 @@ struct MhaParams {
   WsHeader* hdr;
   float* part_out;   // [chunks][2][128][128]: normalised partial outputs of split units
   float* part_lse;   // [chunks][2][128]
+  const float* scale_table;  // SC: [tiles][kMhaScales][kMhaKeys]
 };
 
 __device__ __forceinline__ void report(Misc* m, mla_status_t code) {
@@ -227,7 +245,7 @@ __device__ __forceinline__ Work work_at(const MhaParams& p, const Split& sp, int
   return w;
 }
 
-template <bool PREC>
+template <bool PREC, int SC>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_attn_kernel(const MhaParams p, const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_kv,
@@ -238,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = MhaCfg<PREC>;
   constexpr int kBN = C::kBN;
   Misc* ms = reinterpret_cast<Misc*>(smem + C::kOffMisc);
+  uint8_t* scales = smem + kOffScales<PREC>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = gridDim.x / 2, c = blockIdx.x / 2;  // pairs of neighbouring CTAs
   const int rank = (int)(blockIdx.x & 1);
@@ -256,6 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ms->q_full, 1);
     mbar_init(&ms->q_free, 1);
     mbar_init(&ms->pair_bar, 256);
+    if constexpr (SC > 0)
+      for (int s = 0; s < kScaleSlots; ++s) mbar_init(&ms->scales_full[s], 1);
     ms->abort = 0;
     ms->status = 0;
     fence_mbar_init();
@@ -285,6 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = wk.j0; j < wk.j1; ++j, ++g) {
           const int s = g & 1;
           if (g >= 2 && !(ok = wait_or_abort(&ms->s_full[s], ((g >> 1) & 1) ^ 1, ms))) break;
+          if constexpr (SC > 0) {
+            uint64_t* full = &ms->scales_full[g % kScaleSlots];
+            mbar_arrive_expect_tx(full, kScaleBytes);
+            bulk_g2s(scales + g % kScaleSlots * kScaleBytes, p.scale_table + (int64_t)j * (kScaleBytes / 4), kScaleBytes,
+                     full);
+          }
           uint8_t* kb = smem + C::kOffK + s * C::kKBytes;
           mbar_arrive_expect_tx(&ms->k_full[s], C::kKBytes);
           const int n0 = j * kBN;
@@ -408,6 +435,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this warpgroup's previous values MMA (it wrote O and read P from the buffer about
         // to be overwritten) finished before these scores were computed; confirm its phase
         if (ok && mine > 0) ok = wait_or_abort(&ms->pv_done[wg], (mine - 1) & 1, ms);
+        // SC: each key's factor of the score (its scale times scale_log2), log2 and inverse of its scale
+        // (every lane of the warp loads the same)
+        const float4* factor = reinterpret_cast<const float4*>(scales + g % kScaleSlots * kScaleBytes);
+        const float4 *log2s = factor + kBN / 4, *inverse = factor + kBN / 2;
+        if constexpr (SC > 0) {
+          if (ok) ok = wait_or_abort(&ms->scales_full[g % kScaleSlots], (g / kScaleSlots) & 1, ms);
+        }
+        // a chunk's scores s of keys `key`, ..: SC only, in place
+        auto scaled = [&](float (&s)[16], int key) {
+          if constexpr (SC == 16) {
+            const float f = factor[key / 4].x, o = log2s[key / 4].x;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = fmaf(s[e], f, o);
+          } else if constexpr (SC == 1) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 f = factor[(key + e) / 4], o = log2s[(key + e) / 4];
+              s[e] = fmaf(s[e], f.x, o.x);
+              s[e + 1] = fmaf(s[e + 1], f.y, o.y);
+              s[e + 2] = fmaf(s[e + 2], f.z, o.z);
+              s[e + 3] = fmaf(s[e + 3], f.w, o.w);
+            }
+          }
+        };
         tc_fence_after();
         const int k0 = j * kBN;
         const bool edge = k0 + kBN - 1 > last_key;  // the causal edge crosses this tile
@@ -419,6 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld16(s_col + 32 * q, a);
           tmem_ld16(s_col + 32 * q + 16, b);
           tmem_wait_ld();
+          scaled(a, 32 * q);
+          scaled(b, 32 * q + 16);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const bool va = !edge || k0 + 32 * q + e <= last_key;
@@ -427,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mt = fmaxf(mt, vb ? b[e] : -INFINITY);
           }
         }
-        mt *= p.scale_log2;
+        if constexpr (SC == 0) mt *= p.scale_log2;
         // First tile, or a large jump of some row: rescale this O. Rows jump one by one, but the warp
         // loads and stores tensor memory as one: rows that stay take the factor 1.
         const bool jump = mt > m_run + kRescale;
@@ -457,11 +510,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld16(s_col + 32 * q, a);
           tmem_ld16(s_col + 32 * q + 16, b);
           tmem_wait_ld();
+          scaled(a, 32 * q);
+          scaled(b, 32 * q + 16);
+          const float unit = SC > 0 ? 1.f : p.scale_log2;
           float pk[16];
+          float sa = 0.f, sb = 0.f;  // SC = 16: the two chunks' sums
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float x0 = a[2 * e] * p.scale_log2 - m_run, x1 = a[2 * e + 1] * p.scale_log2 - m_run;
-            float y0 = b[2 * e] * p.scale_log2 - m_run, y1 = b[2 * e + 1] * p.scale_log2 - m_run;
+            float x0 = a[2 * e] * unit - m_run, x1 = a[2 * e + 1] * unit - m_run;
+            float y0 = b[2 * e] * unit - m_run, y1 = b[2 * e + 1] * unit - m_run;
             if (edge) {
               const int kb = k0 + 32 * q + 2 * e;
               if (kb > last_key) x0 = -INFINITY;
@@ -470,7 +527,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (kb + 17 > last_key) y1 = -INFINITY;
             }
             const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(y0), p3 = ex2(y1);
-            sum += (p0 + p1) + (p2 + p3);
+            if constexpr (SC == 16) {
+              sa += p0 + p1;
+              sb += p2 + p3;
+            } else if constexpr (SC == 1) {  // (two of the four loaded: the next pair's load is the same one)
+              const float4 ia = inverse[8 * q + e / 2], ib = inverse[8 * q + 4 + e / 2];
+              sum += (e & 1) == 0 ? fmaf(p0, ia.x, p1 * ia.y) + fmaf(p2, ib.x, p3 * ib.y)
+                                  : fmaf(p0, ia.z, p1 * ia.w) + fmaf(p2, ib.z, p3 * ib.w);
+            } else {
+              sum += (p0 + p1) + (p2 + p3);
+            }
             if constexpr (PREC) {
               const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
               pk[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h0));
@@ -482,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               pk[8 + e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h1));
             }
           }
+          if constexpr (SC == 16) sum += fmaf(sa, inverse[8 * q].x, sb * inverse[8 * q + 4].x);
           tmem_st16(s_col + 16 * q, pk);
         }
         l += sum;
@@ -611,29 +678,46 @@ __global__ void __launch_bounds__(256) mha_chunk_merge_kernel(const MhaParams p,
 // Cached rows -> latent [L][512] bf16 (the e4m3 values; exact) and RoPE rows [L][64] bf16
 // (e4m3 value x rope_scale: kv_scale, one rounding, for the bf16 form; 1, exact, for the
 // precise one). One thread per 8 codes of a row.
-// SC: both times the scale of the row's block (exact for a power of two).
+// SC: both times the scale of the row's block (exact for a power of two), or, where there is a table
+// (the precise form), code * kCodeUnit and the row's numbers in the table, those of its last tile's
+// places past the end as well (keys that no row sees).
 template <bool SC>
-__global__ void mha_dequant_kernel(const float* __restrict__ scales, int scale_shift, const uint8_t* __restrict__ pool, int64_t num_pages,
+__global__ void mha_dequant_kernel(const float* __restrict__ scales, int scale_shift, float* __restrict__ table,
+                                   float scale_log2, const uint8_t* __restrict__ pool, int64_t num_pages,
                                    int page_size, const int32_t* __restrict__ page_table, int L,
                                    float rope_scale, __nv_bfloat16* __restrict__ latent,
                                    __nv_bfloat16* __restrict__ rope, unsigned* status) {
-  const int64_t items = (int64_t)L * (kD / 8);
-  for (int64_t it = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; it < items;
+  constexpr int kPieces = kD / 8;
+  int64_t rows = L;
+  if (SC && table) rows = (rows + kMhaKeys - 1) / kMhaKeys * kMhaKeys;
+  for (int64_t it = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; it < rows * kPieces;
        it += (int64_t)gridDim.x * blockDim.x) {
-    const int n = (int)(it / (kD / 8));
-    const int c8 = (int)(it % (kD / 8));
-    const int32_t page = page_table[n / page_size];
+    const int n = (int)(it / kPieces);
+    const int c8 = (int)(it % kPieces);
     uint2 raw = make_uint2(0u, 0u);
     float scale = 1.f;
-    if (page < 0 || page >= num_pages) {
-      atomicCAS(status, 0u, (unsigned)MLA_ERR_BOUNDS);
-    } else {
-      if constexpr (SC) {
-        scale = scales[((int64_t)page * page_size + n % page_size) >> scale_shift];
-        if (!is_scale(scale)) scale = __int_as_float(0x7FC00000);  // none: NaN for those who see it
+    if (n < L) {
+      const int32_t page = page_table[n / page_size];
+      if (page < 0 || page >= num_pages) {
+        atomicCAS(status, 0u, (unsigned)MLA_ERR_BOUNDS);
+      } else {
+        const int64_t row = (int64_t)page * page_size + n % page_size;
+        if constexpr (SC) scale = scales[row >> scale_shift];
+        raw = *reinterpret_cast<const uint2*>(pool + row * kD + c8 * 8);
       }
-      raw = *reinterpret_cast<const uint2*>(pool + ((int64_t)page * page_size + n % page_size) * kD +
-                                            c8 * 8);
+    }
+    if constexpr (SC) {
+      const bool good = is_scale(scale);
+      if (table) {
+        const float s = good ? scale * (1.f / kCodeUnit) : 1.f;
+        if (c8 < kMhaScales)  // (a scale that is none: NaN scores for the rows that see the key)
+          table[((int64_t)(n / kMhaKeys) * kMhaScales + c8) * kMhaKeys + n % kMhaKeys] =
+              c8 == 0 ? (good ? s * scale_log2 : __int_as_float(0x7FC00000)) : (c8 == 1 ? log2f(s) : 1.f / s);
+        if (n >= L) continue;
+        scale = kCodeUnit;
+      } else if (!good) {
+        scale = __int_as_float(0x7FC00000);  // none: NaN for those who see it
+      }
     }
     float f[8];
     const uint32_t w[2] = {raw.x, raw.y};
@@ -659,8 +743,7 @@ __global__ void mha_dequant_kernel(const float* __restrict__ scales, int scale_s
         const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i] * rope_scale, f[2 * i + 1] * rope_scale);
         o[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      *reinterpret_cast<uint4*>(rope + (int64_t)n * 64 + (c8 - kDV / 8) * 8) =
-          make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(rope + (int64_t)n * 64 + (c8 - kDV / 8) * 8) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -691,7 +774,12 @@ static EncodeFn tensor_map_encoder() {
 
 // The attention launch of one form: tensor maps over q, kvup and the RoPE rows, the
 // attention kernel, and the merge of key-split units when the last round was cut.
-template <bool PREC>
+// A precise call's softmax scale in log2 units (kv_scale, which its keys lack, among it).
+static float scale_log2_of(const MhaArgs& a, bool precise) {
+  return a.sm_scale * (precise ? a.kv_scale : 1.f) * 1.4426950408889634f;
+}
+
+template <bool PREC, int SC>
 static cudaError_t launch_mha_attn(const MhaArgs& a, int grid, cudaStream_t s, int* launches) {
   using C = MhaCfg<PREC>;
   const EncodeFn encode = tensor_map_encoder();
@@ -733,19 +821,21 @@ static cudaError_t launch_mha_attn(const MhaArgs& a, int grid, cudaStream_t s, i
   p.T = a.T;
   p.H = a.H;
   p.bn = C::kBN;
-  p.scale_log2 = a.sm_scale * (PREC ? a.kv_scale : 1.f) * 1.4426950408889634f;
+  p.scale_log2 = scale_log2_of(a, PREC);
   p.out = a.out;
   p.lse = a.lse;
   p.status = a.status;
   p.hdr = a.hdr;
   p.part_out = static_cast<float*>(a.part_out);
   p.part_lse = static_cast<float*>(a.part_lse);
-  constexpr int smem = mha_smem_bytes<PREC>();
-  cudaError_t e = cudaFuncSetAttribute(mha_attn_kernel<PREC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  p.scale_table = a.scale_table;
+  constexpr int smem = mha_smem_bytes<PREC, SC>();
+  auto* kernel = mha_attn_kernel<PREC, SC>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const bool prof = a.prof_start && a.prof_stop;
   if (prof) cudaEventRecord(a.prof_start, s);
-  mha_attn_kernel<PREC><<<grid, kThreads, smem, s>>>(p, mq, mkv, mr);
+  kernel<<<grid, kThreads, smem, s>>>(p, mq, mkv, mr);
   e = cudaGetLastError();
   if (e == cudaSuccess) ++*launches;
   if (prof) cudaEventRecord(a.prof_stop, s);
@@ -768,13 +858,14 @@ cudaError_t launch_mha_prefill(const MhaArgs& a, int num_sms, cudaStream_t s, in
   unsigned* dq_status = a.status + grid;
   cudaError_t e = cudaMemsetAsync(dq_status, 0, sizeof(unsigned), s);
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)a.L * (kD / 8);
+  const bool table = a.scales && a.precise;  // (for the keys past the end, up to a tile's more)
+  const int64_t items = ((int64_t)a.L + (table ? kMhaKeys - 1 : 0)) * (kD / 8);
   const int grid1 = (int)std::min<int64_t>((items + 255) / 256, (int64_t)num_sms * 8);
   auto* dequant = a.scales ? mha_dequant_kernel<true> : mha_dequant_kernel<false>;
-  dequant<<<grid1, 256, 0, s>>>(a.scales, a.scale_shift, a.pool, a.num_pages, a.page_size, a.page_table, a.L,
-                                           a.precise ? 1.f : a.kv_scale,
-                                           reinterpret_cast<__nv_bfloat16*>(a.latent),
-                                           reinterpret_cast<__nv_bfloat16*>(a.rope), dq_status);
+  dequant<<<grid1, 256, 0, s>>>(a.scales, a.scale_shift, table ? a.scale_table : nullptr,
+                                scale_log2_of(a, a.precise), a.pool, a.num_pages, a.page_size, a.page_table, a.L,
+                                a.precise ? 1.f : a.kv_scale, reinterpret_cast<__nv_bfloat16*>(a.latent),
+                                reinterpret_cast<__nv_bfloat16*>(a.rope), dq_status);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ++*launches;
@@ -783,8 +874,11 @@ cudaError_t launch_mha_prefill(const MhaArgs& a, int num_sms, cudaStream_t s, in
   if (e != cudaSuccess) return e;
   ++*launches;
   // 3. attention
-  return a.precise ? launch_mha_attn<true>(a, grid, s, launches)
-                   : launch_mha_attn<false>(a, grid, s, launches);
+  if (table)  // (a tile and its 16-key chunks begin at multiples of 16, and pages at multiples of 64)
+    return a.scale_shift >= 4 ? launch_mha_attn<true, 16>(a, grid, s, launches)
+                              : launch_mha_attn<true, 1>(a, grid, s, launches);
+  return a.precise ? launch_mha_attn<true, 0>(a, grid, s, launches)
+                   : launch_mha_attn<false, 0>(a, grid, s, launches);
 }
 
 }  // namespace mla
