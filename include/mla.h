@@ -416,8 +416,8 @@ mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
  *     s = max(s_old, 2^ceil(log2(max |y| / 448)))   over its new rows' finite entries,
  * s_old being its scale if it holds earlier positions of the sequence (a block that begins with a
  * new position starts afresh), the power of two clamped to 2^-60 .. 2^60 (2^-60 where all is zero).
- * The new codes are e4m3(y / s), rounded to nearest even, infinities and anything past the clamp
- * saturating, NaN kept; where s > s_old the earlier positions' codes become e4m3(code * s_old / s).
+ * The new codes are e4m3(y / s), rounded once to nearest even, infinities and anything past the clamp
+ * saturating, NaN kept; where s > s_old the earlier positions' codes become e4m3(code * s_old / s), so rounded too.
  * With powers of two that shifts their exponents: what was rounded once is not rounded again, but
  * for entries that reach e4m3's subnormals (2^-7 s and below). Earlier positions whose s_old is no scale (see
  * mla_scales_t) become NaN. Codes behind the sequence's last position stay as they were.

@@ -39,10 +39,31 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+// A number about as large as v for a conversion that rounds: v itself, a float's rounding of a product or
+// quotient, where it has no rest, else that cut off, with the last bit set, so that the conversion's rounding to
+// nearest is the only one. rest: what v lacks, its sign at least.
+__device__ __forceinline__ float cut_off(float v, float rest) {
+  const int bits = __float_as_int(v);
+  const int past = (__float_as_int(rest) ^ bits) < 0 ? 1 : 0;  // v is the larger one
+  return rest == 0.f ? v : __int_as_float((bits - past) | 1);
+}
+// a * b (NaN where b is)
+__device__ __forceinline__ float product(float a, float b) {
+  const float v = a * b;
+  return cut_off(v, fmaf(a, b, -v));
+}
+// y / s (infinite or NaN where y is); inv: about 1 / s
+__device__ __forceinline__ float quotient(float y, float s, float inv) {
+  float q = y * inv;
+  const float rest = fmaf(-q, s, y);
+  if (!(fabsf(rest) < INFINITY)) return q;
+  q = fmaf(rest, inv, q);  // the nearest, or the one beside it
+  return cut_off(q, fmaf(-q, s, y));
+}
 // four codes times a factor, rounded again
 __device__ __forceinline__ uint32_t rescaled(uint32_t four, float by) {
   const float2 a = from_e4m3x2(four & 0xFFFFu), b = from_e4m3x2(four >> 16);
-  return e4m3x4(a.x * by, a.y * by, b.x * by, b.y * by);
+  return e4m3x4(product(a.x, by), product(a.y, by), product(b.x, by), product(b.y, by));
 }
 
 // The smallest power of two in [2^-60, 2^60] that brings `top` (finite, not negative) to 448 =
@@ -228,6 +249,7 @@ __global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
   if (first > 0 && was) scale = fmaxf(scale, old);
   if (part == 0 && lane == 0) a.scale[pool_row / G] = scale;
   const float inv = 1.0f / scale;
+  const bool power = (__float_as_int(scale) & 0x7FFFFF) == 0;  // (all but scales kept from elsewhere)
   uint8_t* dst0 = const_cast<uint8_t*>(a.kv.pool) + pool_row * kD;
 #pragma unroll
   for (int k = 0; k < C::kRows; ++k) {
@@ -241,15 +263,23 @@ __global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
         c = make_uint4(rescaled(c.x, by), rescaled(c.y, by), rescaled(c.z, by), rescaled(c.w, by));
         const float2 tail = from_e4m3x2(t);
         reinterpret_cast<uint4*>(dst)[lane] = c;
-        *reinterpret_cast<uint16_t*>(dst + kDV + 2 * lane) = (uint16_t)e4m3x2(tail.x * by, tail.y * by);
+        *reinterpret_cast<uint16_t*>(dst + kDV + 2 * lane) = (uint16_t)e4m3x2(product(tail.x, by), product(tail.y, by));
       }
     } else if (place < end) {
-      uint32_t code[4];
+      uint32_t code[4], pc;
+      if (power) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        code[e] = e4m3x4(y[k][4 * e] * inv, y[k][4 * e + 1] * inv, y[k][4 * e + 2] * inv, y[k][4 * e + 3] * inv);
+        for (int e = 0; e < 4; ++e)
+          code[e] = e4m3x4(y[k][4 * e] * inv, y[k][4 * e + 1] * inv, y[k][4 * e + 2] * inv, y[k][4 * e + 3] * inv);
+        pc = e4m3x2(pe[k].x * inv, pe[k].y * inv);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          code[e] = e4m3x4(quotient(y[k][4 * e], scale, inv), quotient(y[k][4 * e + 1], scale, inv),
+                           quotient(y[k][4 * e + 2], scale, inv), quotient(y[k][4 * e + 3], scale, inv));
+        pc = e4m3x2(quotient(pe[k].x, scale, inv), quotient(pe[k].y, scale, inv));
+      }
       reinterpret_cast<uint4*>(dst)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
-      uint32_t pc = e4m3x2(pe[k].x * inv, pe[k].y * inv);
       if (!rope.interleaved) {
         // dims 2 l, 2 l + 1 of the row: first entries of two pairs (lanes below 16) or second ones
         const uint32_t q0 = __shfl_sync(0xffffffffu, pc, (2 * lane) & 31);
