@@ -436,7 +436,8 @@ mla_status_t mla_cache_gather(const mla_kv_t* kv, int B, const int32_t* starts,
  *                new rows than positions, longer than its table, or with rows outside x (none of
  *                it is written), for a page outside the pool (its positions are not written), and
  *                where cu_rows is found to decrease (rows around it may be left unwritten)
- * No two sequences may hold new positions in the same block. One launch.
+ * No two sequences may hold new positions in the same block. One launch (none where n = 0 and status is
+ * NULL, or B = 0).
  */
 mla_status_t mla_cache_append_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* x,
                                      int64_t x_stride, const int64_t* cu_rows, int B, int64_t n,

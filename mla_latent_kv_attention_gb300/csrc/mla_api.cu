@@ -638,8 +638,9 @@ mla_status_t mla_cache_append_scaled(const mla_kv_t* kv, const mla_scales_t* sca
   if (norm_weight && (!(eps >= 0.f) || !(eps < INFINITY))) return MLA_ERR_INVALID_ARG;
   if ((rope == nullptr) != (positions == nullptr) && n > 0) return MLA_ERR_INVALID_ARG;
   if (x_stride < MLA_D || x_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
-  if (n == 0 || B == 0) return MLA_OK;
-  if (!x || !cu_rows || (axes && !rope)) return MLA_ERR_INVALID_ARG;
+  // (no rows at all: nothing to do but to report sequences that say they have some)
+  if (B == 0 || (n == 0 && !status)) return MLA_OK;
+  if ((!x && n > 0) || !cu_rows || (axes && !rope)) return MLA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(cu_rows, 8) || !aligned(norm_weight, 16) || !aligned(positions, 8) ||
       !aligned(status, 4))
     return MLA_ERR_INVALID_ARG;

@@ -295,7 +295,7 @@ template <int G>
 cudaError_t launch_block(const AppendScaledArgs& a, const mla_rope_t& rope, cudaStream_t s) {
   using C = ScaledCfg<G>;
   const int64_t units = first_unit_of<G>(a.n, a.B);
-  const int64_t grid = (units + C::kUnits - 1) / C::kUnits;
+  const int64_t grid = a.n == 0 ? 1 : (units + C::kUnits - 1) / C::kUnits;  // (no rows: the check of cu_rows alone)
   cache_append_scaled_kernel<G><<<(unsigned)grid, 32 * C::kWarps, 0, s>>>(a, rope);
   return cudaGetLastError();
 }
