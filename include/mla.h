@@ -601,7 +601,8 @@ void mla_set_profile_events(void* start, void* stop);
 
 /*
  * Profiling hook. With a device buffer of `bytes` (8-byte aligned), the next decode /
- * verify / prefill calls on this host thread make each CTA c of their attention kernel
+ * verify / prefill calls on this host thread, under one scale or block scales (not mla_verify_tree and
+ * the MHA form, which leave the buffer as it was), make each CTA c of their attention kernel
  * (while c < bytes / 128) write sixteen 64-bit words at buffer + 128 c: the GPU's global
  * timer (ns) at entry, after the wait on the previous kernel, after the split plan, when
  * the first tile's scores were read, when the last tile's
@@ -609,7 +610,7 @@ void mla_set_profile_events(void* start, void* stop);
  * and at exit; then (tiles << 32 | units) it processed; then, for CTAs with two units or
  * more, the end of the first unit's epilogue and the second unit's first scores; then
  * (decode / verify) the end of the plan's scan and the end of its L2 prefetches (words 13-15
- * are not written). NULL switches
+ * are not written). Where the heads run as two launches the second one's words stay. NULL switches
  * it off. The buffer stays owned by the caller; the results are undefined while two calls
  * overlap on the GPU.
  */

@@ -1704,16 +1704,22 @@ cudaError_t launch_rp_tr(const DecodeArgs& a, const CUtensorMap& mm, const CUten
   return cudaLaunchKernelEx(&cfg, kernel, a, mm, mt);
 }
 
+template <int RP, int PF, bool SC, bool FINE = false>
+cudaError_t launch_rp_sc(const DecodeArgs& a, const CUtensorMap& mm, const CUtensorMap& mt,
+                         int grid, cudaStream_t s) {
+  if constexpr (PF >= 2) {  // (never traced)
+    return launch_rp_tr<RP, PF, false, SC, FINE>(a, mm, mt, grid, s);
+  } else {
+    return a.p.trace ? launch_rp_tr<RP, PF, true, SC, FINE>(a, mm, mt, grid, s)
+                     : launch_rp_tr<RP, PF, false, SC, FINE>(a, mm, mt, grid, s);
+  }
+}
+
 template <int RP, int PF>
 cudaError_t launch_rp(const DecodeArgs& a, const CUtensorMap& mm, const CUtensorMap& mt,
                       int grid, cudaStream_t s) {
-  if (a.p.scales) return launch_rp_tr<RP, PF, false, true>(a, mm, mt, grid, s);
-  if constexpr (PF >= 2) {  // (never traced)
-    return launch_rp_tr<RP, PF, false, false>(a, mm, mt, grid, s);
-  } else {
-    return a.p.trace ? launch_rp_tr<RP, PF, true, false>(a, mm, mt, grid, s)
-                     : launch_rp_tr<RP, PF, false, false>(a, mm, mt, grid, s);
-  }
+  return a.p.scales ? launch_rp_sc<RP, PF, true>(a, mm, mt, grid, s)
+                    : launch_rp_sc<RP, PF, false>(a, mm, mt, grid, s);
 }
 
 }  // namespace
@@ -1744,8 +1750,8 @@ cudaError_t launch_decode_tc(const AttnParams& p, int num_sms, cudaStream_t s, i
     a.status_overwrite = (gi == 0);
     cudaError_t e;
     if (fine)
-      e = a.rows <= 16 ? launch_rp_tr<16, 0, false, true, true>(a, mm, mt, grid, s)
-                       : launch_rp_tr<32, 0, false, true, true>(a, mm, mt, grid, s);
+      e = a.rows <= 16 ? launch_rp_sc<16, 0, true, true>(a, mm, mt, grid, s)
+                       : launch_rp_sc<32, 0, true, true>(a, mm, mt, grid, s);
     else if (a.rows <= 16)
       e = launch_rp<16, 0>(a, mm, mt, grid, s);
     else if (a.rows <= 32)
