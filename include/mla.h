@@ -481,11 +481,13 @@ mla_status_t mla_verify_tree(const mla_kv_t* kv, const void* q, int B, int n, in
  * e4m3(code) * the scale of their block, kv->kv_scale is not read, and all else is as in the calls
  * named. A row that sees a position whose scale is none is NaN, its lse too; a position that a
  * mask hides, or past its sequence, may have any. Weights times scale below 2^-28 of a row's largest
- * such product are not kept in the output (as weights are in the calls without scales).
+ * such product are not kept in the output (as weights are in the calls without scales), below 2^-137 of it
+ * not in lse and the sum either: between scales 2^100 and more apart that can be a weight that counts.
  * mla_verify_scaled: out is float32 [B][n_q][H][512] where out_is_f32 != 0, else bfloat16;
  * visible_shift as in mla_verify_f32_shard. The float32 output carries the weights in twice as many
- * terms (relative error below 1e-6, 2^-33 of the largest term); with more than 32 rows (n_q * H) a
- * sequence it takes two passes over the cache, half of the heads each.
+ * terms, each weight to 2^-18 of itself or 2^-33 of the largest weight times scale. The scores are float32
+ * sums like everywhere: a weight is off by about 2^-21 (|score| + |log2 scale|) besides. With more than 32 rows
+ * (n_q * H) a sequence it takes two passes over the cache, half of the heads each.
  */
 mla_status_t mla_decode_scaled(const mla_kv_t* kv, const mla_scales_t* scales, const void* q, int B,
                                int H, float sm_scale, void* out, float* lse, void* workspace,
