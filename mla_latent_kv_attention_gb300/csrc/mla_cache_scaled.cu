@@ -60,9 +60,11 @@ __device__ __forceinline__ float quotient(float y, float s, float inv) {
   q = fmaf(rest, inv, q);  // the nearest, or the one beside it
   return cut_off(q, fmaf(-q, s, y));
 }
-// four codes times a factor, rounded again
+// four codes times a factor, rounded again; EXACT: the products are (a power of two)
+template <bool EXACT>
 __device__ __forceinline__ uint32_t rescaled(uint32_t four, float by) {
   const float2 a = from_e4m3x2(four & 0xFFFFu), b = from_e4m3x2(four >> 16);
+  if (EXACT) return e4m3x4(a.x * by, a.y * by, b.x * by, b.y * by);
   return e4m3x4(product(a.x, by), product(a.y, by), product(b.x, by), product(b.y, by));
 }
 
@@ -259,11 +261,17 @@ __global__ void __launch_bounds__(32 * ScaledCfg<G>::kWarps)
       if (scale != old) {  // earlier positions move to the block's new scale
         const float by = was ? old / scale : __int_as_float(0x7FC00000);
         uint4 c = reinterpret_cast<const uint4*>(dst)[lane];
-        const uint32_t t = *reinterpret_cast<const uint16_t*>(dst + kDV + 2 * lane);
-        c = make_uint4(rescaled(c.x, by), rescaled(c.y, by), rescaled(c.z, by), rescaled(c.w, by));
-        const float2 tail = from_e4m3x2(t);
+        uint32_t t = *reinterpret_cast<const uint16_t*>(dst + kDV + 2 * lane);
+        if ((__float_as_int(by) & 0x7FFFFF) == 0) {
+          c = make_uint4(rescaled<true>(c.x, by), rescaled<true>(c.y, by), rescaled<true>(c.z, by), rescaled<true>(c.w, by));
+          t = rescaled<true>(t, by);
+        } else {
+          c = make_uint4(rescaled<false>(c.x, by), rescaled<false>(c.y, by), rescaled<false>(c.z, by),
+                         rescaled<false>(c.w, by));
+          t = rescaled<false>(t, by);
+        }
         reinterpret_cast<uint4*>(dst)[lane] = c;
-        *reinterpret_cast<uint16_t*>(dst + kDV + 2 * lane) = (uint16_t)e4m3x2(product(tail.x, by), product(tail.y, by));
+        *reinterpret_cast<uint16_t*>(dst + kDV + 2 * lane) = (uint16_t)t;
       }
     } else if (place < end) {
       uint32_t code[4], pc;
