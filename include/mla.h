@@ -208,6 +208,8 @@ mla_status_t mla_prefill(const mla_kv_t* kv, const void* q, int T, int H, float 
  * are q . key x sm_scale. The tensor cores see the up-projected keys as a bf16 pair (high
  * and low parts: about 16 significant bits), the RoPE part exactly, and the values and the
  * probabilities in fp16, so the results meet the same tolerances as mla_prefill. NaN as there.
+ * (An up-projected value, kv_scale times its sum, past fp16's 65,504 is infinite, one below its 2^-14
+ * loses bits: a cache whose values lie there takes mla_prefill_mha_bf16 or mla_prefill.)
  *   kv     the cache (page size a multiple of 64); kv->seq_lens is not read: L is given
  *          on the host because it sizes the up-projection; sequence 0 of the page table
  *   L      cached positions including the T new ones, 1 <= T <= L <= page-table capacity

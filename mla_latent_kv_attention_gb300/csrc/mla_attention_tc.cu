@@ -902,8 +902,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     }
     return true;
   };
-  // Decode reads each cached row once per call: its lines should not push out of L2 what is
-  // reused (code, query rows, page tables, the partials the merge reads next). Prefill
+  // Decode reads each cached row once per launch: its lines should not push out of L2 what is
+  // reused (code, query rows, page tables, the partials the merge reads next). (A call whose heads
+  // run as two launches reads them twice, and marks them so in the first one too.) Prefill
   // re-reads the same rows for every unit and keeps the default policy, as a tree's verify does
   // for the groups of one sequence.
   const uint64_t read_once = (is_prefill(PF) || (PF == 3 && p.team * p.passes > 1)) ? l2_policy_evict_normal()

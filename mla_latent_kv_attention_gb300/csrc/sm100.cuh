@@ -54,7 +54,6 @@ __device__ __forceinline__ void prefetch_l2(const void* ptr) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr));
 }
 
-// Bulk prefetch of `bytes` contiguous bytes (16-byte aligned, multiple of 16) into L2.
 // Bulk copy of `bytes` (multiple of 16) from global to shared memory, both 16-byte aligned;
 // completion is signalled on `bar` as transaction bytes.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -71,6 +70,7 @@ __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
+// Bulk prefetch of `bytes` contiguous bytes (16-byte aligned, multiple of 16) into L2.
 __device__ __forceinline__ void bulk_prefetch_l2(const void* ptr, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
 }

@@ -29,11 +29,13 @@ def main(argv=None) -> int:
     ap.add_argument("--heads", type=int, default=12, help="long_history_decode only")
     ap.add_argument("--T", type=int, default=8192, help="causal_prefill and mha_prefill only")
     ap.add_argument("--bf16", action="store_true", help="mha_prefill only: the all-bf16 form")
+    ap.add_argument("--block", type=int, default=0, choices=[0, 1, 2, 4, 8, 16, 32, 64],
+                    help="mha_prefill only: a scale for every so many positions (0: one scale)")
     args = ap.parse_args(argv)
     if args.workload == "cache_append":
         return _cache_append(args.iters)
     if args.workload == "mha_prefill":
-        return _mha_prefill(args.T, args.iters, args.bf16)
+        return _mha_prefill(args.T, args.iters, args.bf16, args.block)
     if args.workload == "speculative_step":
         return _speculative_step(args.iters)
     if args.workload == "block_scaled_step":
@@ -82,11 +84,16 @@ def _cache_append(iters: int) -> int:
     return 0 if st == 0 else 1
 
 
-def _mha_prefill(T: int, iters: int, bf16: bool = False) -> int:
+def _mha_prefill(T: int, iters: int, bf16: bool = False, block: int = 0) -> int:
     """The causal prefill chunk (T new positions on a 32,768 prefix, 12 heads) in the MHA form
-    (the default form, or the all-bf16 one)."""
+    (the default form, or the all-bf16 one), under one scale or one for every `block` positions."""
     m = W.mha_prefill(T=T)
     kv = mla.KVCache.from_inputs(m.cache, "cuda")
+    if block:
+        pages, size, _ = kv.pool.shape
+        g = torch.Generator(device="cuda").manual_seed(1)
+        kv.scales = torch.exp2(torch.randint(-8, -5, (pages, size // block), generator=g, device="cuda").float())
+        kv.kv_scale = 1.0
     q = m.q.cuda()
     w = m.w_ukv.cuda()
     L = int(m.cache.seq_lens[0])
